@@ -1,4 +1,5 @@
-"""ctypes binding of libgdn_cpr.so (the C ABI declared in include/gdn_cpr.h).
+"""ctypes binding of libgdn_cpr.so (the C ABI declared in include/gdn_cpr.h) and of
+libgdn_policy.so (the policy-head operators, include/gdn_policy.h).
 
 Argument marshalling only: the functions check torch tensor dtypes, devices and
 contiguity, allocate outputs that the caller did not pass, and call the C entry point of
@@ -14,6 +15,7 @@ from functools import lru_cache
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn_cpr.so")
+POLICY_LIB_PATH = os.path.join(PKG, "libgdn_policy.so")
 
 GDN_OK, GDN_E_NULL, GDN_E_SHAPE, GDN_E_UNSUPPORTED, GDN_E_IDENTITY, GDN_E_DEVICE = range(6)
 GDN_DTYPE_F32, GDN_DTYPE_BF16 = 0, 1
@@ -577,3 +579,413 @@ class Cpr2Decoder:
             _ptr(resync_states), _ptr(self.workspace), self.workspace.numel(),
             _stream(stream)))
         return o
+
+
+# ------------------------------------------------------------------- policy-head operators
+
+GDN_NORM_LAYER, GDN_NORM_RMS = 0, 1
+GDN_REDUCE_TOKEN, GDN_REDUCE_SEQUENCE = 0, 1
+I8_K_ALIGN = 128  # GDN_I8_K_ALIGN
+_NORM_KINDS = {"layer": GDN_NORM_LAYER, "rms": GDN_NORM_RMS}
+_REDUCTIONS = {"token": GDN_REDUCE_TOKEN, "sequence": GDN_REDUCE_SEQUENCE}
+
+
+class GdnNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32)]
+
+
+class GdnLogprobShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("logits_stride", ctypes.c_int64), ("logits_dtype", ctypes.c_int32),
+                ("id_bytes", ctypes.c_int32), ("scale", ctypes.c_double)]
+
+
+class GdnPolicyShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int64),
+                ("reduction", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("dual_clip", ctypes.c_double), ("kl_coef", ctypes.c_double),
+                ("entropy_coef", ctypes.c_double)]
+
+
+_policy_lib = None
+
+
+def policy_lib():
+    """The loaded libgdn_policy.so; raises if it has not been built."""
+    global _policy_lib
+    if _policy_lib is None:
+        if not os.path.exists(POLICY_LIB_PATH):
+            raise RuntimeError(f"{POLICY_LIB_PATH} is missing: build it with "
+                               "__graft_entry__.build()")
+        L = ctypes.CDLL(POLICY_LIB_PATH)
+        P, I32, I64, D = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+        SZ, SZP = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        NS, LS, PS = (ctypes.POINTER(c) for c in (GdnNormShape, GdnLogprobShape, GdnPolicyShape))
+        for name, args in {
+            "gdn_policy_abi_version": [],
+            "gdn_layer_norm_fwd": [NS, P, I64, P, P, D, P, P, P, P],
+            "gdn_layer_norm_bwd_workspace": [NS, SZP],
+            "gdn_layer_norm_bwd": [NS, P, I64, P, I64, P, P, P, P, P, P, P, SZ, P],
+            "gdn_quantize_rows": [P, I64, I64, I64, I32, P, P, P],
+            "gdn_linear_i8_fwd": [I64, I64, I64, P, P, P, P, I32, P, P],
+            "gdn_token_logprob_fwd": [LS, P, P, P, P, P, P],
+            "gdn_token_logprob_bwd": [LS, P, P, P, P, P, P, P, P],
+            "gdn_policy_loss_workspace": [PS, SZP],
+            "gdn_policy_loss_fwd": [PS, P, P, P, P, P, P, P, P, P, P, SZ, P],
+            "gdn_policy_loss_bwd": [PS, P, P, P, P, P, P, P, D, P, P, P],
+        }.items():
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = I32, args
+        L.gdn_policy_last_error.restype = ctypes.c_char_p
+        L.gdn_policy_last_error.argtypes = []
+        _policy_lib = L
+    return _policy_lib
+
+
+def _policy_check(status: int):
+    if status != GDN_OK:
+        raise GdnError(status, policy_lib().gdn_policy_last_error().decode())
+
+
+def policy_abi_version() -> int:
+    return policy_lib().gdn_policy_abi_version()
+
+
+def _code(dtype, name="out_dtype"):
+    torch = _torch()
+    if dtype == torch.float32:
+        return GDN_DTYPE_F32
+    if dtype == torch.bfloat16:
+        return GDN_DTYPE_BF16
+    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
+
+
+def _matrix(t, name, dtypes):
+    """A GPU matrix whose rows are contiguous; returns its row stride (0 repeats a row)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {tuple(t.shape)}")
+    stride, inner = t.stride()
+    if inner != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be contiguous inside a row, got strides {t.stride()}")
+    return stride if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, name, dtypes, n):
+    _need(t, name, dtypes, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+
+
+def _given_or_new(t, name, shape, dtype, device):
+    """The caller's output, checked, or a new one."""
+    torch = _torch()
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, (dtype,), len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _on_stream(fn):
+    """Run fn with `stream` as the current stream, so that what it allocates belongs there."""
+    from functools import wraps
+
+    @wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with _torch().cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _norm_kind(kind):
+    if kind not in _NORM_KINDS:
+        raise ValueError(f"kind must be 'layer' or 'rms', got {kind!r}")
+    return _NORM_KINDS[kind]
+
+
+@_on_stream
+def layer_norm_fwd(x, weight, bias=None, *, eps=1e-5, kind="layer", y=None, mean=None,
+                   rstd=None):
+    """gdn_layer_norm_fwd: the norm of each row of x [M, D] (float32 or bfloat16; rows may
+    have a stride), kind "layer" or "rms"; weight and bias [D] float32 or bfloat16 alike,
+    bias None for 0. ``stream`` may name another stream than the current one.
+    Returns (y [M, D] in x's dtype, mean [M] or None for "rms", rstd [M])."""
+    torch = _torch()
+    dts, f32 = (torch.float32, torch.bfloat16), torch.float32
+    k = _norm_kind(kind)
+    stride = _matrix(x, "x", dts)
+    M, D = x.shape
+    _vector(weight, "weight", dts, D)
+    if bias is not None:
+        _vector(bias, "bias", (weight.dtype,), D)
+    dev = x.device
+    y = _given_or_new(y, "y", (M, D), x.dtype, dev)
+    if k == GDN_NORM_LAYER:
+        mean = _given_or_new(mean, "mean", (M,), f32, dev)
+    elif mean is not None:
+        raise ValueError("kind 'rms' has no mean")
+    rstd = _given_or_new(rstd, "rstd", (M,), f32, dev)
+    _same_device(("x", x), ("weight", weight), ("bias", bias), ("y", y), ("mean", mean),
+                 ("rstd", rstd))
+    shape = GdnNormShape(M, D, k, _code(x.dtype), _code(weight.dtype))
+    _policy_check(policy_lib().gdn_layer_norm_fwd(
+        ctypes.byref(shape), _ptr(x), stride, _ptr(weight), _ptr(bias), eps, _ptr(y),
+        _ptr(mean), _ptr(rstd), _stream(None)))
+    return y, mean, rstd
+
+
+def layer_norm_bwd_workspace_bytes(shape: GdnNormShape) -> int:
+    """gdn_layer_norm_bwd_workspace: device bytes the norm's backward needs."""
+    n = ctypes.c_size_t(0)
+    _policy_check(policy_lib().gdn_layer_norm_bwd_workspace(ctypes.byref(shape),
+                                                            ctypes.byref(n)))
+    return n.value
+
+
+@_on_stream
+def layer_norm_bwd(dy, x, weight, mean, rstd, *, kind="layer", bias=None, dx=None,
+                   d_weight=None, d_bias=None, workspace=None):
+    """gdn_layer_norm_bwd: gradients through layer_norm_fwd, given dy [M, D] in x's dtype and
+    the mean (None for "rms") and rstd that it returned. ``bias`` says whether d_bias is
+    wanted (default: for kind "layer"). ``workspace`` is a uint8 GPU tensor of at least
+    layer_norm_bwd_workspace_bytes() bytes (allocated here when omitted).
+    Returns (dx [M, D] in x's dtype, d_weight [D] float32, d_bias [D] float32 or None)."""
+    torch = _torch()
+    dts, f32 = (torch.float32, torch.bfloat16), torch.float32
+    k = _norm_kind(kind)
+    layer = k == GDN_NORM_LAYER
+    x_stride = _matrix(x, "x", dts)
+    dy_stride = _matrix(dy, "dy", (x.dtype,))
+    if dy.shape != x.shape:
+        raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} differ")
+    M, D = x.shape
+    _vector(weight, "weight", dts, D)
+    if layer:
+        _vector(mean, "mean", (f32,), M)
+    elif mean is not None:
+        raise ValueError("kind 'rms' has no mean")
+    _vector(rstd, "rstd", (f32,), M)
+    dev = x.device
+    dx = _given_or_new(dx, "dx", (M, D), x.dtype, dev)
+    d_weight = _given_or_new(d_weight, "d_weight", (D,), f32, dev)
+    if bias is None:
+        bias = layer or d_bias is not None
+    if bias:
+        d_bias = _given_or_new(d_bias, "d_bias", (D,), f32, dev)
+    elif d_bias is not None:
+        raise ValueError("d_bias is given but bias is False")
+    shape = GdnNormShape(M, D, k, _code(x.dtype), _code(weight.dtype))
+    if workspace is None:
+        workspace = torch.empty(layer_norm_bwd_workspace_bytes(shape), dtype=torch.uint8,
+                                device=dev)
+    _need(workspace, "workspace", (torch.uint8,), 1)
+    _same_device(("x", x), ("dy", dy), ("weight", weight), ("mean", mean), ("rstd", rstd),
+                 ("dx", dx), ("d_weight", d_weight), ("d_bias", d_bias),
+                 ("workspace", workspace))
+    _policy_check(policy_lib().gdn_layer_norm_bwd(
+        ctypes.byref(shape), _ptr(dy), dy_stride, _ptr(x), x_stride, _ptr(weight), _ptr(mean),
+        _ptr(rstd), _ptr(dx), _ptr(d_weight), _ptr(d_bias), _ptr(workspace),
+        workspace.numel(), _stream(None)))
+    return dx, d_weight, d_bias
+
+
+@_on_stream
+def quantize_rows(x, *, xq=None, scale=None):
+    """gdn_quantize_rows: each row of x [M, K] (float32 or bfloat16; rows may have a stride)
+    to int8 with one scale, ties to even. Serves a linear layer's inputs and its weights
+    [N, K]. Returns (xq int8 [M, K rounded up to I8_K_ALIGN, zeros in the padding],
+    scale float32 [M])."""
+    torch = _torch()
+    stride = _matrix(x, "x", (torch.float32, torch.bfloat16))
+    M, K = x.shape
+    xq = _given_or_new(xq, "xq", (M, -(-K // I8_K_ALIGN) * I8_K_ALIGN), torch.int8, x.device)
+    scale = _given_or_new(scale, "scale", (M,), torch.float32, x.device)
+    _same_device(("x", x), ("xq", xq), ("scale", scale))
+    _policy_check(policy_lib().gdn_quantize_rows(_ptr(x), M, K, stride, _code(x.dtype),
+                                                 _ptr(xq), _ptr(scale), _stream(None)))
+    return xq, scale
+
+
+@_on_stream
+def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None):
+    """gdn_linear_i8_fwd: Y = (xq wq^T) x_scale w_scale with exact integer sums. xq int8
+    [M, Kp], wq int8 [N, Kp] as quantize_rows returns them, x_scale [M], w_scale [N] float32.
+    Returns y [M, N] in out_dtype (float32 by default, or bfloat16)."""
+    torch = _torch()
+    i8, f32 = (torch.int8,), (torch.float32,)
+    _need(xq, "xq", i8, 2)
+    _need(wq, "wq", i8, 2)
+    M, K = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K:
+        raise ValueError(f"xq is {tuple(xq.shape)} but wq is {tuple(wq.shape)}")
+    _vector(x_scale, "x_scale", f32, M)
+    _vector(w_scale, "w_scale", f32, N)
+    if out_dtype is None:
+        out_dtype = torch.float32 if y is None else y.dtype
+    code = _code(out_dtype)
+    y = _given_or_new(y, "y", (M, N), out_dtype, xq.device)
+    _same_device(("xq", xq), ("x_scale", x_scale), ("wq", wq), ("w_scale", w_scale), ("y", y))
+    _policy_check(policy_lib().gdn_linear_i8_fwd(M, N, K, _ptr(xq), _ptr(x_scale), _ptr(wq),
+                                                 _ptr(w_scale), code, _ptr(y), _stream(None)))
+    return y
+
+
+def _logprob_args(logits, ids, scale):
+    torch = _torch()
+    stride = _matrix(logits, "logits", (torch.float32, torch.bfloat16))
+    M, V = logits.shape
+    _vector(ids, "ids", (torch.int32, torch.int64), M)
+    return GdnLogprobShape(M, V, stride, _code(logits.dtype),
+                           8 if ids.dtype == torch.int64 else 4, scale)
+
+
+@_on_stream
+def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=None):
+    """gdn_token_logprob_fwd: log-probability of token ids [M] (int32 or int64) under the
+    softmax of scale * logits [M, V] (float32 or bfloat16; rows may have a stride), the
+    log-sum-exp, and with entropy=True the entropy. Rows whose id is outside [0, V) are not
+    scored: zeros. Returns (logp [M], lse [M], entropy [M] or None), float32."""
+    torch = _torch()
+    f32 = torch.float32
+    shape = _logprob_args(logits, ids, scale)
+    M, dev = shape.rows, logits.device
+    logp = _given_or_new(logp, "logp", (M,), f32, dev)
+    lse = _given_or_new(lse, "lse", (M,), f32, dev)
+    ent = torch.empty((M,), dtype=f32, device=dev) if entropy else None
+    _same_device(("logits", logits), ("ids", ids), ("logp", logp), ("lse", lse))
+    _policy_check(policy_lib().gdn_token_logprob_fwd(
+        ctypes.byref(shape), _ptr(logits), _ptr(ids), _ptr(logp), _ptr(lse), _ptr(ent),
+        _stream(None)))
+    return logp, lse, ent
+
+
+@_on_stream
+def token_logprob_bwd(logits, ids, lse, d_logp, *, scale=1.0, entropy=None, d_entropy=None,
+                      d_logits=None):
+    """gdn_token_logprob_bwd: the gradient of token_logprob_fwd's logp, and of its entropy
+    where entropy and d_entropy [M] are given, with respect to the logits. Returns d_logits
+    [M, V] in the logits' dtype; d_logits=logits overwrites them."""
+    torch = _torch()
+    f32 = (torch.float32,)
+    shape = _logprob_args(logits, ids, scale)
+    M, V = logits.shape
+    _vector(lse, "lse", f32, M)
+    _vector(d_logp, "d_logp", f32, M)
+    if d_entropy is not None:
+        if entropy is None:
+            raise ValueError("d_entropy needs the entropy that token_logprob_fwd returned")
+        _vector(entropy, "entropy", f32, M)
+        _vector(d_entropy, "d_entropy", f32, M)
+    else:
+        entropy = None
+    d_logits = _given_or_new(d_logits, "d_logits", (M, V), logits.dtype, logits.device)
+    _same_device(("logits", logits), ("ids", ids), ("lse", lse), ("d_logp", d_logp),
+                 ("entropy", entropy), ("d_entropy", d_entropy), ("d_logits", d_logits))
+    _policy_check(policy_lib().gdn_token_logprob_bwd(
+        ctypes.byref(shape), _ptr(logits), _ptr(ids), _ptr(lse), _ptr(d_logp), _ptr(entropy),
+        _ptr(d_entropy), _ptr(d_logits), _stream(None)))
+    return d_logits
+
+
+def _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens, clip_low,
+                 clip_high, dual_clip, kl_coef, entropy_coef, reduction):
+    torch = _torch()
+    f32 = (torch.float32,)
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be 'token' or 'sequence', got {reduction!r}")
+    _need(logp, "logp", f32, 1)
+    T = logp.shape[0]
+    _vector(old_logp, "old_logp", f32, T)
+    _vector(advantages, "advantages", f32, T)
+    if ref_logp is not None:
+        _vector(ref_logp, "ref_logp", f32, T)
+    if entropy is not None:
+        _vector(entropy, "entropy", f32, T)
+    if mask is not None:
+        _vector(mask, "mask", (torch.bool, torch.uint8), T)
+    N = 1
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", (torch.int32,), 1)
+        N = cu_seqlens.shape[0] - 1
+    _same_device(("logp", logp), ("old_logp", old_logp), ("advantages", advantages),
+                 ("ref_logp", ref_logp), ("entropy", entropy), ("mask", mask),
+                 ("cu_seqlens", cu_seqlens))
+    return GdnPolicyShape(T, N, _REDUCTIONS[reduction], 0, clip_low, clip_high,
+                          0.0 if dual_clip is None else dual_clip,
+                          0.0 if ref_logp is None else kl_coef,
+                          0.0 if entropy is None else entropy_coef)
+
+
+def policy_loss_workspace_bytes(shape: GdnPolicyShape) -> int:
+    """gdn_policy_loss_workspace: device bytes the policy loss needs."""
+    n = ctypes.c_size_t(0)
+    _policy_check(policy_lib().gdn_policy_loss_workspace(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+@_on_stream
+def policy_loss_fwd(logp, old_logp, advantages, *, ref_logp=None, entropy=None, mask=None,
+                    cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=None, kl_coef=0.0,
+                    entropy_coef=0.0, reduction="token", stats=None, weight=None,
+                    workspace=None):
+    """gdn_policy_loss_fwd: the clipped policy loss of a packed batch (logp, old_logp,
+    advantages [T] float32; ref_logp adds the KL term, entropy the entropy term; mask [T]
+    bool, None for all scored; cu_seqlens int32 [N + 1], None for one sequence).
+    Returns (stats [5]: loss and the weighted means of policy loss, KL, entropy and share of
+    tokens cut off; weight [N]: the weight of a scored token of each sequence), float32."""
+    torch = _torch()
+    shape = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
+                         clip_low, clip_high, dual_clip, kl_coef, entropy_coef, reduction)
+    dev = logp.device
+    stats = _given_or_new(stats, "stats", (5,), torch.float32, dev)
+    weight = _given_or_new(weight, "weight", (shape.seqs,), torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(policy_loss_workspace_bytes(shape), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", (torch.uint8,), 1)
+    _same_device(("logp", logp), ("stats", stats), ("weight", weight), ("workspace", workspace))
+    _policy_check(policy_lib().gdn_policy_loss_fwd(
+        ctypes.byref(shape), _ptr(logp), _ptr(old_logp), _ptr(advantages), _ptr(ref_logp),
+        _ptr(entropy), _ptr(mask), _ptr(cu_seqlens), _ptr(stats), _ptr(weight),
+        _ptr(workspace), workspace.numel(), _stream(None)))
+    return stats, weight
+
+
+@_on_stream
+def policy_loss_bwd(logp, old_logp, advantages, weight, *, ref_logp=None, entropy=None,
+                    mask=None, cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=None,
+                    kl_coef=0.0, entropy_coef=0.0, reduction="token", d_loss=1.0, d_logp=None,
+                    d_entropy=None):
+    """gdn_policy_loss_bwd: the gradient of d_loss * loss, given the weight [N] that
+    policy_loss_fwd returned for the same arguments. Returns (d_logp [T], d_entropy [T], or
+    None without an entropy), float32."""
+    torch = _torch()
+    f32 = torch.float32
+    shape = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
+                         clip_low, clip_high, dual_clip, kl_coef, entropy_coef, reduction)
+    _vector(weight, "weight", (f32,), shape.seqs)
+    T, dev = shape.tokens, logp.device
+    d_logp = _given_or_new(d_logp, "d_logp", (T,), f32, dev)
+    if entropy is not None:
+        d_entropy = _given_or_new(d_entropy, "d_entropy", (T,), f32, dev)
+    elif d_entropy is not None:
+        raise ValueError("d_entropy is given without an entropy")
+    _same_device(("logp", logp), ("weight", weight), ("d_logp", d_logp),
+                 ("d_entropy", d_entropy))
+    _policy_check(policy_lib().gdn_policy_loss_bwd(
+        ctypes.byref(shape), _ptr(logp), _ptr(old_logp), _ptr(advantages), _ptr(ref_logp),
+        _ptr(mask), _ptr(cu_seqlens), _ptr(weight), d_loss, _ptr(d_logp), _ptr(d_entropy),
+        _stream(None)))
+    return d_logp, d_entropy

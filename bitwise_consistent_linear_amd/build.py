@@ -1,4 +1,4 @@
-"""Build libgdn_cpr.so in-tree with hipcc for gfx950 (cross-compiles without a GPU).
+"""Build libgdn_cpr.so and libgdn_policy.so in-tree with hipcc for gfx950 (cross-compiles without a GPU).
 
 Flags that the contract depends on:
   -ffp-contract=off                  no fusion other than the explicit fmaf
@@ -38,9 +38,12 @@ FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source into bitwise_consistent_linear_amd/libgdn_cpr.so; return its path.
-    Sources compile to objects side by side (one hipcc per source), then link."""
+POLICY_LIB = os.path.join(PKG, "libgdn_policy.so")
+POLICY_SOURCES = ["norm.hip", "linear_i8.hip", "logprob.hip", "policy_loss.hip", "policy_api.cpp"]
+
+
+def _build(sources, lib, verbose):
+    """Compile the sources to objects side by side (one hipcc per source), then link them."""
     from concurrent.futures import ThreadPoolExecutor
 
     objdir = os.path.join(ROOT, "_build")
@@ -55,14 +58,14 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         return obj, subprocess.run(cmd, capture_output=True, text=True)
 
-    jobs = max(1, min(len(SOURCES), os.cpu_count() or 1))
+    jobs = max(1, min(len(sources), os.cpu_count() or 1))
     with ThreadPoolExecutor(jobs) as pool:
-        results = list(pool.map(compile_one, SOURCES))
-    for (obj, res), src in zip(results, SOURCES):
+        results = list(pool.map(compile_one, sources))
+    for (obj, res), src in zip(results, sources):
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError(f"hipcc failed to compile {src}")
-    tmp = LIB + ".tmp"
+    tmp = lib + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp,
            *[obj for obj, _ in results]]
     if verbose:
@@ -70,9 +73,21 @@ def build(verbose: bool = False) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed to link libgdn_cpr.so")
-    os.replace(tmp, LIB)
-    return LIB
+        raise RuntimeError(f"hipcc failed to link {os.path.basename(lib)}")
+    os.replace(tmp, lib)
+    return lib
+
+
+def build(verbose: bool = False) -> str:
+    """Build bitwise_consistent_linear_amd/libgdn_cpr.so; return its path."""
+    return _build(SOURCES, LIB, verbose)
+
+
+def build_policy(verbose: bool = False) -> str:
+    """Build bitwise_consistent_linear_amd/libgdn_policy.so, the policy-head operators, with
+    the same flags; return its path. A library of its own: libgdn_cpr.so holds exactly the
+    contract's entry points and only its binary32 instructions."""
+    return _build(POLICY_SOURCES, POLICY_LIB, verbose)
 
 
 PROBE_LIB = os.path.join(PKG, "libgdn_probe.so")
@@ -96,11 +111,11 @@ def build_probe(verbose: bool = False) -> str:
 KERNEL_SOURCES = [s for s in SOURCES if s.endswith(".hip")]
 
 
-def device_asm(out_path: str) -> str:
-    """Write the gfx950 assembly of every kernel source, concatenated (for instruction-mix
-    checks)."""
+def device_asm(out_path: str, sources=None) -> str:
+    """Write the gfx950 assembly of the kernel sources (default: libgdn_cpr.so's),
+    concatenated (for instruction-mix checks)."""
     parts = []
-    for src in KERNEL_SOURCES:
+    for src in KERNEL_SOURCES if sources is None else sources:
         one = out_path + "." + src + ".s"
         cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
                "-fno-fast-math", "-fno-gpu-flush-denormals-to-zero",
@@ -118,4 +133,5 @@ def device_asm(out_path: str) -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_policy(verbose=True))
     print(build_probe(verbose=True))

@@ -1,0 +1,196 @@
+// Log-probability of the chosen token of each row of logits, and its gradient, on gfx950.
+//
+// Forward: bound by the one read of the logits. A workgroup takes a row; each thread keeps a
+// running maximum m of its logits and, relative to it, the sums s of the exponentials and t
+// of the exponentials times the differences; the threads' triples are then merged over lanes
+// and waves in a fixed order. lse = scale m + log s, logp = scale (v[id] - m) - log s,
+// entropy = log s - scale t / s: differences from the maximum keep what differences of large
+// logits would lose. The order depends on the vocabulary alone, so a row has the same bits
+// in any batch.
+//
+// Backward: elementwise in the logits, bound by reading them and writing the gradient.
+
+#include "policy_internal.h"
+#include "policy_rows.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLowest = -3.4028234663852886e38f;
+
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+__device__ __forceinline__ int64_t id_of(const LogprobArgs &p, int64_t row) {
+  return p.id64 ? static_cast<const int64_t *>(p.ids)[row]
+                : (int64_t)static_cast<const int32_t *>(p.ids)[row];
+}
+
+// Over some logits v (not yet scaled): their maximum m (the lowest finite value if there are
+// none), s = sum(exp(scale (v - m))) and t = sum(exp(scale (v - m)) (v - m)). Differences
+// come before the scale, so neither overflows a sum, and c = scale / ln 2 turns them into
+// powers of two. A v of -infinity has exp 0, and its difference is held finite in t.
+// kFar: a distance whose exponential is 0 for every admitted scale (>= 2^-40) and whose
+// product with a count of values is finite.
+constexpr float kFar = -1.0e28f;
+struct Softmax {
+  float m, s, t;
+};
+
+// The sums taken relative to `to` >= a.m. Where a.m is the lowest value and s is 0 they stay 0.
+__device__ __forceinline__ void rebase(Softmax &a, float to, float c) {
+  const float d = fmaxf(a.m - to, kFar), k = __builtin_amdgcn_exp2f(d * c);
+  a.t = k * fmaf(a.s, d, a.t);
+  a.s = k * a.s;
+  a.m = to;
+}
+
+__device__ __forceinline__ Softmax merge(Softmax a, Softmax b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  rebase(a, m, c);
+  rebase(b, m, c);
+  a.s += b.s;
+  a.t += b.t;
+  return a;
+}
+
+// Eight logits of a row at [col, col + 8), -infinity past its end.
+template <bool B16>
+__device__ __forceinline__ void load_logits(Vec8<B16> &v, const void *base, int64_t off,
+                                            int64_t col, int64_t vocab) {
+  if (col + 8 <= vocab) {
+    v.load(base, off + col);
+  } else {
+    const int n = col < vocab ? (int)(vocab - col) : 0;
+    v.load_part(base, off + col, n, kNegInf);
+  }
+}
+
+constexpr int kFwdThreads = 512, kFwdVecs = 4;
+
+template <bool B16, bool ENT>
+__global__ __launch_bounds__(kFwdThreads) void logprob_fwd_kernel(const LogprobArgs p) {
+  __shared__ Softmax part[kFwdThreads / 64];
+  const int64_t row = blockIdx.x, V = p.vocab;
+  const int64_t id = id_of(p, row);
+  if (id < 0 || id >= V) {
+    if (threadIdx.x == 0) {
+      p.logp[row] = p.lse[row] = 0.0f;
+      if (ENT) p.entropy[row] = 0.0f;
+    }
+    return;
+  }
+  const int64_t off = row * p.stride;
+  const float c = p.scale_log2e;
+  Softmax a{kLowest, 0.0f, 0.0f};
+  for (int64_t c0 = 0; c0 < V; c0 += kFwdThreads * 8 * kFwdVecs) {
+    Vec8<B16> x[kFwdVecs];
+#pragma unroll
+    for (int j = 0; j < kFwdVecs; ++j)
+      load_logits(x[j], p.logits, off, c0 + 8 * (j * kFwdThreads + threadIdx.x), V);
+    float top = a.m;
+#pragma unroll
+    for (int j = 0; j < kFwdVecs; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[j].get(e));
+    rebase(a, top, c);
+#pragma unroll
+    for (int j = 0; j < kFwdVecs; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = x[j].get(e) - top, k = __builtin_amdgcn_exp2f(d * c);
+        a.s += k;
+        if (ENT) a.t = fmaf(k, fmaxf(d, kFar), a.t);
+      }
+  }
+#pragma unroll
+  for (int w = 1; w < 64; w *= 2) {
+    const Softmax b{__shfl_xor(a.m, w, 64), __shfl_xor(a.s, w, 64), __shfl_xor(a.t, w, 64)};
+    a = merge(a, b, c);
+  }
+  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kFwdThreads / 64; ++i) a = merge(a, part[i], c);
+    const float z = B16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[off + id])
+                        : static_cast<const float *>(p.logits)[off + id];
+    const float ls = logf(a.s);
+    const bool none = a.s == 0.0f;  // every logit is -inf
+    p.lse[row] = none ? kNegInf : fmaf(a.m, p.scale, ls);
+    p.logp[row] = none ? kNegInf : fmaf(z - a.m, p.scale, -ls);
+    if (ENT) p.entropy[row] = none ? 0.0f : fmaf(-a.t / a.s, p.scale, ls);
+  }
+}
+
+constexpr int kBwdThreads = 256, kBwdVecs = 2, kBwdSpan = kBwdThreads * 8 * kBwdVecs;
+
+template <bool B16, bool ENT>
+__global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobArgs p) {
+  const int64_t V = p.vocab, spans = (V + kBwdSpan - 1) / kBwdSpan;
+  const int64_t row = blockIdx.x / spans, c0 = (blockIdx.x % spans) * kBwdSpan;
+  const int64_t id = id_of(p, row);
+  const float lse = p.lse[row];
+  const bool use = id >= 0 && id < V && lse != kNegInf;
+  const float scale = p.scale;
+  const float g = use ? p.d_logp[row] * scale : 0.0f;
+  const float h = ENT && use ? p.d_entropy[row] * scale : 0.0f;
+  const float H = ENT && use ? p.entropy[row] : 0.0f;
+  Vec8<B16> x[kBwdVecs];
+  if (use) {
+#pragma unroll
+    for (int j = 0; j < kBwdVecs; ++j)
+      load_row(x[j], p.logits, row * p.stride, c0 + 8 * (j * kBwdThreads + threadIdx.x), V);
+  }
+#pragma unroll
+  for (int j = 0; j < kBwdVecs; ++j) {
+    const int64_t c = c0 + 8 * (j * kBwdThreads + threadIdx.x);
+    float d[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = 0.0f;
+    if (use) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = fmaf(x[j].get(e), scale, -lse), q = exp_of(z);
+        float k = g;
+        if (ENT) k = fmaf(h, z + H, g);
+        d[e] = q == 0.0f ? 0.0f : -q * k;
+        if (c + e == id) d[e] += g;
+      }
+    }
+    store_row<B16>(p.d_logits, row * V, c, V, d);
+  }
+}
+
+hipError_t run(const void *fn, const LogprobArgs &a, int64_t grid, int threads,
+               hipStream_t stream) {
+  LogprobArgs args = a;
+  void *kargs[] = {&args};
+  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(threads), kargs, 0, stream);
+}
+
+}  // namespace
+
+hipError_t launch_logprob_fwd(const LogprobArgs &a, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  const void *fn = a.bf16 ? (a.entropy ? (const void *)logprob_fwd_kernel<true, true>
+                                       : (const void *)logprob_fwd_kernel<true, false>)
+                          : (a.entropy ? (const void *)logprob_fwd_kernel<false, true>
+                                       : (const void *)logprob_fwd_kernel<false, false>);
+  return run(fn, a, a.rows, kFwdThreads, stream);
+}
+
+int64_t logprob_bwd_grid(const LogprobArgs &a) {
+  return a.rows * ((a.vocab + kBwdSpan - 1) / kBwdSpan);
+}
+
+hipError_t launch_logprob_bwd(const LogprobArgs &a, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  const void *fn = a.bf16 ? (a.d_entropy ? (const void *)logprob_bwd_kernel<true, true>
+                                         : (const void *)logprob_bwd_kernel<true, false>)
+                          : (a.d_entropy ? (const void *)logprob_bwd_kernel<false, true>
+                                         : (const void *)logprob_bwd_kernel<false, false>);
+  return run(fn, a, logprob_bwd_grid(a), kBwdThreads, stream);
+}
+
+}  // namespace gdn
