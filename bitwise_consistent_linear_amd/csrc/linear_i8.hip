@@ -108,47 +108,244 @@ hipError_t quantize_as(const QuantizeArgs &a, hipStream_t stream) {
 
 // ------------------------------------------------------------------------------ product
 
-// Values of one output row at columns n .. n + 3.
+// v_mfma_i32_16x16x64_i8: lane l gives row l % 16 of either operand at k = 16 (l / 16) .. + 15,
+// and holds the results of rows 4 (l / 16) .. + 3 of the first operand and row l % 16 of the
+// second. The first operand is W, so a lane's four results are neighbours in a row of Y; two
+// products whose W rows are 8 (i / 4) + 4 j + i % 4 (j = 0, 1) give a lane eight neighbours.
+__device__ __forceinline__ i32x4 mfma(i32x4 w, i32x4 x, i32x4 acc) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, acc, 0, 0, 0);
+}
+__device__ __forceinline__ int pair_row(int i, int j) { return 8 * (i / 4) + 4 * j + i % 4; }
+
+// Eight neighbouring results of row m from column n on.
 template <bool YB>
-__device__ __forceinline__ void store4(const LinearI8Args &p, int64_t m, int64_t n, i32x4 acc,
-                                       float xs, const float (&ws)[4]) {
-  float v[4];
+__device__ __forceinline__ void store8(const LinearI8Args &p, int64_t m, int64_t n, i32x4 lo,
+                                       i32x4 hi, float xs, const float (&ws)[8]) {
+  float v[8];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) v[r] = (float)acc[r] * xs * ws[r];
-  const int64_t at = m * p.n + n;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (n + r < p.n) {
-      if (YB)
-        static_cast<uint16_t *>(p.y)[at + r] = (uint16_t)to_bf16(v[r]);
-      else
-        static_cast<float *>(p.y)[at + r] = v[r];
-    }
+  for (int r = 0; r < 4; ++r) {
+    v[r] = (float)lo[r] * xs * ws[r];
+    v[4 + r] = (float)hi[r] * xs * ws[4 + r];
+  }
+  store_row<YB>(p.y, m * p.n, n, p.n, v);
 }
 
-// One wave per 16 x 16 tile of Y, operands straight from memory. v_mfma_i32_16x16x64_i8: lane
-// l gives row l % 16 of either operand at k = 16 (l / 16) .. + 15, and holds the results of
-// rows 4 (l / 16) .. + 3 of the first operand and row l % 16 of the second. The first operand
-// is W, so a lane's four results are neighbours in a row of Y.
-template <bool YB>
-__global__ __launch_bounds__(64) void linear_i8_kernel(const LinearI8Args p) {
-  const int l = threadIdx.x;
-  const int64_t tiles_n = (p.n + 15) / 16;
-  const int64_t n0 = blockIdx.x % tiles_n * 16, m0 = blockIdx.x / tiles_n * 16;
-  const int64_t wrow = n0 + l % 16 < p.n ? n0 + l % 16 : p.n - 1;
-  const int64_t xrow = m0 + l % 16 < p.m ? m0 + l % 16 : p.m - 1;
-  const int8_t *w = p.wq + wrow * p.k + 16 * (l / 16), *x = p.xq + xrow * p.k + 16 * (l / 16);
-  i32x4 acc = {0, 0, 0, 0};
-  for (int k = 0; k < p.k; k += 64)
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4 *>(w + k),
-                                                *reinterpret_cast<const i32x4 *>(x + k), acc, 0, 0, 0);
-  const int64_t m = m0 + l % 16, n = n0 + 4 * (l / 16);
-  if (m < p.m) {
-    float ws[4];
+__device__ __forceinline__ void load_scales(const LinearI8Args &p, int64_t n, float (&ws)[8]) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) ws[r] = n + r < p.n ? p.w_scale[n + r] : 0.0f;
-    store4<YB>(p, m, n, acc, p.x_scale[m], ws);
+  for (int r = 0; r < 8; ++r) ws[r] = n + r < p.n ? p.w_scale[n + r] : 0.0f;
+}
+
+// Few rows: W's bytes are what counts, each read once, straight into the operand registers. A
+// workgroup takes 32 columns and MT groups of 16 rows; its eight waves take the 128-byte lines
+// of K in turn and their integer sums are added in LDS.
+template <int MT, bool YB>
+__global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args p) {
+  constexpr int U = MT == 4 ? 1 : MT == 2 ? 2 : 4;  // lines of K in flight
+  __shared__ i32x4 part[8][2 * MT][64];
+  const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t n0 = (int64_t)blockIdx.x * 32;
+  const int8_t *w[2], *x[MT];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t row = n0 + pair_row(l % 16, j);
+    w[j] = p.wq + (row < p.n ? row : p.n - 1) * p.k + 16 * (l / 16);
   }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = 16 * i + l % 16;
+    x[i] = p.xq + (row < p.m ? row : p.m - 1) * p.k + 16 * (l / 16);
+  }
+  i32x4 acc[2][MT];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
+  auto at = [](const int8_t *b, int k) { return *reinterpret_cast<const i32x4 *>(b + k); };
+  const int lines = p.k / 128;
+  int line = wave;
+  for (; line + 8 * (U - 1) < lines; line += 8 * U) {
+    i32x4 wf[U][2][2], xf[U][2][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = (line + 8 * u) * 128 + 64 * h;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) wf[u][h][j] = at(w[j], k);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xf[u][h][i] = at(x[i], k);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[j][i] = mfma(wf[u][h][j], xf[u][h][i], acc[j][i]);
+  }
+  for (; line < lines; line += 8)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = line * 128 + 64 * h;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const i32x4 wf = at(w[j], k);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[j][i] = mfma(wf, at(x[i], k), acc[j][i]);
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) part[wave][2 * i + j][l] = acc[j][i];
+  __syncthreads();
+  if (wave < MT) {  // wave i finishes rows 16 i .. + 15
+    i32x4 lo = part[0][2 * wave][l], hi = part[0][2 * wave + 1][l];
+#pragma unroll
+    for (int v = 1; v < 8; ++v) {
+      lo += part[v][2 * wave][l];
+      hi += part[v][2 * wave + 1][l];
+    }
+    const int64_t m = 16 * wave + l % 16, n = n0 + 8 * (l / 16);
+    if (m < p.m) {
+      float ws[8];
+      load_scales(p, n, ws);
+      store8<YB>(p, m, n, lo, hi, p.x_scale[m], ws);
+    }
+  }
+}
+
+// A BN x BM tile of Y by (BN / TN) x (BM / TM) waves, each TN columns by TM rows. K goes
+// through LDS 128 bytes at a time, two stages: the loads of the next one, straight from memory
+// into LDS, are in flight while the matrix units work on the current one. A line of 128 bytes
+// is held as eight 16-byte chunks, chunk c of row r at place c ^ key(r), so that the lanes of
+// an operand read, which want the same chunk of 16 rows, spread over the banks. The loads
+// write LDS in the order of the lanes, so the permutation is in which chunk a lane fetches.
+__device__ __forceinline__ int x_key(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int w_key(int r) { return ((r >> 3) & 3) << 1 | ((r >> 1) & 1); }
+
+template <int BM, int BN, int TM, int TN, bool YB>
+__global__ __launch_bounds__(BM / TM *(BN / TN) * 64) void linear_i8_tile_kernel(const LinearI8Args p) {
+  constexpr int kWaves = BM / TM * (BN / TN), MI = TM / 16, NP = TN / 32;
+  constexpr int kLoads = (BM + BN) / 8 / kWaves;  // 1 KiB (8 rows) each, per wave and stage
+  static_assert((BM + BN) / 8 % kWaves == 0 && BN / 8 % 1 == 0, "whole loads");
+  __shared__ __align__(128) int8_t stage0[(BM + BN) * 128];
+  __shared__ __align__(128) int8_t stage1[(BM + BN) * 128];
+  const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  // tiles: each XCD (workgroup % 8) a run of neighbours, in bands of 8 tiles of rows
+  const int64_t tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
+  const int64_t total = tiles_m * tiles_n, per = (total + 7) / 8;
+  const int64_t tile = blockIdx.x % 8 * per + blockIdx.x / 8;
+  if (blockIdx.x / 8 >= per || tile >= total) return;
+  const int64_t band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
+  const int64_t height = tiles_m - 8 * band < 8 ? tiles_m - 8 * band : 8;
+  const int64_t m0 = (8 * band + in_band % height) * BM, n0 = in_band / height * BN;
+
+  // the wave's loads of a stage: a base in scalar registers and an offset per lane; rows past
+  // the end repeat the last one
+  const int8_t *wbase = p.wq + n0 * p.k, *xbase = p.xq + m0 * p.k;
+  const int last_w = (int)(p.n - n0 < BN ? p.n - n0 : BN) - 1;
+  const int last_x = (int)(p.m - m0 < BM ? p.m - m0 : BM) - 1;
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = (wave * kLoads + i) * 8 + l / 8;  // W's rows, then X's
+    if ((wave * kLoads + i) * 8 < BN)
+      off[i] = (uint32_t)(r < last_w ? r : last_w) * p.k + 16 * (l % 8 ^ w_key(r));
+    else
+      off[i] = (uint32_t)(r - BN < last_x ? r - BN : last_x) * p.k + 16 * (l % 8 ^ x_key(r - BN));
+  }
+  auto fetch = [&](int8_t *to, int k) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int8_t *base = ((wave * kLoads + i) * 8 < BN ? wbase : xbase) + k;
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void *)(base + off[i]),
+          (__attribute__((address_space(3))) void *)(to + (wave * kLoads + i) * 1024), 16, 0, 0);
+    }
+  };
+
+  i32x4 acc[2 * NP][MI];
+#pragma unroll
+  for (int j = 0; j < 2 * NP; ++j)
+#pragma unroll
+    for (int i = 0; i < MI; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
+  const int wn = wave % (BN / TN) * TN, wm = wave / (BN / TN) * TM;
+  auto compute = [&](const int8_t *from) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      i32x4 xf[MI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int r = wm + 16 * i + l % 16;
+        xf[i] = *reinterpret_cast<const i32x4 *>(from + (BN + r) * 128 + 16 * ((4 * h + l / 16) ^ x_key(r)));
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * NP; ++j) {
+        const int r = wn + j / 2 * 32 + pair_row(l % 16, j % 2);
+        const i32x4 wf = *reinterpret_cast<const i32x4 *>(from + r * 128 + 16 * ((4 * h + l / 16) ^ w_key(r)));
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[j][i] = mfma(wf, xf[i], acc[j][i]);
+      }
+    }
+  };
+
+  fetch(stage0, 0);
+  for (int k = 0; k + 256 <= p.k; k += 256) {
+    __syncthreads();  // stage0 has arrived; stage1's last reader is done
+    fetch(stage1, k + 128);
+    compute(stage0);
+    __syncthreads();
+    fetch(stage0, k + 256 < p.k ? k + 256 : k);  // after the last stage: one not needed
+    compute(stage1);
+  }
+  if (p.k % 256 != 0) {
+    __syncthreads();
+    compute(stage0);
+  }
+
+#pragma unroll
+  for (int q = 0; q < NP; ++q) {
+    const int64_t n = n0 + wn + 32 * q + 8 * (l / 16);
+    float ws[8];
+    load_scales(p, n, ws);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t m = m0 + wm + 16 * i + l % 16;
+      if (m < p.m) store8<YB>(p, m, n, acc[2 * q][i], acc[2 * q + 1][i], p.x_scale[m], ws);
+    }
+  }
+}
+
+struct Launch {
+  const void *fn;
+  int threads;
+  int64_t grid;
+};
+
+template <int MT>
+Launch rows_launch(const LinearI8Args &a) {
+  return {a.y_bf16 ? (const void *)linear_i8_rows_kernel<MT, true>
+                   : (const void *)linear_i8_rows_kernel<MT, false>,
+          512, (a.n + 31) / 32};
+}
+
+template <int BM, int BN, int TM, int TN>
+Launch tile_launch(const LinearI8Args &a) {
+  const int64_t total = (a.m + BM - 1) / BM * ((a.n + BN - 1) / BN);
+  return {a.y_bf16 ? (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, true>
+                   : (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, false>,
+          BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
+}
+
+Launch pick(const LinearI8Args &a) {
+  if (a.m <= 16) return rows_launch<1>(a);
+  if (a.m <= 32) return rows_launch<2>(a);
+  if (a.m <= 64) return rows_launch<4>(a);
+  const int64_t big = (a.m + 255) / 256 * ((a.n + 255) / 256);
+  if (big >= 200) return tile_launch<256, 256, 64, 128>(a);
+  return tile_launch<128, 128, 64, 64>(a);
 }
 
 }  // namespace
@@ -162,16 +359,14 @@ hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t stream) {
   return quantize_as<1024, 8>(a, stream);
 }
 
-int64_t linear_i8_grid(const LinearI8Args &a) { return (a.m + 15) / 16 * ((a.n + 15) / 16); }
+int64_t linear_i8_grid(const LinearI8Args &a) { return pick(a).grid; }
 
 hipError_t launch_linear_i8(const LinearI8Args &a, hipStream_t stream) {
-  const int64_t grid = linear_i8_grid(a);
-  if (grid <= 0) return hipSuccess;
+  if (a.m == 0 || a.n == 0) return hipSuccess;
+  const Launch go = pick(a);
   LinearI8Args args = a;
   void *kargs[] = {&args};
-  const void *fn = a.y_bf16 ? (const void *)linear_i8_kernel<true>
-                            : (const void *)linear_i8_kernel<false>;
-  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(64), kargs, 0, stream);
+  return hipLaunchKernel(go.fn, dim3((unsigned)go.grid), dim3(go.threads), kargs, 0, stream);
 }
 
 }  // namespace gdn
