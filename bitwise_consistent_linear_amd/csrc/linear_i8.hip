@@ -12,6 +12,7 @@ namespace gdn {
 namespace {
 
 using i32x4 = int __attribute__((ext_vector_type(4)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------------- quantisation
 
@@ -110,68 +111,63 @@ hipError_t quantize_as(const QuantizeArgs &a, hipStream_t stream) {
 
 // v_mfma_i32_16x16x64_i8: lane l gives row l % 16 of either operand at k = 16 (l / 16) .. + 15,
 // and holds the results of rows 4 (l / 16) .. + 3 of the first operand and row l % 16 of the
-// second. The first operand is W, so a lane's four results are neighbours in a row of Y; two
-// products whose W rows are 8 (i / 4) + 4 j + i % 4 (j = 0, 1) give a lane eight neighbours.
+// second. The first operand is W, so a lane's four results are neighbours in a row of Y.
 __device__ __forceinline__ i32x4 mfma(i32x4 w, i32x4 x, i32x4 acc) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, acc, 0, 0, 0);
 }
-__device__ __forceinline__ int pair_row(int i, int j) { return 8 * (i / 4) + 4 * j + i % 4; }
 
-// Eight neighbouring results of row m from column n on.
-template <bool YB>
-__device__ __forceinline__ void store8(const LinearI8Args &p, int64_t m, int64_t n, i32x4 lo,
-                                       i32x4 hi, float xs, const float (&ws)[8]) {
-  float v[8];
+__device__ __forceinline__ f32x4 scaled(i32x4 acc, float xs, f32x4 ws) {
+  f32x4 v;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    v[r] = (float)lo[r] * xs * ws[r];
-    v[4 + r] = (float)hi[r] * xs * ws[4 + r];
-  }
-  store_row<YB>(p.y, m * p.n, n, p.n, v);
+  for (int r = 0; r < 4; ++r) v[r] = (float)acc[r] * xs * ws[r];
+  return v;
 }
 
-__device__ __forceinline__ void load_scales(const LinearI8Args &p, int64_t n, float (&ws)[8]) {
+__device__ __forceinline__ f32x4 column_scales(const LinearI8Args &p, int64_t n) {
+  f32x4 ws;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) ws[r] = n + r < p.n ? p.w_scale[n + r] : 0.0f;
+  for (int r = 0; r < 4; ++r) ws[r] = p.w_scale[n + r < p.n ? n + r : p.n - 1];
+  return ws;
 }
 
-// Few rows: W's bytes are what counts, each read once, straight into the operand registers. A
-// workgroup takes 32 columns and MT groups of 16 rows; its eight waves take the 128-byte lines
-// of K in turn and their integer sums are added in LDS.
-template <int MT, bool YB>
+// Few rows: W's bytes are what counts, each read once by a group of 16 MT rows, straight into
+// the operand registers. A workgroup takes 16 NT columns; its eight waves take the 128-byte
+// lines of K in turn and their integer sums are added in LDS.
+template <int MT, int NT, bool YB>
 __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args p) {
-  constexpr int U = MT == 4 ? 1 : MT == 2 ? 2 : 4;  // lines of K in flight
-  __shared__ i32x4 part[8][2 * MT][64];
+  constexpr int U = MT == 2 ? 2 : 4;  // lines of K in flight
+  __shared__ i32x4 part[8][NT * MT][64];
   const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t n0 = (int64_t)blockIdx.x * 32;
-  const int8_t *w[2], *x[MT];
+  const int64_t tiles_n = (p.n + 16 * NT - 1) / (16 * NT);
+  const int64_t n0 = blockIdx.x % tiles_n * (16 * NT), m0 = blockIdx.x / tiles_n * (16 * MT);
+  const int8_t *w[NT], *x[MT];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t row = n0 + pair_row(l % 16, j);
+  for (int j = 0; j < NT; ++j) {
+    const int64_t row = n0 + 16 * j + l % 16;
     w[j] = p.wq + (row < p.n ? row : p.n - 1) * p.k + 16 * (l / 16);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int64_t row = 16 * i + l % 16;
+    const int64_t row = m0 + 16 * i + l % 16;
     x[i] = p.xq + (row < p.m ? row : p.m - 1) * p.k + 16 * (l / 16);
   }
-  i32x4 acc[2][MT];
+  i32x4 acc[NT][MT];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
   auto at = [](const int8_t *b, int k) { return *reinterpret_cast<const i32x4 *>(b + k); };
   const int lines = p.k / 128;
   int line = wave;
   for (; line + 8 * (U - 1) < lines; line += 8 * U) {
-    i32x4 wf[U][2][2], xf[U][2][MT];
+    i32x4 wf[U][2][NT], xf[U][2][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = (line + 8 * u) * 128 + 64 * h;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) wf[u][h][j] = at(w[j], k);
+        for (int j = 0; j < NT; ++j) wf[u][h][j] = at(w[j], k);
 #pragma unroll
         for (int i = 0; i < MT; ++i) xf[u][h][i] = at(x[i], k);
       }
@@ -180,7 +176,7 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int i = 0; i < MT; ++i) acc[j][i] = mfma(wf[u][h][j], xf[u][h][i], acc[j][i]);
   }
@@ -189,132 +185,225 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
     for (int h = 0; h < 2; ++h) {
       const int k = line * 128 + 64 * h;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < NT; ++j) {
         const i32x4 wf = at(w[j], k);
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = mfma(wf, at(x[i], k), acc[j][i]);
       }
     }
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) part[wave][2 * i + j][l] = acc[j][i];
+    for (int i = 0; i < MT; ++i) part[wave][j * MT + i][l] = acc[j][i];
   __syncthreads();
-  if (wave < MT) {  // wave i finishes rows 16 i .. + 15
-    i32x4 lo = part[0][2 * wave][l], hi = part[0][2 * wave + 1][l];
+  if (wave < NT * MT) {  // wave j MT + i finishes columns 16 j .. + 15 of rows 16 i .. + 15
+    i32x4 sum = part[0][wave][l];
 #pragma unroll
-    for (int v = 1; v < 8; ++v) {
-      lo += part[v][2 * wave][l];
-      hi += part[v][2 * wave + 1][l];
-    }
-    const int64_t m = 16 * wave + l % 16, n = n0 + 8 * (l / 16);
+    for (int v = 1; v < 8; ++v) sum += part[v][wave][l];
+    const int64_t m = m0 + wave % MT * 16 + l % 16, n = n0 + wave / MT * 16 + 4 * (l / 16);
     if (m < p.m) {
-      float ws[8];
-      load_scales(p, n, ws);
-      store8<YB>(p, m, n, lo, hi, p.x_scale[m], ws);
+      const f32x4 v = scaled(sum, p.x_scale[m], column_scales(p, n));
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < p.n) {
+          if (YB)
+            static_cast<uint16_t *>(p.y)[m * p.n + n + r] = (uint16_t)to_bf16(v[r]);
+          else
+            static_cast<float *>(p.y)[m * p.n + n + r] = v[r];
+        }
     }
   }
 }
 
-// A BN x BM tile of Y by (BN / TN) x (BM / TM) waves, each TN columns by TM rows. K goes
-// through LDS 128 bytes at a time, two stages: the loads of the next one, straight from memory
-// into LDS, are in flight while the matrix units work on the current one. A line of 128 bytes
-// is held as eight 16-byte chunks, chunk c of row r at place c ^ key(r), so that the lanes of
-// an operand read, which want the same chunk of 16 rows, spread over the banks. The loads
-// write LDS in the order of the lanes, so the permutation is in which chunk a lane fetches.
-__device__ __forceinline__ int x_key(int r) { return (r >> 1) & 7; }
-__device__ __forceinline__ int w_key(int r) { return ((r >> 3) & 3) << 1 | ((r >> 1) & 1); }
+// Sixteen bytes of row m of Y from column n on: 4 binary32 or 8 bf16 values.
+template <bool YB>
+__device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, int64_t n, i32x4 v) {
+  using unaligned = int __attribute__((ext_vector_type(4), aligned(YB ? 2 : 4)));
+  constexpr int kChunk = YB ? 8 : 4;
+  if (n + kChunk <= p.n) {
+    if (YB)
+      __builtin_nontemporal_store(
+          v, reinterpret_cast<unaligned *>(static_cast<uint16_t *>(p.y) + m * p.n + n));
+    else
+      __builtin_nontemporal_store(
+          v, reinterpret_cast<unaligned *>(static_cast<float *>(p.y) + m * p.n + n));
+  } else {
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e)
+      if (n + e < p.n) {
+        if (YB)
+          static_cast<uint16_t *>(p.y)[m * p.n + n + e] =
+              (uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2)));
+        else
+          static_cast<int *>(p.y)[m * p.n + n + e] = v[e];
+      }
+  }
+}
+
+// A BN x BM tile of Y by (BN / TN) x (BM / TM) waves, each TN columns by TM rows.
+//
+// K goes through LDS in stages of 64 bytes of every row of the tile, four buffers of one
+// stage each: loads straight from memory into LDS run three stages ahead, and the operands
+// of the next stage are read from LDS under the products of the current one, interleaved
+// with them. A stage has one barrier: past it, the next stage has arrived for every wave and
+// the buffer of the current one, in registers by now, is free for the stage four ahead.
+//
+// The loads are the instruction itself: it has no destination register, and as the compiler's
+// builtin every later read of LDS waits for all of them. So the waits for them are written
+// out (arrive), and nothing else in the loop goes through the vector memory counter.
+//
+// A row's 64 bytes are four 16-byte chunks, chunk c of row r at place c ^ key(r), so that the
+// lanes of an operand read, which want one chunk of 16 rows, spread over the LDS banks (no
+// bank conflicts measured). The loads fill LDS in the order of their lanes, so the permutation
+// is in which chunk a lane fetches.
+//
+// Results go through LDS as well, 16 rows of a wave at a time, so that neighbouring lanes
+// store neighbouring values; the stores bypass the caches, which hold the operands.
+__device__ __forceinline__ int chunk_key(int r) { return (r >> 2) & 3; }
+
+// 16 bytes per lane from base + offset to LDS, lane after lane from `to` (uniform) on.
+__device__ __forceinline__ void load_to_lds(const int8_t *base, uint32_t offset, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"  // a wait state between writing m0 and its use
+      "global_load_lds_dwordx4 %1, %2"
+      :: "s"(to), "v"(offset), "s"(base) : "memory", "m0");
+}
+
+// At most `Loads` of the wave's loads are still on their way, every read of LDS is done, and
+// all waves are here.
+template <int Loads>
+__device__ __forceinline__ void arrive() {
+  static_assert(Loads < 64, "six bits of the counter");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (Loads & 15) | Loads >> 4 << 14);  // lgkmcnt = 0
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 template <int BM, int BN, int TM, int TN, bool YB>
-__global__ __launch_bounds__(BM / TM *(BN / TN) * 64) void linear_i8_tile_kernel(const LinearI8Args p) {
-  constexpr int kWaves = BM / TM * (BN / TN), MI = TM / 16, NP = TN / 32;
-  constexpr int kLoads = (BM + BN) / 8 / kWaves;  // 1 KiB (8 rows) each, per wave and stage
-  static_assert((BM + BN) / 8 % kWaves == 0 && BN / 8 % 1 == 0, "whole loads");
-  __shared__ __align__(128) int8_t stage0[(BM + BN) * 128];
-  __shared__ __align__(128) int8_t stage1[(BM + BN) * 128];
+__global__ __launch_bounds__(BM / TM *(BN / TN) * 64) __attribute__((amdgpu_waves_per_eu(TM * TN > 8192 ? 1 : 2)))
+void linear_i8_tile_kernel(const LinearI8Args p) {
+  constexpr int kWaves = BM / TM * (BN / TN), MI = TM / 16, NJ = TN / 16;
+  constexpr int kLoads = (BM + BN) / 16 / kWaves;  // 1 KiB (16 rows) each, per wave and stage
+  constexpr int kStage = (BM + BN) * 64;
+  static_assert((BM + BN) / 16 % kWaves == 0, "whole loads");
+  static_assert(kStage * 4 / kWaves >= 16 * TN * 4, "a wave's share of LDS holds 16 rows");
+  __shared__ __align__(128) int8_t lds[4 * kStage];
   const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // tiles: each XCD (workgroup % 8) a run of neighbours, in bands of 8 tiles of rows
   const int64_t tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
   const int64_t total = tiles_m * tiles_n, per = (total + 7) / 8;
   const int64_t tile = blockIdx.x % 8 * per + blockIdx.x / 8;
-  if (blockIdx.x / 8 >= per || tile >= total) return;
+  if (tile >= total) return;
   const int64_t band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
   const int64_t height = tiles_m - 8 * band < 8 ? tiles_m - 8 * band : 8;
   const int64_t m0 = (8 * band + in_band % height) * BM, n0 = in_band / height * BN;
 
-  // the wave's loads of a stage: a base in scalar registers and an offset per lane; rows past
-  // the end repeat the last one
+  // the wave's loads of a stage: a base in scalar registers and an offset per lane (below
+  // 256 rows of 2^16 bytes); rows past the end repeat the last one
   const int8_t *wbase = p.wq + n0 * p.k, *xbase = p.xq + m0 * p.k;
   const int last_w = (int)(p.n - n0 < BN ? p.n - n0 : BN) - 1;
   const int last_x = (int)(p.m - m0 < BM ? p.m - m0 : BM) - 1;
   uint32_t off[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = (wave * kLoads + i) * 8 + l / 8;  // W's rows, then X's
-    if ((wave * kLoads + i) * 8 < BN)
-      off[i] = (uint32_t)(r < last_w ? r : last_w) * p.k + 16 * (l % 8 ^ w_key(r));
-    else
-      off[i] = (uint32_t)(r - BN < last_x ? r - BN : last_x) * p.k + 16 * (l % 8 ^ x_key(r - BN));
+    const int at = (wave * kLoads + i) * 16, r = at + l / 4;  // W's rows, then X's
+    const int row = at < BN ? (r < last_w ? r : last_w) : (r - BN < last_x ? r - BN : last_x);
+    off[i] = (uint32_t)row * p.k + 16 * (l % 4 ^ chunk_key(r));
   }
-  auto fetch = [&](int8_t *to, int k) {
+  const int last = p.k - 64;  // past the end the last stage is fetched again, unused
+  const uint32_t lds_at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)lds + wave * kLoads * 1024);
+  auto fetch = [&](int buf, int k) {
+    if (k > last) k = last;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int8_t *base = ((wave * kLoads + i) * 8 < BN ? wbase : xbase) + k;
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void *)(base + off[i]),
-          (__attribute__((address_space(3))) void *)(to + (wave * kLoads + i) * 1024), 16, 0, 0);
-    }
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(((wave * kLoads + i) * 16 < BN ? wbase : xbase) + k, off[i],
+                  lds_at + buf * kStage + i * 1024);
   };
 
-  i32x4 acc[2 * NP][MI];
+  i32x4 acc[NJ][MI], xf[2][MI], wf[2][NJ];
 #pragma unroll
-  for (int j = 0; j < 2 * NP; ++j)
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int i = 0; i < MI; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
   const int wn = wave % (BN / TN) * TN, wm = wave / (BN / TN) * TM;
-  auto compute = [&](const int8_t *from) {
+  const int lane_at = l % 16 * 64 + 16 * ((l / 16) ^ chunk_key(l % 16));
+  auto read = [&](int buf, int b) {
+    const int8_t *from = lds + buf * kStage;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i32x4 xf[MI];
+    for (int i = 0; i < MI; ++i)
+      xf[b][i] = *reinterpret_cast<const i32x4 *>(from + (BN + wm + 16 * i) * 64 + lane_at);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int r = wm + 16 * i + l % 16;
-        xf[i] = *reinterpret_cast<const i32x4 *>(from + (BN + r) * 128 + 16 * ((4 * h + l / 16) ^ x_key(r)));
-      }
-#pragma unroll
-      for (int j = 0; j < 2 * NP; ++j) {
-        const int r = wn + j / 2 * 32 + pair_row(l % 16, j % 2);
-        const i32x4 wf = *reinterpret_cast<const i32x4 *>(from + r * 128 + 16 * ((4 * h + l / 16) ^ w_key(r)));
-#pragma unroll
-        for (int i = 0; i < MI; ++i) acc[j][i] = mfma(wf, xf[i], acc[j][i]);
-      }
-    }
+    for (int j = 0; j < NJ; ++j)
+      wf[b][j] = *reinterpret_cast<const i32x4 *>(from + (wn + 16 * j) * 64 + lane_at);
   };
-
-  fetch(stage0, 0);
-  for (int k = 0; k + 256 <= p.k; k += 256) {
-    __syncthreads();  // stage0 has arrived; stage1's last reader is done
-    fetch(stage1, k + 128);
-    compute(stage0);
-    __syncthreads();
-    fetch(stage0, k + 256 < p.k ? k + 256 : k);  // after the last stage: one not needed
-    compute(stage1);
-  }
-  if (p.k % 256 != 0) {
-    __syncthreads();
-    compute(stage0);
-  }
-
+  // One stage: the two stages after the next one may still be on their way.
+  auto step = [&](int cur, int b, int k) {
+    arrive<2 * kLoads>();
+    fetch(cur, k + 256);
+    read((cur + 1) % 4, 1 - b);
 #pragma unroll
-  for (int q = 0; q < NP; ++q) {
-    const int64_t n = n0 + wn + 32 * q + 8 * (l / 16);
-    float ws[8];
-    load_scales(p, n, ws);
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int64_t m = m0 + wm + 16 * i + l % 16;
-      if (m < p.m) store8<YB>(p, m, n, acc[2 * q][i], acc[2 * q + 1][i], p.x_scale[m], ws);
+      for (int i = 0; i < MI; ++i) acc[j][i] = mfma(wf[b][j], xf[b][i], acc[j][i]);
+    // an operand read, two products, ...
+#pragma unroll
+    for (int q = 0; q < MI + NJ; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, MI * NJ / (MI + NJ), 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fetch(i, 64 * i);
+  arrive<3 * kLoads>();
+  read(0, 0);
+  int k = 0;
+  for (; k + 256 <= p.k; k += 256) {
+    step(0, 0, k);
+    step(1, 1, k + 64);
+    step(2, 0, k + 128);
+    step(3, 1, k + 192);
+  }
+  if (k < p.k) {  // 128 bytes left
+    step(0, 0, k);
+    step(1, 1, k + 64);
+  }
+
+  arrive<0>();  // every load has landed and every operand been read: LDS is free
+  int8_t *own = lds + wave * (kStage * 4 / kWaves);
+  f32x4 ws[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) ws[j] = column_scales(p, n0 + wn + 16 * j + 4 * (l / 16));
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t mi = m0 + wm + 16 * i;
+    const float xs = p.x_scale[mi + l % 16 < p.m ? mi + l % 16 : p.m - 1];
+    // row r of 16: TN values as 16-byte chunks (4 binary32 or 8 bf16), chunk c at c ^ r
+    constexpr int kChunk = YB ? 8 : 4, kChunks = TN / kChunk;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const f32x4 v = scaled(acc[j][i], xs, ws[j]);
+      const int r = l % 16, n = 16 * j + 4 * (l / 16), c = (n / kChunk) ^ (r % kChunks);
+      int8_t *at = own + (r * kChunks + c) * 16;
+      if (YB)
+        *reinterpret_cast<uint2 *>(at + n % kChunk * 2) =
+            make_uint2(to_bf16(v[0]) | to_bf16(v[1]) << 16, to_bf16(v[2]) | to_bf16(v[3]) << 16);
+      else
+        *reinterpret_cast<f32x4 *>(at) = v;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int g = 0; g < kChunks / 4; ++g) {
+      const int q = 64 * g + l, r = q / kChunks, c = q % kChunks;
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(own + (r * kChunks + (c ^ (r % kChunks))) * 16);
+      const int64_t m = mi + r, n = n0 + wn + kChunk * c;
+      if (m < p.m) store_chunk<YB>(p, m, n, v);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -324,11 +413,11 @@ struct Launch {
   int64_t grid;
 };
 
-template <int MT>
+template <int MT, int NT>
 Launch rows_launch(const LinearI8Args &a) {
-  return {a.y_bf16 ? (const void *)linear_i8_rows_kernel<MT, true>
-                   : (const void *)linear_i8_rows_kernel<MT, false>,
-          512, (a.n + 31) / 32};
+  return {a.y_bf16 ? (const void *)linear_i8_rows_kernel<MT, NT, true>
+                   : (const void *)linear_i8_rows_kernel<MT, NT, false>,
+          512, (a.m + 16 * MT - 1) / (16 * MT) * ((a.n + 16 * NT - 1) / (16 * NT))};
 }
 
 template <int BM, int BN, int TM, int TN>
@@ -339,13 +428,25 @@ Launch tile_launch(const LinearI8Args &a) {
           BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
 }
 
+// The kernel of a size, by how many workgroups each would have. Up to 256 (one for each
+// compute unit) the rows kernels' split of K over the waves pays: 16 x 4096 x 4096 takes
+// 9.8 us in 256 workgroups of 16 x 16 against 13.4 in 64 of 64 x 64 tiles, and twice the
+// columns or rows for a workgroup costs 1 to 3 us. Past that, the largest tile that still
+// gives every unit one: 512 x 4096 x 4096 takes 20.4 us in tiles of 64 x 128 (256), 24.7 of
+// 128 x 128 (128), 50 of 256 x 256 (32); 4096 x 4096 x 4096 takes 130, 83 and 66. A tile is
+// not taller than twice the rows: 16 x 65536 x 4096 takes 63 us in tiles of 64 rows, 77 of 256.
 Launch pick(const LinearI8Args &a) {
-  if (a.m <= 16) return rows_launch<1>(a);
-  if (a.m <= 32) return rows_launch<2>(a);
-  if (a.m <= 64) return rows_launch<4>(a);
-  const int64_t big = (a.m + 255) / 256 * ((a.n + 255) / 256);
-  if (big >= 200) return tile_launch<256, 256, 64, 128>(a);
-  return tile_launch<128, 128, 64, 64>(a);
+  auto count = [&](int rows, int cols) {
+    return (a.m + rows - 1) / rows * ((a.n + cols - 1) / cols);
+  };
+  if (count(16, 16) <= 256) return rows_launch<1, 1>(a);
+  if (a.m <= 16 && count(16, 32) <= 256) return rows_launch<1, 2>(a);
+  if (count(32, 16) <= 256) return rows_launch<2, 1>(a);
+  if (count(32, 32) <= 256) return rows_launch<2, 2>(a);
+  if (a.m > 128 && count(256, 256) >= 200) return tile_launch<256, 256, 64, 128>(a);
+  if (a.m > 64 && count(128, 128) >= 256) return tile_launch<128, 128, 64, 64>(a);
+  if (count(64, 128) >= 256) return tile_launch<64, 128, 32, 64>(a);
+  return tile_launch<64, 64, 32, 32>(a);
 }
 
 }  // namespace

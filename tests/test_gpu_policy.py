@@ -212,7 +212,12 @@ def test_quantize_strided_rows():
 I8_SIZES = [(1, 1, 128), (1, 300, 256), (3, 17, 128), (16, 64, 4096), (17, 130, 384),
             (33, 257, 1024), (64, 48, 8192), (65, 1000, 640), (100, 129, 128), (129, 255, 2048),
             (200, 1030, 512), (256, 512, 1152), (257, 300, 256), (513, 640, 384),
-            (1000, 96, 256), (1300, 1100, 896), (8, 5000, 128), (2, 64, 65536)]
+            (1000, 96, 256), (1300, 1100, 896), (8, 5000, 128), (2, 64, 65536),
+            # tiles of 64 x 64, 64 x 128, 128 x 128 and 256 x 256, whole and ragged, with K of
+            # an even and an odd number of 128-byte lines, one line among them
+            (300, 4000, 128), (320, 4032, 512), (600, 4100, 384), (1024, 2048, 256),
+            (1100, 4100, 384), (2048, 2048, 128), (3500, 3700, 384), (3841, 3585, 128),
+            (200, 65537, 256)]
 
 
 @pytest.mark.parametrize("M,N,K", I8_SIZES)
