@@ -655,19 +655,47 @@ def policy_abi_version() -> int:
 
 def _code(dtype, name="out_dtype"):
     torch = _torch()
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return GDN_DTYPE_F32
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return GDN_DTYPE_BF16
     raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
 
 
-def _matrix(t, name, dtypes):
-    """A GPU matrix whose rows are contiguous; returns its row stride (0 repeats a row)."""
+@lru_cache(maxsize=None)
+def _dtypes():
+    """(float32,), (float32, bfloat16), (int8,), (int32, int64), (bool, uint8)"""
+    t = _torch()
+    return ((t.float32,), (t.float32, t.bfloat16), (t.int8,), (t.int32, t.int64),
+            (t.bool, t.uint8))
+
+
+# These calls take microseconds on the GPU, so their checks are one expression each; what is
+# wrong is found out only where something is.
+
+def _refuse(t, name, dtypes, shape, index):
+    _need(t, name, dtypes, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, expected GPU {index}")
+
+
+def _take(t, name, dtypes, shape, index):
+    """The pointer of a dense tensor of `shape` on GPU `index`."""
+    if not (hasattr(t, "get_device") and t.get_device() == index and t.dtype in dtypes
+            and t.shape == shape and t.is_contiguous()):
+        _refuse(t, name, dtypes, shape, index)
+    return t.data_ptr()
+
+
+def _rows(t, name, dtypes):
+    """Row stride, device index of a GPU matrix whose rows are contiguous (stride 0 repeats a
+    row)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on a GPU device")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
@@ -676,24 +704,35 @@ def _matrix(t, name, dtypes):
     stride, inner = t.stride()
     if inner != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must be contiguous inside a row, got strides {t.stride()}")
-    return stride if t.shape[0] > 1 else t.shape[1]
+    return (stride if t.shape[0] > 1 else t.shape[1]), index
 
 
-def _vector(t, name, dtypes, n):
-    _need(t, name, dtypes, 1)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-
-
-def _given_or_new(t, name, shape, dtype, device):
+def _place(t, name, dtype, shape, like, index):
     """The caller's output, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=like.device)
+    _take(t, name, (dtype,), shape, index)
+    return t
+
+
+def _raw_stream(index):
+    """The current stream of GPU `index`, which has to be the current device: the library
+    launches there."""
+    torch = _torch()
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the tensors are on GPU {index}, the current device is "
+                         f"{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _workspace_ptr(t, need, like, index):
+    """(tensor to keep, pointer, bytes) of a uint8 workspace, the caller's or a new one."""
     torch = _torch()
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, (dtype,), len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
-    return t
+        t = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif _need(t, "workspace", (torch.uint8,), 1).get_device() != index:
+        raise ValueError(f"workspace is on {t.device}, expected GPU {index}")
+    return t, t.data_ptr(), t.numel()
 
 
 def _on_stream(fn):
@@ -722,27 +761,22 @@ def layer_norm_fwd(x, weight, bias=None, *, eps=1e-5, kind="layer", y=None, mean
     have a stride), kind "layer" or "rms"; weight and bias [D] float32 or bfloat16 alike,
     bias None for 0. ``stream`` may name another stream than the current one.
     Returns (y [M, D] in x's dtype, mean [M] or None for "rms", rstd [M])."""
-    torch = _torch()
-    dts, f32 = (torch.float32, torch.bfloat16), torch.float32
+    f32, fl = _dtypes()[:2]
     k = _norm_kind(kind)
-    stride = _matrix(x, "x", dts)
+    stride, dev = _rows(x, "x", fl)
     M, D = x.shape
-    _vector(weight, "weight", dts, D)
-    if bias is not None:
-        _vector(bias, "bias", (weight.dtype,), D)
-    dev = x.device
-    y = _given_or_new(y, "y", (M, D), x.dtype, dev)
+    w = _take(weight, "weight", fl, (D,), dev)
+    b = None if bias is None else _take(bias, "bias", (weight.dtype,), (D,), dev)
+    y = _place(y, "y", x.dtype, (M, D), x, dev)
     if k == GDN_NORM_LAYER:
-        mean = _given_or_new(mean, "mean", (M,), f32, dev)
+        mean = _place(mean, "mean", f32[0], (M,), x, dev)
     elif mean is not None:
         raise ValueError("kind 'rms' has no mean")
-    rstd = _given_or_new(rstd, "rstd", (M,), f32, dev)
-    _same_device(("x", x), ("weight", weight), ("bias", bias), ("y", y), ("mean", mean),
-                 ("rstd", rstd))
+    rstd = _place(rstd, "rstd", f32[0], (M,), x, dev)
     shape = GdnNormShape(M, D, k, _code(x.dtype), _code(weight.dtype))
     _policy_check(policy_lib().gdn_layer_norm_fwd(
-        ctypes.byref(shape), _ptr(x), stride, _ptr(weight), _ptr(bias), eps, _ptr(y),
-        _ptr(mean), _ptr(rstd), _stream(None)))
+        ctypes.byref(shape), x.data_ptr(), stride, w, b, eps, y.data_ptr(), _ptr(mean),
+        rstd.data_ptr(), _raw_stream(dev)))
     return y, mean, rstd
 
 
@@ -762,42 +796,35 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, kind="layer", bias=None, dx=Non
     wanted (default: for kind "layer"). ``workspace`` is a uint8 GPU tensor of at least
     layer_norm_bwd_workspace_bytes() bytes (allocated here when omitted).
     Returns (dx [M, D] in x's dtype, d_weight [D] float32, d_bias [D] float32 or None)."""
-    torch = _torch()
-    dts, f32 = (torch.float32, torch.bfloat16), torch.float32
+    f32, fl = _dtypes()[:2]
     k = _norm_kind(kind)
     layer = k == GDN_NORM_LAYER
-    x_stride = _matrix(x, "x", dts)
-    dy_stride = _matrix(dy, "dy", (x.dtype,))
-    if dy.shape != x.shape:
-        raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} differ")
+    x_stride, dev = _rows(x, "x", fl)
+    dy_stride, dy_dev = _rows(dy, "dy", (x.dtype,))
+    if dy.shape != x.shape or dy_dev != dev:
+        raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} differ, in shape or GPU")
     M, D = x.shape
-    _vector(weight, "weight", dts, D)
+    w = _take(weight, "weight", fl, (D,), dev)
     if layer:
-        _vector(mean, "mean", (f32,), M)
+        _take(mean, "mean", f32, (M,), dev)
     elif mean is not None:
         raise ValueError("kind 'rms' has no mean")
-    _vector(rstd, "rstd", (f32,), M)
-    dev = x.device
-    dx = _given_or_new(dx, "dx", (M, D), x.dtype, dev)
-    d_weight = _given_or_new(d_weight, "d_weight", (D,), f32, dev)
+    rs = _take(rstd, "rstd", f32, (M,), dev)
+    dx = _place(dx, "dx", x.dtype, (M, D), x, dev)
+    d_weight = _place(d_weight, "d_weight", f32[0], (D,), x, dev)
     if bias is None:
         bias = layer or d_bias is not None
     if bias:
-        d_bias = _given_or_new(d_bias, "d_bias", (D,), f32, dev)
+        d_bias = _place(d_bias, "d_bias", f32[0], (D,), x, dev)
     elif d_bias is not None:
         raise ValueError("d_bias is given but bias is False")
     shape = GdnNormShape(M, D, k, _code(x.dtype), _code(weight.dtype))
-    if workspace is None:
-        workspace = torch.empty(layer_norm_bwd_workspace_bytes(shape), dtype=torch.uint8,
-                                device=dev)
-    _need(workspace, "workspace", (torch.uint8,), 1)
-    _same_device(("x", x), ("dy", dy), ("weight", weight), ("mean", mean), ("rstd", rstd),
-                 ("dx", dx), ("d_weight", d_weight), ("d_bias", d_bias),
-                 ("workspace", workspace))
+    need = 0 if workspace is not None else layer_norm_bwd_workspace_bytes(shape)
+    ws, ws_ptr, ws_bytes = _workspace_ptr(workspace, need, x, dev)
     _policy_check(policy_lib().gdn_layer_norm_bwd(
-        ctypes.byref(shape), _ptr(dy), dy_stride, _ptr(x), x_stride, _ptr(weight), _ptr(mean),
-        _ptr(rstd), _ptr(dx), _ptr(d_weight), _ptr(d_bias), _ptr(workspace),
-        workspace.numel(), _stream(None)))
+        ctypes.byref(shape), dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, w, _ptr(mean),
+        rs, dx.data_ptr(), d_weight.data_ptr(), _ptr(d_bias), ws_ptr, ws_bytes,
+        _raw_stream(dev)))
     return dx, d_weight, d_bias
 
 
@@ -807,14 +834,14 @@ def quantize_rows(x, *, xq=None, scale=None):
     to int8 with one scale, ties to even. Serves a linear layer's inputs and its weights
     [N, K]. Returns (xq int8 [M, K rounded up to I8_K_ALIGN, zeros in the padding],
     scale float32 [M])."""
-    torch = _torch()
-    stride = _matrix(x, "x", (torch.float32, torch.bfloat16))
+    f32, fl, i8 = _dtypes()[:3]
+    stride, dev = _rows(x, "x", fl)
     M, K = x.shape
-    xq = _given_or_new(xq, "xq", (M, -(-K // I8_K_ALIGN) * I8_K_ALIGN), torch.int8, x.device)
-    scale = _given_or_new(scale, "scale", (M,), torch.float32, x.device)
-    _same_device(("x", x), ("xq", xq), ("scale", scale))
-    _policy_check(policy_lib().gdn_quantize_rows(_ptr(x), M, K, stride, _code(x.dtype),
-                                                 _ptr(xq), _ptr(scale), _stream(None)))
+    xq = _place(xq, "xq", i8[0], (M, -(-K // I8_K_ALIGN) * I8_K_ALIGN), x, dev)
+    scale = _place(scale, "scale", f32[0], (M,), x, dev)
+    _policy_check(policy_lib().gdn_quantize_rows(
+        x.data_ptr(), M, K, stride, _code(x.dtype), xq.data_ptr(), scale.data_ptr(),
+        _raw_stream(dev)))
     return xq, scale
 
 
@@ -823,33 +850,32 @@ def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None):
     """gdn_linear_i8_fwd: Y = (xq wq^T) x_scale w_scale with exact integer sums. xq int8
     [M, Kp], wq int8 [N, Kp] as quantize_rows returns them, x_scale [M], w_scale [N] float32.
     Returns y [M, N] in out_dtype (float32 by default, or bfloat16)."""
-    torch = _torch()
-    i8, f32 = (torch.int8,), (torch.float32,)
+    f32, _, i8 = _dtypes()[:3]
     _need(xq, "xq", i8, 2)
     _need(wq, "wq", i8, 2)
     M, K = xq.shape
     N = wq.shape[0]
     if wq.shape[1] != K:
         raise ValueError(f"xq is {tuple(xq.shape)} but wq is {tuple(wq.shape)}")
-    _vector(x_scale, "x_scale", f32, M)
-    _vector(w_scale, "w_scale", f32, N)
+    dev = xq.get_device()
+    x_ptr, w_ptr = _take(xq, "xq", i8, (M, K), dev), _take(wq, "wq", i8, (N, K), dev)
+    xs = _take(x_scale, "x_scale", f32, (M,), dev)
+    ws = _take(w_scale, "w_scale", f32, (N,), dev)
     if out_dtype is None:
-        out_dtype = torch.float32 if y is None else y.dtype
+        out_dtype = f32[0] if y is None else y.dtype
     code = _code(out_dtype)
-    y = _given_or_new(y, "y", (M, N), out_dtype, xq.device)
-    _same_device(("xq", xq), ("x_scale", x_scale), ("wq", wq), ("w_scale", w_scale), ("y", y))
-    _policy_check(policy_lib().gdn_linear_i8_fwd(M, N, K, _ptr(xq), _ptr(x_scale), _ptr(wq),
-                                                 _ptr(w_scale), code, _ptr(y), _stream(None)))
+    y = _place(y, "y", out_dtype, (M, N), xq, dev)
+    _policy_check(policy_lib().gdn_linear_i8_fwd(M, N, K, x_ptr, xs, w_ptr, ws, code,
+                                                 y.data_ptr(), _raw_stream(dev)))
     return y
 
 
 def _logprob_args(logits, ids, scale):
-    torch = _torch()
-    stride = _matrix(logits, "logits", (torch.float32, torch.bfloat16))
+    _, fl, _, ints, _ = _dtypes()
+    stride, dev = _rows(logits, "logits", fl)
     M, V = logits.shape
-    _vector(ids, "ids", (torch.int32, torch.int64), M)
-    return GdnLogprobShape(M, V, stride, _code(logits.dtype),
-                           8 if ids.dtype == torch.int64 else 4, scale)
+    _take(ids, "ids", ints, (M,), dev)
+    return GdnLogprobShape(M, V, stride, _code(logits.dtype), ids.element_size(), scale), dev
 
 
 @_on_stream
@@ -858,17 +884,15 @@ def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=N
     softmax of scale * logits [M, V] (float32 or bfloat16; rows may have a stride), the
     log-sum-exp, and with entropy=True the entropy. Rows whose id is outside [0, V) are not
     scored: zeros. Returns (logp [M], lse [M], entropy [M] or None), float32."""
-    torch = _torch()
-    f32 = torch.float32
-    shape = _logprob_args(logits, ids, scale)
-    M, dev = shape.rows, logits.device
-    logp = _given_or_new(logp, "logp", (M,), f32, dev)
-    lse = _given_or_new(lse, "lse", (M,), f32, dev)
-    ent = torch.empty((M,), dtype=f32, device=dev) if entropy else None
-    _same_device(("logits", logits), ("ids", ids), ("logp", logp), ("lse", lse))
+    f32 = _dtypes()[0][0]
+    shape, dev = _logprob_args(logits, ids, scale)
+    rows = (shape.rows,)
+    logp = _place(logp, "logp", f32, rows, logits, dev)
+    lse = _place(lse, "lse", f32, rows, logits, dev)
+    ent = _place(None, "entropy", f32, rows, logits, dev) if entropy else None
     _policy_check(policy_lib().gdn_token_logprob_fwd(
-        ctypes.byref(shape), _ptr(logits), _ptr(ids), _ptr(logp), _ptr(lse), _ptr(ent),
-        _stream(None)))
+        ctypes.byref(shape), logits.data_ptr(), ids.data_ptr(), logp.data_ptr(),
+        lse.data_ptr(), _ptr(ent), _raw_stream(dev)))
     return logp, lse, ent
 
 
@@ -878,55 +902,46 @@ def token_logprob_bwd(logits, ids, lse, d_logp, *, scale=1.0, entropy=None, d_en
     """gdn_token_logprob_bwd: the gradient of token_logprob_fwd's logp, and of its entropy
     where entropy and d_entropy [M] are given, with respect to the logits. Returns d_logits
     [M, V] in the logits' dtype; d_logits=logits overwrites them."""
-    torch = _torch()
-    f32 = (torch.float32,)
-    shape = _logprob_args(logits, ids, scale)
-    M, V = logits.shape
-    _vector(lse, "lse", f32, M)
-    _vector(d_logp, "d_logp", f32, M)
+    f32 = _dtypes()[0]
+    shape, dev = _logprob_args(logits, ids, scale)
+    rows = (shape.rows,)
+    lse_ptr = _take(lse, "lse", f32, rows, dev)
+    dlp = _take(d_logp, "d_logp", f32, rows, dev)
+    ent = d_ent = None
     if d_entropy is not None:
         if entropy is None:
             raise ValueError("d_entropy needs the entropy that token_logprob_fwd returned")
-        _vector(entropy, "entropy", f32, M)
-        _vector(d_entropy, "d_entropy", f32, M)
-    else:
-        entropy = None
-    d_logits = _given_or_new(d_logits, "d_logits", (M, V), logits.dtype, logits.device)
-    _same_device(("logits", logits), ("ids", ids), ("lse", lse), ("d_logp", d_logp),
-                 ("entropy", entropy), ("d_entropy", d_entropy), ("d_logits", d_logits))
+        ent = _take(entropy, "entropy", f32, rows, dev)
+        d_ent = _take(d_entropy, "d_entropy", f32, rows, dev)
+    d_logits = _place(d_logits, "d_logits", logits.dtype, logits.shape, logits, dev)
     _policy_check(policy_lib().gdn_token_logprob_bwd(
-        ctypes.byref(shape), _ptr(logits), _ptr(ids), _ptr(lse), _ptr(d_logp), _ptr(entropy),
-        _ptr(d_entropy), _ptr(d_logits), _stream(None)))
+        ctypes.byref(shape), logits.data_ptr(), ids.data_ptr(), lse_ptr, dlp, ent, d_ent,
+        d_logits.data_ptr(), _raw_stream(dev)))
     return d_logits
 
 
 def _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens, clip_low,
                  clip_high, dual_clip, kl_coef, entropy_coef, reduction):
-    torch = _torch()
-    f32 = (torch.float32,)
+    """(GdnPolicyShape, device index, pointers up to cu_seqlens) of a policy loss call."""
+    f32, _, _, ints, flags = _dtypes()
     if reduction not in _REDUCTIONS:
         raise ValueError(f"reduction must be 'token' or 'sequence', got {reduction!r}")
     _need(logp, "logp", f32, 1)
-    T = logp.shape[0]
-    _vector(old_logp, "old_logp", f32, T)
-    _vector(advantages, "advantages", f32, T)
-    if ref_logp is not None:
-        _vector(ref_logp, "ref_logp", f32, T)
-    if entropy is not None:
-        _vector(entropy, "entropy", f32, T)
-    if mask is not None:
-        _vector(mask, "mask", (torch.bool, torch.uint8), T)
+    dev, tokens = logp.get_device(), logp.shape
     N = 1
     if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", (torch.int32,), 1)
         N = cu_seqlens.shape[0] - 1
-    _same_device(("logp", logp), ("old_logp", old_logp), ("advantages", advantages),
-                 ("ref_logp", ref_logp), ("entropy", entropy), ("mask", mask),
-                 ("cu_seqlens", cu_seqlens))
-    return GdnPolicyShape(T, N, _REDUCTIONS[reduction], 0, clip_low, clip_high,
+    ptrs = (logp.data_ptr(), _take(old_logp, "old_logp", f32, tokens, dev),
+            _take(advantages, "advantages", f32, tokens, dev),
+            None if ref_logp is None else _take(ref_logp, "ref_logp", f32, tokens, dev),
+            None if entropy is None else _take(entropy, "entropy", f32, tokens, dev),
+            None if mask is None else _take(mask, "mask", flags, tokens, dev),
+            None if cu_seqlens is None else _take(cu_seqlens, "cu_seqlens", ints[:1], (N + 1,),
+                                                  dev))
+    return GdnPolicyShape(tokens[0], N, _REDUCTIONS[reduction], 0, clip_low, clip_high,
                           0.0 if dual_clip is None else dual_clip,
                           0.0 if ref_logp is None else kl_coef,
-                          0.0 if entropy is None else entropy_coef)
+                          0.0 if entropy is None else entropy_coef), dev, ptrs
 
 
 def policy_loss_workspace_bytes(shape: GdnPolicyShape) -> int:
@@ -946,20 +961,17 @@ def policy_loss_fwd(logp, old_logp, advantages, *, ref_logp=None, entropy=None, 
     bool, None for all scored; cu_seqlens int32 [N + 1], None for one sequence).
     Returns (stats [5]: loss and the weighted means of policy loss, KL, entropy and share of
     tokens cut off; weight [N]: the weight of a scored token of each sequence), float32."""
-    torch = _torch()
-    shape = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
-                         clip_low, clip_high, dual_clip, kl_coef, entropy_coef, reduction)
-    dev = logp.device
-    stats = _given_or_new(stats, "stats", (5,), torch.float32, dev)
-    weight = _given_or_new(weight, "weight", (shape.seqs,), torch.float32, dev)
-    if workspace is None:
-        workspace = torch.empty(policy_loss_workspace_bytes(shape), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", (torch.uint8,), 1)
-    _same_device(("logp", logp), ("stats", stats), ("weight", weight), ("workspace", workspace))
+    f32 = _dtypes()[0][0]
+    shape, dev, ptrs = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask,
+                                    cu_seqlens, clip_low, clip_high, dual_clip, kl_coef,
+                                    entropy_coef, reduction)
+    stats = _place(stats, "stats", f32, (5,), logp, dev)
+    weight = _place(weight, "weight", f32, (shape.seqs,), logp, dev)
+    need = 0 if workspace is not None else policy_loss_workspace_bytes(shape)
+    ws, ws_ptr, ws_bytes = _workspace_ptr(workspace, need, logp, dev)
     _policy_check(policy_lib().gdn_policy_loss_fwd(
-        ctypes.byref(shape), _ptr(logp), _ptr(old_logp), _ptr(advantages), _ptr(ref_logp),
-        _ptr(entropy), _ptr(mask), _ptr(cu_seqlens), _ptr(stats), _ptr(weight),
-        _ptr(workspace), workspace.numel(), _stream(None)))
+        ctypes.byref(shape), *ptrs, stats.data_ptr(), weight.data_ptr(), ws_ptr, ws_bytes,
+        _raw_stream(dev)))
     return stats, weight
 
 
@@ -971,21 +983,17 @@ def policy_loss_bwd(logp, old_logp, advantages, weight, *, ref_logp=None, entrop
     """gdn_policy_loss_bwd: the gradient of d_loss * loss, given the weight [N] that
     policy_loss_fwd returned for the same arguments. Returns (d_logp [T], d_entropy [T], or
     None without an entropy), float32."""
-    torch = _torch()
-    f32 = torch.float32
-    shape = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
-                         clip_low, clip_high, dual_clip, kl_coef, entropy_coef, reduction)
-    _vector(weight, "weight", (f32,), shape.seqs)
-    T, dev = shape.tokens, logp.device
-    d_logp = _given_or_new(d_logp, "d_logp", (T,), f32, dev)
+    f32 = _dtypes()[0]
+    shape, dev, ptrs = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask,
+                                    cu_seqlens, clip_low, clip_high, dual_clip, kl_coef,
+                                    entropy_coef, reduction)
+    w = _take(weight, "weight", f32, (shape.seqs,), dev)
+    d_logp = _place(d_logp, "d_logp", f32[0], logp.shape, logp, dev)
     if entropy is not None:
-        d_entropy = _given_or_new(d_entropy, "d_entropy", (T,), f32, dev)
+        d_entropy = _place(d_entropy, "d_entropy", f32[0], logp.shape, logp, dev)
     elif d_entropy is not None:
         raise ValueError("d_entropy is given without an entropy")
-    _same_device(("logp", logp), ("weight", weight), ("d_logp", d_logp),
-                 ("d_entropy", d_entropy))
     _policy_check(policy_lib().gdn_policy_loss_bwd(
-        ctypes.byref(shape), _ptr(logp), _ptr(old_logp), _ptr(advantages), _ptr(ref_logp),
-        _ptr(mask), _ptr(cu_seqlens), _ptr(weight), d_loss, _ptr(d_logp), _ptr(d_entropy),
-        _stream(None)))
+        ctypes.byref(shape), *ptrs[:4], *ptrs[5:], w, d_loss, d_logp.data_ptr(),
+        _ptr(d_entropy), _raw_stream(dev)))
     return d_logp, d_entropy

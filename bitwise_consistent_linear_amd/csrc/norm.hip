@@ -101,16 +101,26 @@ __global__ __launch_bounds__(T *G) void norm_bwd_kernel(const NormArgs p) {
   const int64_t per = (p.rows + p.blocks - 1) / p.blocks;
   const int64_t lo = per * blockIdx.x, hi = lo + per < p.rows ? lo + per : p.rows;
   int par = 0;
-  for (int64_t r0 = lo; r0 < hi; r0 += G, par ^= 1) {
-    const bool live = r0 + g < hi;
-    const int64_t row = live ? r0 + g : hi - 1;
-    Vec8<XB> x[NV], dy[NV];
+  auto load = [&](Vec8<XB> (&x)[NV], Vec8<XB> (&dy)[NV], float &mean, float &rstd, int64_t row) {
+    if (row >= hi) row = hi - 1;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       load_row(x[j], p.x, row * p.x_stride, 8 * (j * T + t), D);
       load_row(dy[j], p.dy, row * p.dy_stride, 8 * (j * T + t), D);
     }
-    const float mean = layer ? p.mean[row] : 0.0f, rstd = p.rstd[row];
+    mean = layer ? p.mean[row] : 0.0f;
+    rstd = p.rstd[row];
+  };
+  Vec8<XB> x[NV], dy[NV];
+  float mean, rstd;
+  if (lo < hi) load(x, dy, mean, rstd, lo + g);
+  for (int64_t r0 = lo; r0 < hi; r0 += G, par ^= 1) {
+    const bool live = r0 + g < hi;
+    const int64_t row = r0 + g;
+    // the next row's loads are in flight under this one's sums
+    Vec8<XB> nx[NV], ndy[NV];
+    float nmean, nrstd;
+    load(nx, ndy, nmean, nrstd, row + G);
     float s1 = 0.0f, s2 = 0.0f;  // zeros past the row's end: dy is 0 there
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -125,8 +135,10 @@ __global__ __launch_bounds__(T *G) void norm_bwd_kernel(const NormArgs p) {
           db[j][e] += d;
         }
       }
-    const float c1 = row_sum<T>(s1, slot[par][0]) * inv;
-    const float c2 = layer ? row_sum<T>(s2, slot[par][1]) * inv : 0.0f;
+    float c1, c2;
+    row_sum2<T>(s1, s2, slot[par], c1, c2);
+    c1 *= inv;
+    c2 = layer ? c2 * inv : 0.0f;
     if (live) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -140,6 +152,13 @@ __global__ __launch_bounds__(T *G) void norm_bwd_kernel(const NormArgs p) {
         store_row<XB>(p.y, row * D, 8 * (j * T + t), D, o);
       }
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      x[j] = nx[j];
+      dy[j] = ndy[j];
+    }
+    mean = nmean;
+    rstd = nrstd;
   }
   // groups in ascending order
   auto gather = [&](float (&acc)[NV][8]) {
@@ -181,6 +200,7 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const NormArgs p) {
   float *out = blockIdx.y == 0 ? p.d_weight : p.d_bias;
   float s = 0.0f;
   if (col < D)
+#pragma unroll 8
     for (int b = wave; b < p.blocks; b += 16)
       s += p.partials[((int64_t)b * 2 + blockIdx.y) * D + col];
   part[wave][lane] = s;

@@ -114,6 +114,7 @@ gdn_status_t policy_shape(const char *fn, const gdn_policy_shape_t *sh, PolicyAr
   a.dual = sh->dual_clip;
   a.kl_coef = sh->kl_coef;
   a.entropy_coef = sh->entropy_coef;
+  a.span = policy_span(sh->tokens);
   a.slots = policy_slots(sh->tokens, sh->seqs);
   return GDN_OK;
 }

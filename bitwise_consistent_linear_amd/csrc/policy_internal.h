@@ -67,12 +67,13 @@ struct PolicyArgs {
   float *stats, *seq_weight;
   const float *weight;  // backward
   float *d_logp, *d_entropy;
-  double *partials;  // [5][slots]
-  double *seq_sums;  // [5][seqs]
-  int64_t slots;
+  double *partials;  // [slots][5]
+  double *seq_sums;  // [seqs][5]
+  int64_t slots, span;
 };
-// Slots of per-(block of tokens, sequence) sums: a block meets the sequences in order, so
-// block + sequence numbers the pairs that meet without a gap or a repeat.
+// Tokens of one wave of the forward, and slots of per-(span, sequence) sums: spans meet the
+// sequences in order, so span + sequence numbers the pairs that meet without a repeat.
+int64_t policy_span(int64_t tokens);
 int64_t policy_slots(int64_t tokens, int64_t seqs);
 hipError_t launch_policy_fwd(const PolicyArgs &args, hipStream_t stream);
 hipError_t launch_policy_bwd(const PolicyArgs &args, hipStream_t stream);

@@ -4,29 +4,60 @@
 // latency up to millions of tokens. The ratio is compared with the clip borders and the sums
 // are long, so the arithmetic is binary64 (its vector rate is far from the bound here).
 //
-// Forward: a wave takes 256 consecutive tokens, 4 per lane, and adds them up for each
-// sequence that meets them; a pair (block of tokens, sequence) has the slot block + sequence,
-// which no other pair has, since the pairs that meet form a staircase. One workgroup then adds
-// each sequence's slots in order, forms the weights and the loss. No atomics: the same bits
-// on every launch. Backward: elementwise, each token's sequence found from its wave's first.
+// Forward: a wave takes a span of consecutive tokens, 256 at a time and 4 per lane, and adds
+// them up for each sequence that meets the span; a pair (span, sequence) has the slot span +
+// sequence, which no other pair has, since the pairs that meet form a staircase. One workgroup
+// then adds each sequence's slots in order, forms the weights and the loss. No atomics: the
+// same bits on every launch. Backward: elementwise, each token's sequence found from its
+// wave's first.
+//
+// What a wave waits for is memory: it issues all loads of its tokens first, finds its first
+// sequence by a search of 64 lanes (one round of loads for 64 sequences, two for 4096), and
+// then holds the next 64 starts in its lanes.
 
 #include "policy_internal.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kSpan = 256, kPer = kSpan / 64;  // tokens per wave and per lane
-constexpr int kSums = 5;                       // pg, kl, entropy, cut, count
+constexpr int kChunk = 256, kPer = kChunk / 64;  // tokens of a wave at a time, and per lane
+constexpr int kSums = 5;                         // pg, kl, entropy, cut, count
+constexpr int64_t kMostSpans = 4096;             // longer batches have longer spans
+
+int64_t span_of(int64_t tokens) {  // tokens of a wave, by their number alone
+  const int64_t chunks = (tokens + kChunk - 1) / kChunk;
+  return kChunk * (chunks > kMostSpans ? (chunks + kMostSpans - 1) / kMostSpans : 1);
+}
+
+struct Inputs {  // of one token
+  float logp, old, adv, ref, entropy;
+  bool use;
+};
 
 struct Token {
   double ratio_adv, pg, kl, kl_slope;  // r A, -gain, exp(u) - u - 1, 1 - exp(u)
   bool moves;
 };
 
-__device__ __forceinline__ Token token_terms(const PolicyArgs &p, int64_t t) {
+// Tokens past `end` are not used; nothing of them is read.
+__device__ __forceinline__ Inputs load_token(const PolicyArgs &p, int64_t t, int64_t end,
+                                             bool want_entropy) {
+  Inputs v{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, false};
+  if (t < end) {
+    v.logp = p.logp[t];
+    v.old = p.old_logp[t];
+    v.adv = p.adv[t];
+    if (p.ref) v.ref = p.ref[t];
+    if (want_entropy && p.entropy) v.entropy = p.entropy[t];
+    v.use = !p.mask || p.mask[t];
+  }
+  return v;
+}
+
+__device__ __forceinline__ Token token_terms(const PolicyArgs &p, const Inputs &v) {
   Token o;
-  const double lp = p.logp[t], adv = p.adv[t];
-  const double r = exp(lp - (double)p.old_logp[t]);
+  const double lp = v.logp, adv = v.adv;
+  const double r = exp(lp - (double)v.old);
   const double clamped = r < p.lo ? p.lo : (r > p.hi ? p.hi : r);
   const double plain = r * adv, clipped = clamped * adv;
   o.ratio_adv = plain;
@@ -40,167 +71,255 @@ __device__ __forceinline__ Token token_terms(const PolicyArgs &p, int64_t t) {
   o.kl = 0.0;
   o.kl_slope = 0.0;
   if (p.ref) {
-    const double u = (double)p.ref[t] - lp, e = exp(u);
+    const double u = (double)v.ref - lp, e = exp(u);
     o.kl = e - u - 1.0;
     o.kl_slope = 1.0 - e;
   }
   return o;
 }
 
-// Start of sequence n, clamped to [0, tokens]; n == seqs gives the end of the last one.
+// Start of sequence n, clamped to [0, tokens]; n >= seqs gives the end of the last one.
 __device__ __forceinline__ int64_t start_of(const PolicyArgs &p, int64_t n) {
+  if (n > p.seqs) n = p.seqs;
   if (!p.cu) return n == 0 ? 0 : p.tokens;
   const int64_t v = p.cu[n];
   return v < 0 ? 0 : (v > p.tokens ? p.tokens : v);
 }
 
 // The last sequence that starts at or before token t (sequences of no tokens before it are
-// passed over): the one that holds t if any does.
+// passed over): the one that holds t if any does. Uniform over the wave; 64 starts a round.
 __device__ __forceinline__ int64_t find_seq(const PolicyArgs &p, int64_t t) {
-  int64_t lo = 0, hi = p.seqs - 1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) / 2;
-    if (start_of(p, mid) <= t)
-      lo = mid;
-    else
-      hi = mid - 1;
+  int64_t lo = 0, len = p.seqs;  // the answer is in [lo, lo + len)
+  while (len > 1) {
+    const int64_t step = (len + 63) / 64, at = lo + step * (int64_t)(threadIdx.x % 64);
+    const int below = __popcll(__ballot(at < lo + len && start_of(p, at) <= t));
+    const int64_t end = lo + len;
+    lo += step * (below > 0 ? below - 1 : 0);
+    len = end - lo < step ? end - lo : step;
   }
   return lo;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int s = 32; s > 0; s /= 2) v += __shfl_xor(v, s, 64);
-  return v;
+// A cursor over the sequences that meet a wave's tokens: lane i holds the start of sequence
+// first + i.
+struct Starts {
+  int64_t first;
+  int held;
+  __device__ __forceinline__ void load(const PolicyArgs &p, int64_t n) {
+    first = n;
+    held = (int)start_of(p, n + threadIdx.x % 64);
+  }
+  // start of sequence n in [first, first + 64)
+  __device__ __forceinline__ int64_t at(int64_t n) const {
+    return __builtin_amdgcn_readlane(held, __builtin_amdgcn_readfirstlane((int)(n - first)));
+  }
+};
+
+// v plus its neighbour's by a DPP move, 0 where there is none.
+template <int Ctrl, int Rows>
+__device__ __forceinline__ double plus_moved(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, Ctrl, Rows, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), Ctrl, Rows, 0xF, true);
+  return v + __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// Sum over the wave's lanes, in lane 63: runs of 2, 4, 8, 16 lanes, then the rows of 16.
+__device__ __forceinline__ double wave_total(double v) {
+  v = plus_moved<0x111, 0xF>(v);  // from one lane below in the row of 16, two, four, eight
+  v = plus_moved<0x112, 0xF>(v);
+  v = plus_moved<0x114, 0xF>(v);
+  v = plus_moved<0x118, 0xF>(v);
+  v = plus_moved<0x142, 0xA>(v);  // the row before, into rows 1 and 3
+  return plus_moved<0x143, 0xC>(v);  // the first two rows, into the others
 }
 
 __global__ __launch_bounds__(256) void policy_tokens_kernel(const PolicyArgs p) {
-  const int64_t block = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+  const int64_t block = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lane = threadIdx.x % 64;
-  const int64_t t0 = block * kSpan;
+  const int64_t t0 = block * p.span;
   if (t0 >= p.tokens) return;
-  const int64_t t1 = t0 + kSpan < p.tokens ? t0 + kSpan : p.tokens;
-  double v[kPer][4];
-  bool use[kPer];
+  const int64_t end = t0 + p.span < p.tokens ? t0 + p.span : p.tokens;
+  Inputs in[kPer];
+  auto load = [&](int64_t c0) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int64_t t = t0 + 64 * j + lane;
-    use[j] = t < t1 && (!p.mask || p.mask[t]);
+    for (int j = 0; j < kPer; ++j) in[j] = load_token(p, c0 + 64 * j + lane, end, true);
+  };
+  load(t0);
+  int64_t n = find_seq(p, t0);
+  Starts starts;
+  starts.load(p, n);
+  int64_t s = starts.at(n), e = starts.at(n + 1);
+  double sum[3] = {0.0, 0.0, 0.0};  // of the lane's tokens of sequence n so far
+  int cut = 0, count = 0;           // of the wave's
+  auto flush = [&]() {
+    double *out = p.partials + (block + n) * kSums;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[j][k] = 0.0;
-    if (use[j]) {
-      const Token o = token_terms(p, t);
-      v[j][0] = o.pg;
-      v[j][1] = o.kl;
-      v[j][2] = p.entropy ? (double)p.entropy[t] : 0.0;
-      v[j][3] = o.moves ? 0.0 : 1.0;
+    for (int k = 0; k < 3; ++k) {
+      const double v = wave_total(sum[k]);
+      if (lane == 63) out[k] = v;
+      sum[k] = 0.0;
+    }
+    if (lane == 63) {
+      out[3] = (double)cut;
+      out[4] = (double)count;
+    }
+    cut = count = 0;
+  };
+  for (int64_t c0 = t0; c0 < end; c0 += kChunk) {
+    const int64_t c1 = c0 + kChunk < end ? c0 + kChunk : end;
+    if (c0 > t0) load(c0);
+    Token o[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) o[j] = token_terms(p, in[j]);
+    // the sequences that meet [c0, c1), those that end in it put down
+    while (s < c1) {
+      if (e > s && e > c0) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int64_t t = c0 + 64 * j + lane;
+          const bool mine = in[j].use && t >= s && t < e;
+          if (mine) {
+            sum[0] += o[j].pg;
+            sum[1] += o[j].kl;
+            sum[2] += (double)in[j].entropy;
+          }
+          count += __popcll(__ballot(mine));
+          cut += __popcll(__ballot(mine && !o[j].moves));
+        }
+      }
+      if (e > c1) break;
+      if (e > s && e > t0) flush();
+      if (++n >= p.seqs) {
+        s = e = p.tokens;
+        break;
+      }
+      if (n - starts.first >= 63) starts.load(p, n);
+      s = e;
+      e = starts.at(n + 1);
     }
   }
-  // cu_seqlens that fall are clamped: a slot is written for every sequence from the first
-  // that meets the block on, within the slots there are
-  for (int64_t n = find_seq(p, t0); n < p.seqs; ++n) {
-    const int64_t s = start_of(p, n);
-    if (s >= t1) break;
-    const int64_t e = start_of(p, n + 1);
-    if (e <= s || e <= t0) continue;
-    double sum[kSums] = {0.0, 0.0, 0.0, 0.0, 0.0};
+  if (s < end && e > end) flush();
+}
+
+// Sums over a workgroup of 1024 threads, in every thread, waves in order.
+template <int K>
+__device__ __forceinline__ void group_total(double (&v)[K], double (&slot)[16][K]) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int64_t t = t0 + 64 * j + lane;
-      if (use[j] && t >= s && t < e) {
+  for (int k = 0; k < K; ++k) {
+    const double t = wave_total(v[k]);
+    if (threadIdx.x % 64 == 63) slot[threadIdx.x / 64][k] = t;
+  }
+  __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum[k] += v[j][k];
-        sum[4] += 1.0;
-      }
-    }
+  for (int k = 0; k < K; ++k) {
+    v[k] = slot[0][k];
 #pragma unroll
-    for (int k = 0; k < kSums; ++k) sum[k] = wave_sum(sum[k]);
-    if (lane == 0) {
-#pragma unroll
-      for (int k = 0; k < kSums; ++k) p.partials[k * p.slots + block + n] = sum[k];
-    }
+    for (int i = 1; i < 16; ++i) v[k] += slot[i][k];
   }
 }
 
-// Sum over a workgroup of 1024 threads, in every thread, waves in order.
-__device__ __forceinline__ double group_sum(double v, double *slot) {
-  v = wave_sum(v);
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) slot[threadIdx.x / 64] = v;
-  __syncthreads();
-  double s = slot[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) s += slot[i];
-  return s;
-}
+constexpr int kInLds = 512;  // sequences whose sums stay in LDS
 
 __global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p) {
-  __shared__ double slot[16];
+  __shared__ double held[kInLds * kSums], slot2[16][2], slot4[16][4];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  constexpr int kFew = 8;  // a sequence of at most so many slots is one thread's, else a wave's
-  double count = 0.0, live = 0.0;
-  for (int64_t n = tid; n < p.seqs; n += 1024) {
+  constexpr int kFew = 64;  // a sequence of at most so many slots is summed by single threads
+  double *sums = p.seqs <= kInLds ? held : p.seq_sums;  // [seqs][kSums]
+  auto slots = [&](int64_t n, int64_t &lo, int64_t &hi) {  // [lo, hi) of sequence n
     const int64_t s = start_of(p, n), e = start_of(p, n + 1);
-    const int64_t lo = s / kSpan + n, hi = e > s ? (e - 1) / kSpan + n : lo - 1;
-    if (hi - lo >= kFew) continue;
-    for (int k = 0; k < kSums; ++k) {
-      double v = 0.0;
-      for (int64_t i = lo; i <= hi; ++i) v += p.partials[k * p.slots + i];
-      p.seq_sums[k * p.seqs + n] = v;
-    }
+    lo = s / p.span + n;
+    hi = e > s ? (e - 1) / p.span + n + 1 : lo;
+  };
+  for (int64_t q = tid; q < p.seqs * kSums; q += 1024) {
+    int64_t lo, hi;
+    slots(q / kSums, lo, hi);
+    if (hi - lo > kFew) continue;
+    const double *part = p.partials + q % kSums;
+    double v = 0.0;
+#pragma unroll 8
+    for (int64_t i = lo; i < hi; ++i) v += part[i * kSums];
+    sums[q] = v;
   }
   for (int64_t n = wave; n < p.seqs; n += 16) {
-    const int64_t s = start_of(p, n), e = start_of(p, n + 1);
-    const int64_t lo = s / kSpan + n, hi = e > s ? (e - 1) / kSpan + n : lo - 1;
-    if (hi - lo < kFew) continue;
+    int64_t lo, hi;
+    slots(n, lo, hi);
+    if (hi - lo <= kFew) continue;
+    double v[kSums] = {};
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += 64)
+#pragma unroll
+      for (int k = 0; k < kSums; ++k) v[k] += p.partials[i * kSums + k];
+#pragma unroll
     for (int k = 0; k < kSums; ++k) {
-      double v = 0.0;
-      for (int64_t i = lo + lane; i <= hi; i += 64) v += p.partials[k * p.slots + i];
-      v = wave_sum(v);
-      if (lane == 0) p.seq_sums[k * p.seqs + n] = v;
+      v[k] = wave_total(v[k]);
+      if (lane == 63) sums[n * kSums + k] = v[k];
     }
   }
   __syncthreads();
+  double all[2] = {0.0, 0.0};  // scored tokens, sequences with any
   for (int64_t n = tid; n < p.seqs; n += 1024) {
-    const double c = p.seq_sums[4 * p.seqs + n];
-    count += c;
-    live += c > 0.0 ? 1.0 : 0.0;
+    const double c = sums[n * kSums + 4];
+    all[0] += c;
+    all[1] += c > 0.0 ? 1.0 : 0.0;
   }
-  count = group_sum(count, slot);
-  live = group_sum(live, slot);
+  group_total(all, slot2);
   double out[4] = {0.0, 0.0, 0.0, 0.0};
   for (int64_t n = tid; n < p.seqs; n += 1024) {
-    const double c = p.seq_sums[4 * p.seqs + n];
-    const double w = c > 0.0 ? (p.by_sequence ? 1.0 / (c * live) : 1.0 / count) : 0.0;
+    const double c = sums[n * kSums + 4];
+    const double w = c > 0.0 ? (p.by_sequence ? 1.0 / (c * all[1]) : 1.0 / all[0]) : 0.0;
     p.seq_weight[n] = (float)w;
     if (c > 0.0)
-      for (int k = 0; k < 4; ++k) out[k] += w * p.seq_sums[k * p.seqs + n];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) out[k] += w * sums[n * kSums + k];
   }
-  for (int k = 0; k < 4; ++k) out[k] = group_sum(out[k], slot);
+  group_total(out, slot4);
   if (tid == 0) {
     p.stats[0] = (float)(out[0] + p.kl_coef * out[1] - p.entropy_coef * out[2]);
+#pragma unroll
     for (int k = 0; k < 4; ++k) p.stats[k + 1] = (float)out[k];
   }
 }
 
 __global__ __launch_bounds__(256) void policy_grad_kernel(const PolicyArgs p) {
-  const int64_t block = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+  const int64_t block = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lane = threadIdx.x % 64;
-  const int64_t t0 = block * kSpan;
+  const int64_t t0 = block * kChunk;
   if (t0 >= p.tokens) return;
+  const int64_t end = t0 + kChunk < p.tokens ? t0 + kChunk : p.tokens;
+  Inputs in[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) in[j] = load_token(p, t0 + 64 * j + lane, end, false);
   int64_t n = find_seq(p, t0);
+  Starts starts;
+  starts.load(p, n);
+  float weight = n + lane < p.seqs ? p.weight[n + lane] : 0.0f;  // of sequence first + lane
+  float w[kPer] = {};
+  for (int64_t s = starts.at(n); n < p.seqs && s < end; ++n) {
+    if (n - starts.first >= 63) {
+      starts.load(p, n);
+      weight = n + lane < p.seqs ? p.weight[n + lane] : 0.0f;
+    }
+    const int64_t e = starts.at(n + 1);
+    const float wn = __int_as_float(__builtin_amdgcn_readlane(
+        __float_as_int(weight), __builtin_amdgcn_readfirstlane((int)(n - starts.first))));
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t t = t0 + 64 * j + lane;
+      if (t >= s && t < e) w[j] = wn;
+    }
+    s = e;
+  }
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int64_t t = t0 + 64 * j + lane;
-    if (t >= p.tokens) break;
-    while (n + 1 < p.seqs && start_of(p, n + 1) <= t) ++n;
-    const bool in = t >= start_of(p, n) && t < start_of(p, n + 1);
+    if (t >= end) break;
     float dl = 0.0f, de = 0.0f;
-    if (in && (!p.mask || p.mask[t])) {
-      const Token o = token_terms(p, t);
-      const double w = (double)p.weight[n] * p.d_loss;
-      dl = (float)(w * (p.kl_coef * o.kl_slope - (o.moves ? o.ratio_adv : 0.0)));
-      de = (float)(-w * p.entropy_coef);
+    if (in[j].use && w[j] != 0.0f) {  // a scored token of a sequence has a weight
+      const Token o = token_terms(p, in[j]);
+      const double v = (double)w[j] * p.d_loss;
+      dl = (float)(v * (p.kl_coef * o.kl_slope - (o.moves ? o.ratio_adv : 0.0)));
+      de = (float)(-v * p.entropy_coef);
     }
     p.d_logp[t] = dl;
     if (p.d_entropy) p.d_entropy[t] = de;
@@ -216,12 +335,17 @@ hipError_t run(const void *fn, const PolicyArgs &a, int64_t grid, int threads,
 
 }  // namespace
 
-int64_t policy_slots(int64_t tokens, int64_t seqs) { return (tokens + kSpan - 1) / kSpan + seqs; }
+int64_t policy_span(int64_t tokens) { return span_of(tokens); }
+
+int64_t policy_slots(int64_t tokens, int64_t seqs) {
+  const int64_t span = span_of(tokens);
+  return (tokens + span - 1) / span + seqs;
+}
 
 hipError_t launch_policy_fwd(const PolicyArgs &a, hipStream_t stream) {
-  const int64_t blocks = (a.tokens + kSpan - 1) / kSpan;
-  if (blocks > 0) {
-    const hipError_t e = run((const void *)policy_tokens_kernel, a, (blocks + 3) / 4, 256, stream);
+  const int64_t spans = (a.tokens + a.span - 1) / a.span;
+  if (spans > 0) {
+    const hipError_t e = run((const void *)policy_tokens_kernel, a, (spans + 3) / 4, 256, stream);
     if (e != hipSuccess) return e;
   }
   return run((const void *)policy_finish_kernel, a, 1, 1024, stream);
@@ -229,7 +353,7 @@ hipError_t launch_policy_fwd(const PolicyArgs &a, hipStream_t stream) {
 
 hipError_t launch_policy_bwd(const PolicyArgs &a, hipStream_t stream) {
   if (a.tokens == 0) return hipSuccess;
-  const int64_t blocks = (a.tokens + kSpan - 1) / kSpan;
+  const int64_t blocks = (a.tokens + kChunk - 1) / kChunk;
   return run((const void *)policy_grad_kernel, a, (blocks + 3) / 4, 256, stream);
 }
 

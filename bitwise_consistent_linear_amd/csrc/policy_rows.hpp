@@ -141,4 +141,27 @@ __device__ __forceinline__ float row_sum(float v, float *slot) {
   }
 }
 
+// Two such sums at once, through one barrier.
+template <int T, int N>
+__device__ __forceinline__ void row_sum2(float a, float b, float (&slot)[2][N], float &sa,
+                                         float &sb) {
+  sa = lane_sum<(T < 64 ? T : 64)>(a);
+  sb = lane_sum<(T < 64 ? T : 64)>(b);
+  if constexpr (T > 64) {
+    const int wave = threadIdx.x / 64, first = wave / (T / 64) * (T / 64);
+    if (threadIdx.x % 64 == 0) {
+      slot[0][wave] = sa;
+      slot[1][wave] = sb;
+    }
+    __syncthreads();
+    sa = slot[0][first];
+    sb = slot[1][first];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) {
+      sa += slot[0][first + i];
+      sb += slot[1][first + i];
+    }
+  }
+}
+
 }  // namespace gdn

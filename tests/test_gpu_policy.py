@@ -463,6 +463,29 @@ def test_policy_without_mask_and_offsets():
     assert stats.tolist() == [0.0] * 5 and weight.tolist() == [0.0]
 
 
+def test_policy_long_batch():
+    """More tokens than one chunk for each of the most spans: a wave walks over several chunks
+    and carries a sequence from one to the next."""
+    lengths = [700001, 3, 0, 255, 600000, 1]
+    cu, logp, old, adv, ref, ent, mask = policy_inputs("x", lengths, 9)
+    mask &= np.random.default_rng(10).random(len(mask)) < 0.02
+    mask[-1] = True
+    up = lambda v: torch.from_numpy(v).to(DEV)  # noqa: E731
+    for reduction in ("token", "sequence"):
+        kw = dict(ref_logp=up(ref), entropy=up(ent), mask=up(mask), cu_seqlens=up(cu),
+                  kl_coef=0.05, entropy_coef=0.01, reduction=reduction)
+        stats, weight = api.policy_loss_fwd(up(logp), up(old), up(adv), **kw)
+        dl, de = api.policy_loss_bwd(up(logp), up(old), up(adv), weight, **kw)
+        ws, ww, wl, we = R.policy(logp, old, adv, ref, ent, mask, cu, 0.2, 0.2, 0.0, 0.05, 0.01,
+                                  reduction)
+        size = np.abs(ws[1:]).max() + 1.0
+        R.check(stats, ws, torch.from_numpy(np.abs(ws) * R.POLICY_REL + R.POLICY_ABS * size),
+                "stats")
+        R.check(weight, ww, torch.from_numpy(np.abs(ww) * R.U), "weight")
+        R.check(dl, wl, torch.from_numpy(np.abs(wl) * R.POLICY_REL + R.POLICY_ABS * 1e-3), "d_logp")
+        R.check(de, we, torch.from_numpy(np.abs(we) * R.POLICY_REL), "d_entropy")
+
+
 def test_policy_at_the_clip_borders():
     """Ratios a rounding away from the borders on either side: binary64 tells them apart as
     the definition does."""
