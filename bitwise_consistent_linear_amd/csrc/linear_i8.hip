@@ -207,7 +207,7 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
       for (int r = 0; r < 4; ++r)
         if (n + r < p.n) {
           if (YB)
-            static_cast<uint16_t *>(p.y)[m * p.n + n + r] = (uint16_t)to_bf16(v[r]);
+            static_cast<uint16_t *>(p.y)[m * p.n + n + r] = to_bf16(v[r]);
           else
             static_cast<float *>(p.y)[m * p.n + n + r] = v[r];
         }
@@ -390,7 +390,7 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
       int8_t *at = own + (r * kChunks + c) * 16;
       if (YB)
         *reinterpret_cast<uint2 *>(at + n % kChunk * 2) =
-            make_uint2(to_bf16(v[0]) | to_bf16(v[1]) << 16, to_bf16(v[2]) | to_bf16(v[3]) << 16);
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
       else
         *reinterpret_cast<f32x4 *>(at) = v;
     }

@@ -1,11 +1,12 @@
 // Layer norm and root-mean-square norm, forward and backward, on gfx950.
 //
 // Both are bound by memory: the forward reads x and writes y, the backward reads x and dy and
-// writes dx. T threads hold a row in registers, 8 consecutive values at a time, so the
-// statistics take two passes over registers and one over memory: the mean first, then the
-// sum of squared distances from it, which keeps the variance exact to a few roundings where
-// a sum of squares less the squared mean would cancel. A workgroup walks over several rows
-// with weight and bias in registers.
+// writes dx. A row is held in registers, eight consecutive values (times NV) per thread, by as
+// many waves as it fills (or by a row of 16 lanes up to 128 values), so the statistics take
+// two passes over registers and one over memory: the mean first, then the sum of squared
+// distances from it, which keeps the variance exact to a few roundings where a sum of squares
+// less the squared mean would cancel. A workgroup walks over rows with the weight (and bias)
+// in registers, the next row's loads in flight under the current one.
 //
 // The reduction order depends on the width alone, so a row has the same bits in every batch.
 
@@ -16,12 +17,20 @@ namespace gdn {
 namespace {
 
 constexpr int kFwdGrid = 2048;  // workgroups of a forward launch; more rows are walked over
+constexpr int kBwdGrid = 256;   // blocks of rows of a backward launch
 
-template <bool XB, bool WB, int T, int NV>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(const NormArgs p) {
-  constexpr int kThreads = T < 256 ? 256 : T, RPW = kThreads / T;
-  __shared__ float slot[2][kThreads / 64];
-  const int t = threadIdx.x % T, D = p.width;
+// How a row is split: threads of one row, rows at a time, threads of a workgroup.
+struct Split {
+  int row_threads, groups, nv;
+  int threads() const { return row_threads * groups; }
+};
+
+// G: lanes that share a row, 16 or 64 (then p.row_threads / 64 waves do).
+template <bool XB, bool WB, int G, int NV>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(const NormArgs p) {
+  __shared__ float slot[2][1][16];
+  const int T = G == 64 ? p.row_threads : G, groups = (int)blockDim.x / T;
+  const int t = threadIdx.x % T, g = threadIdx.x / T, D = p.width;
   const bool layer = p.layer;
   const float inv = 1.0f / (float)D;
   Vec8<WB> w[NV], b[NV];
@@ -33,38 +42,42 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(const NormA
     else
       b[j].zero();
   }
-  // one group of T threads per row; the rows past the end repeat the last one, unwritten
-  for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < p.rows; r0 += (int64_t)gridDim.x * RPW) {
-    int64_t row = r0 + threadIdx.x / T;
-    const bool live = row < p.rows;
-    if (!live) row = p.rows - 1;
-    Vec8<XB> x[NV];
+  // rows past the end repeat the last one, unwritten
+  auto load = [&](Vec8<XB> (&x)[NV], int64_t row) {
+    if (row >= p.rows) row = p.rows - 1;
 #pragma unroll
     for (int j = 0; j < NV; ++j) load_row(x[j], p.x, row * p.x_stride, 8 * (j * T + t), D);
-    float mean = 0.0f;
+  };
+  const int64_t step = (int64_t)gridDim.x * groups;
+  Vec8<XB> x[NV], next[NV];
+  load(x, (int64_t)blockIdx.x * groups + g);
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step) {
+    const int64_t row = r0 + g;
+    if (r0 + step < p.rows) load(next, row + step);
+    float mean[1] = {0.0f};
     if (layer) {
-      float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += x[j].get(e);
-      mean = row_sum<T>(s, slot[0]) * inv;
+        for (int e = 0; e < 8; ++e) mean[0] += x[j].get(e);
+      row_sums<G>(mean, T / 64, slot[0]);
+      mean[0] *= inv;
     }
-    float q = 0.0f;
+    float var[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int left = D - 8 * (j * T + t);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = e < left ? x[j].get(e) - mean : 0.0f;
-        q = fmaf(d, d, q);
+        const float d = e < left ? x[j].get(e) - mean[0] : 0.0f;
+        var[0] = fmaf(d, d, var[0]);
       }
     }
-    const float var = row_sum<T>(q, slot[1]) * inv;
-    const float rstd = 1.0f / sqrtf(var + p.eps);
-    if (live) {
+    row_sums<G>(var, T / 64, slot[1]);
+    const float rstd = 1.0f / sqrtf(fmaf(var[0], inv, p.eps));
+    if (row < p.rows) {
       if (t == 0) {
-        if (layer) p.mean[row] = mean;
+        if (layer) p.mean[row] = mean[0];
         p.rstd[row] = rstd;
       }
 #pragma unroll
@@ -72,111 +85,110 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(const NormA
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          y[e] = fmaf((x[j].get(e) - mean) * rstd, w[j].get(e), b[j].get(e));
+          y[e] = fmaf((x[j].get(e) - mean[0]) * rstd, w[j].get(e), b[j].get(e));
         store_row<XB>(p.y, row * D, 8 * (j * T + t), D, y);
       }
     }
-    // rms writes slot[1] again without a barrier of the mean's in between
+    // rms writes slot[1] again without the mean's barrier in between
     if (!layer && T > 64) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) x[j] = next[j];
   }
 }
 
 // Backward of one block of rows: dx, and the block's sums of dy * xh and of dy for every
-// column. G groups of T threads take rows in turn; a thread keeps its columns' sums.
-template <bool XB, bool WB, int T, int NV, int G>
-__global__ __launch_bounds__(T *G) void norm_bwd_kernel(const NormArgs p) {
-  __shared__ float slot[2][2][T * G / 64];
-  __shared__ float share[G > 1 ? T * NV * 8 : 1];
+// column. Groups of T threads take rows in turn; a thread keeps its columns' sums.
+template <bool XB, bool WB, int G, int NV>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
+  __shared__ float slot[2][2][16];
+  __shared__ float share[4096];  // the columns of a group, where there are several
+  const int T = G == 64 ? p.row_threads : G, groups = (int)blockDim.x / T;
   const int t = threadIdx.x % T, g = threadIdx.x / T, D = p.width;
   const bool layer = p.layer;
   const float inv = 1.0f / (float)D;
   Vec8<WB> w[NV];
   float dw[NV][8], db[NV][8];
+  constexpr bool kAhead = NV == 1;  // with NV = 2 the next row would not fit the registers
+  auto load_weight = [&]() {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    load_row(w[j], p.weight, 0, 8 * (j * T + t), D);
+    for (int j = 0; j < NV; ++j) load_row(w[j], p.weight, 0, 8 * (j * T + t), D);
+  };
+  if (kAhead) load_weight();
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[j][e] = db[j][e] = 0.0f;
-  }
-  const int64_t per = (p.rows + p.blocks - 1) / p.blocks;
-  const int64_t lo = per * blockIdx.x, hi = lo + per < p.rows ? lo + per : p.rows;
-  int par = 0;
-  auto load = [&](Vec8<XB> (&x)[NV], Vec8<XB> (&dy)[NV], float &mean, float &rstd, int64_t row) {
+  const int64_t lo = (int64_t)p.block_rows * blockIdx.x;
+  const int64_t hi = lo + p.block_rows < p.rows ? lo + p.block_rows : p.rows;
+  struct Row {
+    Vec8<XB> x[NV], dy[NV];
+    float mean, rstd;
+  };
+  auto load = [&](Row &r, int64_t row) {  // past the end the last one again, unused
     if (row >= hi) row = hi - 1;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_row(x[j], p.x, row * p.x_stride, 8 * (j * T + t), D);
-      load_row(dy[j], p.dy, row * p.dy_stride, 8 * (j * T + t), D);
+      load_row(r.x[j], p.x, row * p.x_stride, 8 * (j * T + t), D);
+      load_row(r.dy[j], p.dy, row * p.dy_stride, 8 * (j * T + t), D);
     }
-    mean = layer ? p.mean[row] : 0.0f;
-    rstd = p.rstd[row];
+    r.mean = layer ? p.mean[row] : 0.0f;
+    r.rstd = p.rstd[row];
   };
-  Vec8<XB> x[NV], dy[NV];
-  float mean, rstd;
-  if (lo < hi) load(x, dy, mean, rstd, lo + g);
-  for (int64_t r0 = lo; r0 < hi; r0 += G, par ^= 1) {
-    const bool live = r0 + g < hi;
+  Row cur, next;
+  if (kAhead && lo < hi) load(cur, lo + g);
+  int par = 0;
+  for (int64_t r0 = lo; r0 < hi; r0 += groups, par ^= 1) {
     const int64_t row = r0 + g;
-    // the next row's loads are in flight under this one's sums
-    Vec8<XB> nx[NV], ndy[NV];
-    float nmean, nrstd;
-    load(nx, ndy, nmean, nrstd, row + G);
-    float s1 = 0.0f, s2 = 0.0f;  // zeros past the row's end: dy is 0 there
+    if (kAhead) {
+      load(next, row + groups);
+    } else {
+      load(cur, row);
+      load_weight();
+    }
+    float c[2] = {0.0f, 0.0f};  // sums of g xh and of g; dy is 0 past the row's end
+    float xh[NV][8], gw[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xh = (x[j].get(e) - mean) * rstd, d = dy[j].get(e);
-        const float gw = d * w[j].get(e);
-        s1 = fmaf(gw, xh, s1);
-        s2 += gw;
-        if (live) {
-          dw[j][e] = fmaf(d, xh, dw[j][e]);
+        const float d = cur.dy[j].get(e);
+        xh[j][e] = (cur.x[j].get(e) - cur.mean) * cur.rstd;
+        gw[j][e] = d * w[j].get(e);
+        c[0] = fmaf(gw[j][e], xh[j][e], c[0]);
+        c[1] += gw[j][e];
+        if (row < hi) {
+          dw[j][e] = fmaf(d, xh[j][e], dw[j][e]);
           db[j][e] += d;
         }
       }
-    float c1, c2;
-    row_sum2<T>(s1, s2, slot[par], c1, c2);
-    c1 *= inv;
-    c2 = layer ? c2 * inv : 0.0f;
-    if (live) {
+    row_sums<G>(c, T / 64, slot[par]);
+    const float c1 = c[0] * inv, c2 = layer ? c[1] * inv : 0.0f;
+    if (row < hi) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xh = (x[j].get(e) - mean) * rstd;
-          const float gw = dy[j].get(e) * w[j].get(e);
-          o[e] = (fmaf(-xh, c1, gw) - c2) * rstd;
-        }
+        for (int e = 0; e < 8; ++e) o[e] = (fmaf(-xh[j][e], c1, gw[j][e]) - c2) * cur.rstd;
         store_row<XB>(p.y, row * D, 8 * (j * T + t), D, o);
       }
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      x[j] = nx[j];
-      dy[j] = ndy[j];
-    }
-    mean = nmean;
-    rstd = nrstd;
+    if (kAhead) cur = next;
   }
   // groups in ascending order
   auto gather = [&](float (&acc)[NV][8]) {
-    if constexpr (G > 1) {
-      for (int k = 1; k < G; ++k) {
-        if (g == k)
+    for (int k = 1; k < groups; ++k) {
+      if (g == k)
 #pragma unroll
-          for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) share[(j * T + t) * 8 + e] = acc[j][e];
-        __syncthreads();
-        if (g == 0)
+          for (int e = 0; e < 8; ++e) share[(j * 8 + e) * T + t] = acc[j][e];
+      __syncthreads();
+      if (g == 0)
 #pragma unroll
-          for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[j][e] += share[(j * T + t) * 8 + e];
-        __syncthreads();
-      }
+          for (int e = 0; e < 8; ++e) acc[j][e] += share[(j * 8 + e) * T + t];
+      __syncthreads();
     }
   };
   gather(dw);
@@ -212,20 +224,31 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const NormArgs p) {
   }
 }
 
-template <int T, int NV>
+template <int G, int NV>
 const void *fwd_fn(const NormArgs &a) {
-  return a.x_bf16 ? (a.w_bf16 ? (const void *)norm_fwd_kernel<true, true, T, NV>
-                              : (const void *)norm_fwd_kernel<true, false, T, NV>)
-                  : (a.w_bf16 ? (const void *)norm_fwd_kernel<false, true, T, NV>
-                              : (const void *)norm_fwd_kernel<false, false, T, NV>);
+  return a.x_bf16 ? (a.w_bf16 ? (const void *)norm_fwd_kernel<true, true, G, NV>
+                              : (const void *)norm_fwd_kernel<true, false, G, NV>)
+                  : (a.w_bf16 ? (const void *)norm_fwd_kernel<false, true, G, NV>
+                              : (const void *)norm_fwd_kernel<false, false, G, NV>);
 }
 
-template <int T, int NV, int G>
+template <int G, int NV>
 const void *bwd_fn(const NormArgs &a) {
-  return a.x_bf16 ? (a.w_bf16 ? (const void *)norm_bwd_kernel<true, true, T, NV, G>
-                              : (const void *)norm_bwd_kernel<true, false, T, NV, G>)
-                  : (a.w_bf16 ? (const void *)norm_bwd_kernel<false, true, T, NV, G>
-                              : (const void *)norm_bwd_kernel<false, false, T, NV, G>);
+  return a.x_bf16 ? (a.w_bf16 ? (const void *)norm_bwd_kernel<true, true, G, NV>
+                              : (const void *)norm_bwd_kernel<true, false, G, NV>)
+                  : (a.w_bf16 ? (const void *)norm_bwd_kernel<false, true, G, NV>
+                              : (const void *)norm_bwd_kernel<false, false, G, NV>);
+}
+
+// Eight values a thread up to 8192, sixteen above; a row of 16 lanes for 128 values and less.
+// `most` threads of a workgroup where a row needs fewer.
+Split split_of(int width, int most) {
+  Split s;
+  s.nv = width <= 8192 ? 1 : 2;
+  const int vecs = (width + 8 * s.nv - 1) / (8 * s.nv);
+  s.row_threads = vecs <= 16 ? 16 : (vecs + 63) / 64 * 64;
+  s.groups = s.row_threads >= most ? 1 : most / s.row_threads;
+  return s;
 }
 
 hipError_t run(const void *fn, const NormArgs &a, dim3 grid, int threads, hipStream_t stream) {
@@ -234,40 +257,44 @@ hipError_t run(const void *fn, const NormArgs &a, dim3 grid, int threads, hipStr
   return hipLaunchKernel(fn, grid, dim3(threads), kargs, 0, stream);
 }
 
+// Rows of a backward block, by rows and width alone (the same bits on any device). More
+// blocks than compute units only add partial sums to write and read: 16384 x 4096 bf16 takes
+// 88.6 us with 256 blocks of two rows at a time, 93.0 with 512 and 99.9 with 1024.
+int64_t block_rows_of(int64_t rows, int32_t width) {
+  const int groups = split_of(width, 1024).groups;
+  const int64_t per = (rows + kBwdGrid - 1) / kBwdGrid;
+  return (per + groups - 1) / groups * groups;
+}
+
 }  // namespace
 
-// Blocks of rows of a backward launch, by rows and width alone (the same bits on any device).
 int norm_bwd_blocks(int64_t rows, int32_t width) {
-  const int64_t most = 512;
-  return (int)(rows < most ? (rows < 1 ? 1 : rows) : most);
+  if (rows == 0) return 1;  // a block that writes zeros
+  const int64_t per = block_rows_of(rows, width);
+  return (int)((rows + per - 1) / per);
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  int T, threads = 256;
-  const void *fn;
-  if (a.width <= 128) { T = 16; fn = fwd_fn<16, 1>(a); }
-  else if (a.width <= 512) { T = 64; fn = fwd_fn<64, 1>(a); }
-  else if (a.width <= 2048) { T = 64; fn = fwd_fn<64, 4>(a); }
-  else if (a.width <= 8192) { T = 256; fn = fwd_fn<256, 4>(a); }
-  else { T = threads = 1024; fn = fwd_fn<1024, 2>(a); }
-  const int64_t need = (a.rows + threads / T - 1) / (threads / T);
-  return run(fn, a, dim3((unsigned)(need < kFwdGrid ? need : kFwdGrid)), threads, stream);
+  const Split s = split_of(a.width, 256);
+  NormArgs args = a;
+  args.row_threads = s.row_threads;
+  const void *fn = s.row_threads == 16 ? fwd_fn<16, 1>(a) : s.nv == 1 ? fwd_fn<64, 1>(a)
+                                                                      : fwd_fn<64, 2>(a);
+  const int64_t need = (a.rows + s.groups - 1) / s.groups;
+  return run(fn, args, dim3((unsigned)(need < kFwdGrid ? need : kFwdGrid)), s.threads(), stream);
 }
 
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream) {
-  int threads;
-  const void *fn;
-  if (a.width <= 128) { threads = 256; fn = bwd_fn<16, 1, 16>(a); }
-  else if (a.width <= 512) { threads = 256; fn = bwd_fn<64, 1, 4>(a); }
-  else if (a.width <= 2048) { threads = 256; fn = bwd_fn<256, 1, 1>(a); }
-  else if (a.width <= 4096) { threads = 512; fn = bwd_fn<512, 1, 1>(a); }
-  else if (a.width <= 8192) { threads = 1024; fn = bwd_fn<1024, 1, 1>(a); }
-  else { threads = 1024; fn = bwd_fn<1024, 2, 1>(a); }
-  // rows == 0: one block that writes zeros
-  hipError_t e = run(fn, a, dim3((unsigned)a.blocks), threads, stream);
+  const Split s = split_of(a.width, 1024);
+  NormArgs args = a;
+  args.row_threads = s.row_threads;
+  args.block_rows = (int32_t)block_rows_of(a.rows, a.width);
+  const void *fn = s.row_threads == 16 ? bwd_fn<16, 1>(a) : s.nv == 1 ? bwd_fn<64, 1>(a)
+                                                                      : bwd_fn<64, 2>(a);
+  hipError_t e = run(fn, args, dim3((unsigned)a.blocks), s.threads(), stream);
   if (e != hipSuccess) return e;
-  return run((const void *)norm_columns_kernel, a,
+  return run((const void *)norm_columns_kernel, args,
              dim3((unsigned)((a.width + 63) / 64), a.d_bias ? 2 : 1), 1024, stream);
 }
 

@@ -16,12 +16,13 @@ using f32x4_a4 = float __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Round to nearest even; NaN stays NaN.
-__device__ __forceinline__ uint32_t to_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+// Two values rounded to bf16 (to nearest even; one instruction on gfx950), `a` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+  using f32x2 = float __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
+__device__ __forceinline__ uint16_t to_bf16(float f) { return (uint16_t)pack_bf16(f, 0.0f); }
 
 // Eight consecutive values as loaded (bf16 bits or binary32).
 template <bool BF16>
@@ -50,7 +51,7 @@ struct Vec8<true> {
   __device__ __forceinline__ static void store(void *base, int64_t idx, const float (&v)[8]) {
     u32x4_a2 o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = to_bf16(v[2 * i]) | (to_bf16(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<u32x4_a2 *>(static_cast<uint16_t *>(base) + idx) = o;
   }
   __device__ __forceinline__ static void store_part(void *base, int64_t idx, const float (&v)[8],
@@ -58,7 +59,7 @@ struct Vec8<true> {
     uint16_t *b = static_cast<uint16_t *>(base) + idx;
 #pragma unroll
     for (int e = 0; e < 7; ++e)
-      if (e < n) b[e] = (uint16_t)to_bf16(v[e]);
+      if (e < n) b[e] = to_bf16(v[e]);
   }
 };
 
@@ -113,54 +114,56 @@ __device__ __forceinline__ void store_row(void *base, int64_t row_off, int64_t c
     Vec8<BF16>::store_part(base, row_off + col, v, (int)(width - col));
 }
 
-// Sum over groups of G neighbouring lanes (a power of two up to 64), in every lane.
+// A lane's neighbour n places on in its row of 16 lanes, around the row's end.
+template <int N>
+__device__ __forceinline__ float rotated(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 | N, 0xF, 0xF, true));
+}
+
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Sum over each row of 16 lanes or over the wave's 64, in every lane (pairs are added in an
+// order that all lanes share up to commutation, so all have the same bits).
 template <int G>
 __device__ __forceinline__ float lane_sum(float v) {
-#pragma unroll
-  for (int s = G / 2; s > 0; s /= 2) v += __shfl_xor(v, s, 64);
+  static_assert(G == 16 || G == 64, "a row of lanes or the wave");
+  v += rotated<8>(v);
+  v += rotated<4>(v);
+  v += rotated<2>(v);
+  v += rotated<1>(v);
+  if constexpr (G == 64) v = (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
   return v;
 }
 
-// Sum over the T threads that share a row, in every one of them: the lanes of a wave by
-// lane_sum, waves in ascending order through `slot` (one float per wave of the workgroup,
-// which must not be written again before the workgroup's next barrier after this one).
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float *slot) {
-  if constexpr (T <= 64) {
-    return lane_sum<T>(v);
-  } else {
-    v = lane_sum<64>(v);
-    const int wave = threadIdx.x / 64;
-    if (threadIdx.x % 64 == 0) slot[wave] = v;
-    __syncthreads();
-    const int first = wave / (T / 64) * (T / 64);
-    float s = slot[first];
-#pragma unroll
-    for (int i = 1; i < T / 64; ++i) s += slot[first + i];
-    return s;
-  }
+// Maximum over the wave's lanes, in every lane (a NaN is passed over).
+__device__ __forceinline__ float lane_max(float v) {
+  v = fmaxf(v, rotated<8>(v));
+  v = fmaxf(v, rotated<4>(v));
+  v = fmaxf(v, rotated<2>(v));
+  v = fmaxf(v, rotated<1>(v));
+  return fmaxf(fmaxf(lane_of(v, 0), lane_of(v, 16)), fmaxf(lane_of(v, 32), lane_of(v, 48)));
 }
 
-// Two such sums at once, through one barrier.
-template <int T, int N>
-__device__ __forceinline__ void row_sum2(float a, float b, float (&slot)[2][N], float &sa,
-                                         float &sb) {
-  sa = lane_sum<(T < 64 ? T : 64)>(a);
-  sb = lane_sum<(T < 64 ? T : 64)>(b);
-  if constexpr (T > 64) {
-    const int wave = threadIdx.x / 64, first = wave / (T / 64) * (T / 64);
-    if (threadIdx.x % 64 == 0) {
-      slot[0][wave] = sa;
-      slot[1][wave] = sb;
-    }
-    __syncthreads();
-    sa = slot[0][first];
-    sb = slot[1][first];
+// K sums at once over the `waves` waves that share a row (the wave's alone, or a row of 16
+// lanes, for G lanes a row): lanes first, then the waves in ascending order through `slot`,
+// which must not be written again before the workgroup's next barrier after this one.
+template <int G, int K, int N>
+__device__ __forceinline__ void row_sums(float (&v)[K], int waves, float (&slot)[K][N]) {
 #pragma unroll
-    for (int i = 1; i < T / 64; ++i) {
-      sa += slot[0][first + i];
-      sb += slot[1][first + i];
-    }
+  for (int k = 0; k < K; ++k) v[k] = lane_sum<G>(v[k]);
+  if (G < 64 || waves == 1) return;
+  const int wave = threadIdx.x / 64, first = wave / waves * waves;
+  if (threadIdx.x % 64 == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) slot[k][wave] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    v[k] = slot[k][first];
+    for (int i = 1; i < waves; ++i) v[k] += slot[k][first + i];
   }
 }
 
