@@ -2,8 +2,8 @@
 //
 // Forward: bound by the one read of the logits. A workgroup takes a row; each thread keeps a
 // running maximum m of its logits and, relative to it, the sums s of the exponentials and t
-// of the exponentials times the differences; the threads' triples are then merged over lanes
-// and waves in a fixed order. lse = scale m + log s, logp = scale (v[id] - m) - log s,
+// of the exponentials times the differences, the next tile's loads in flight under this one's
+// arithmetic; the threads' triples are then merged over lanes and waves in a fixed order. lse = scale m + log s, logp = scale (v[id] - m) - log s,
 // entropy = log s - scale t / s: differences from the maximum keep what differences of large
 // logits would lose. The order depends on the vocabulary alone, so a row has the same bits
 // in any batch.
@@ -46,12 +46,11 @@ __device__ __forceinline__ void rebase(Softmax &a, float to, float c) {
   a.m = to;
 }
 
-__device__ __forceinline__ Softmax merge(Softmax a, Softmax b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  rebase(a, m, c);
-  rebase(b, m, c);
-  a.s += b.s;
-  a.t += b.t;
+// The wave's lanes together, in every lane.
+__device__ __forceinline__ Softmax over_lanes(Softmax a, float c) {
+  rebase(a, lane_max(a.m), c);
+  a.s = lane_sum<64>(a.s);
+  a.t = lane_sum<64>(a.t);
   return a;
 }
 
@@ -67,12 +66,13 @@ __device__ __forceinline__ void load_logits(Vec8<B16> &v, const void *base, int6
   }
 }
 
-constexpr int kFwdThreads = 512, kFwdVecs = 4;
+constexpr int kFwdVecs = 4;
 
 template <bool B16, bool ENT>
-__global__ __launch_bounds__(kFwdThreads) void logprob_fwd_kernel(const LogprobArgs p) {
-  __shared__ Softmax part[kFwdThreads / 64];
+__global__ __launch_bounds__(512) void logprob_fwd_kernel(const LogprobArgs p) {
+  __shared__ Softmax part[8];
   const int64_t row = blockIdx.x, V = p.vocab;
+  const int threads = blockDim.x, lane = threadIdx.x % 64, waves = threads / 64;
   const int64_t id = id_of(p, row);
   if (id < 0 || id >= V) {
     if (threadIdx.x == 0) {
@@ -83,12 +83,19 @@ __global__ __launch_bounds__(kFwdThreads) void logprob_fwd_kernel(const LogprobA
   }
   const int64_t off = row * p.stride;
   const float c = p.scale_log2e;
-  Softmax a{kLowest, 0.0f, 0.0f};
-  for (int64_t c0 = 0; c0 < V; c0 += kFwdThreads * 8 * kFwdVecs) {
-    Vec8<B16> x[kFwdVecs];
+  const float chosen = B16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[off + id])
+                           : static_cast<const float *>(p.logits)[off + id];
+  const int64_t tile = (int64_t)threads * 8 * kFwdVecs;
+  auto load = [&](Vec8<B16> (&x)[kFwdVecs], int64_t c0) {
 #pragma unroll
     for (int j = 0; j < kFwdVecs; ++j)
-      load_logits(x[j], p.logits, off, c0 + 8 * (j * kFwdThreads + threadIdx.x), V);
+      load_logits(x[j], p.logits, off, c0 + 8 * (int64_t)(j * threads + threadIdx.x), V);
+  };
+  Softmax a{kLowest, 0.0f, 0.0f};
+  Vec8<B16> x[kFwdVecs], next[kFwdVecs];
+  load(x, 0);
+  for (int64_t c0 = 0; c0 < V; c0 += tile) {
+    if (c0 + tile < V) load(next, c0 + tile);
     float top = a.m;
 #pragma unroll
     for (int j = 0; j < kFwdVecs; ++j)
@@ -103,24 +110,32 @@ __global__ __launch_bounds__(kFwdThreads) void logprob_fwd_kernel(const LogprobA
         a.s += k;
         if (ENT) a.t = fmaf(k, fmaxf(d, kFar), a.t);
       }
-  }
 #pragma unroll
-  for (int w = 1; w < 64; w *= 2) {
-    const Softmax b{__shfl_xor(a.m, w, 64), __shfl_xor(a.s, w, 64), __shfl_xor(a.t, w, 64)};
-    a = merge(a, b, c);
+    for (int j = 0; j < kFwdVecs; ++j) x[j] = next[j];
   }
-  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = a;
-  __syncthreads();
+  a = over_lanes(a, c);
+  if (waves > 1) {
+    if (lane == 0) part[threadIdx.x / 64] = a;
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    a = lane < waves ? part[lane] : Softmax{kLowest, 0.0f, 0.0f};
+    a = over_lanes(a, c);
+  }
   if (threadIdx.x == 0) {
-    for (int i = 1; i < kFwdThreads / 64; ++i) a = merge(a, part[i], c);
-    const float z = B16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[off + id])
-                        : static_cast<const float *>(p.logits)[off + id];
     const float ls = logf(a.s);
     const bool none = a.s == 0.0f;  // every logit is -inf
     p.lse[row] = none ? kNegInf : fmaf(a.m, p.scale, ls);
-    p.logp[row] = none ? kNegInf : fmaf(z - a.m, p.scale, -ls);
+    p.logp[row] = none ? kNegInf : fmaf(chosen - a.m, p.scale, -ls);
     if (ENT) p.entropy[row] = none ? 0.0f : fmaf(-a.t / a.s, p.scale, ls);
   }
+}
+
+// Threads of a row, by the vocabulary alone: one tile of 32 values a thread up to 8192 values
+// and 512 threads from there. 8192 rows of 65536 bf16 values take 179 us at 512 threads (6.0
+// TB/s), 191 at 256 and 221 at 1024; of 2048 values 11.0 us at 64 threads, 44 at 512. A row
+// by itself is bound by what one compute unit can fetch: 131072 binary32 values take 12 us.
+int fwd_threads(int64_t vocab) {
+  return vocab <= 2048 ? 64 : vocab <= 4096 ? 128 : vocab <= 8192 ? 256 : 512;
 }
 
 constexpr int kBwdThreads = 256, kBwdVecs = 2, kBwdSpan = kBwdThreads * 8 * kBwdVecs;
@@ -177,7 +192,7 @@ hipError_t launch_logprob_fwd(const LogprobArgs &a, hipStream_t stream) {
                                        : (const void *)logprob_fwd_kernel<true, false>)
                           : (a.entropy ? (const void *)logprob_fwd_kernel<false, true>
                                        : (const void *)logprob_fwd_kernel<false, false>);
-  return run(fn, a, a.rows, kFwdThreads, stream);
+  return run(fn, a, a.rows, fwd_threads(a.vocab), stream);
 }
 
 int64_t logprob_bwd_grid(const LogprobArgs &a) {
