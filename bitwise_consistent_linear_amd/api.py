@@ -735,17 +735,10 @@ def _workspace_ptr(t, need, like, index):
     return t, t.data_ptr(), t.numel()
 
 
-def _on_stream(fn):
-    """Run fn with `stream` as the current stream, so that what it allocates belongs there."""
-    from functools import wraps
-
-    @wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with _torch().cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
+def _elsewhere(stream, fn, *args, **kw):
+    """fn with `stream` as the current stream, so that what it allocates belongs there."""
+    with _torch().cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def _norm_kind(kind):
@@ -754,13 +747,15 @@ def _norm_kind(kind):
     return _NORM_KINDS[kind]
 
 
-@_on_stream
 def layer_norm_fwd(x, weight, bias=None, *, eps=1e-5, kind="layer", y=None, mean=None,
-                   rstd=None):
+                   rstd=None, stream=None):
     """gdn_layer_norm_fwd: the norm of each row of x [M, D] (float32 or bfloat16; rows may
     have a stride), kind "layer" or "rms"; weight and bias [D] float32 or bfloat16 alike,
     bias None for 0. ``stream`` may name another stream than the current one.
     Returns (y [M, D] in x's dtype, mean [M] or None for "rms", rstd [M])."""
+    if stream is not None:
+        return _elsewhere(stream, layer_norm_fwd, x, weight, bias, eps=eps, kind=kind, y=y,
+                          mean=mean, rstd=rstd)
     f32, fl = _dtypes()[:2]
     k = _norm_kind(kind)
     stride, dev = _rows(x, "x", fl)
@@ -788,14 +783,17 @@ def layer_norm_bwd_workspace_bytes(shape: GdnNormShape) -> int:
     return n.value
 
 
-@_on_stream
 def layer_norm_bwd(dy, x, weight, mean, rstd, *, kind="layer", bias=None, dx=None,
-                   d_weight=None, d_bias=None, workspace=None):
+                   d_weight=None, d_bias=None, workspace=None, stream=None):
     """gdn_layer_norm_bwd: gradients through layer_norm_fwd, given dy [M, D] in x's dtype and
     the mean (None for "rms") and rstd that it returned. ``bias`` says whether d_bias is
     wanted (default: for kind "layer"). ``workspace`` is a uint8 GPU tensor of at least
     layer_norm_bwd_workspace_bytes() bytes (allocated here when omitted).
     Returns (dx [M, D] in x's dtype, d_weight [D] float32, d_bias [D] float32 or None)."""
+    if stream is not None:
+        return _elsewhere(stream, layer_norm_bwd, dy, x, weight, mean, rstd, kind=kind,
+                          bias=bias, dx=dx, d_weight=d_weight, d_bias=d_bias,
+                          workspace=workspace)
     f32, fl = _dtypes()[:2]
     k = _norm_kind(kind)
     layer = k == GDN_NORM_LAYER
@@ -828,12 +826,13 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, kind="layer", bias=None, dx=Non
     return dx, d_weight, d_bias
 
 
-@_on_stream
-def quantize_rows(x, *, xq=None, scale=None):
+def quantize_rows(x, *, xq=None, scale=None, stream=None):
     """gdn_quantize_rows: each row of x [M, K] (float32 or bfloat16; rows may have a stride)
     to int8 with one scale, ties to even. Serves a linear layer's inputs and its weights
     [N, K]. Returns (xq int8 [M, K rounded up to I8_K_ALIGN, zeros in the padding],
     scale float32 [M])."""
+    if stream is not None:
+        return _elsewhere(stream, quantize_rows, x, xq=xq, scale=scale)
     f32, fl, i8 = _dtypes()[:3]
     stride, dev = _rows(x, "x", fl)
     M, K = x.shape
@@ -845,11 +844,13 @@ def quantize_rows(x, *, xq=None, scale=None):
     return xq, scale
 
 
-@_on_stream
-def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None):
+def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, stream=None):
     """gdn_linear_i8_fwd: Y = (xq wq^T) x_scale w_scale with exact integer sums. xq int8
     [M, Kp], wq int8 [N, Kp] as quantize_rows returns them, x_scale [M], w_scale [N] float32.
     Returns y [M, N] in out_dtype (float32 by default, or bfloat16)."""
+    if stream is not None:
+        return _elsewhere(stream, linear_i8_fwd, xq, x_scale, wq, w_scale,
+                          out_dtype=out_dtype, y=y)
     f32, _, i8 = _dtypes()[:3]
     _need(xq, "xq", i8, 2)
     _need(wq, "wq", i8, 2)
@@ -878,12 +879,15 @@ def _logprob_args(logits, ids, scale):
     return GdnLogprobShape(M, V, stride, _code(logits.dtype), ids.element_size(), scale), dev
 
 
-@_on_stream
-def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=None):
+def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=None,
+                      stream=None):
     """gdn_token_logprob_fwd: log-probability of token ids [M] (int32 or int64) under the
     softmax of scale * logits [M, V] (float32 or bfloat16; rows may have a stride), the
     log-sum-exp, and with entropy=True the entropy. Rows whose id is outside [0, V) are not
     scored: zeros. Returns (logp [M], lse [M], entropy [M] or None), float32."""
+    if stream is not None:
+        return _elsewhere(stream, token_logprob_fwd, logits, ids, scale=scale,
+                          entropy=entropy, logp=logp, lse=lse)
     f32 = _dtypes()[0][0]
     shape, dev = _logprob_args(logits, ids, scale)
     rows = (shape.rows,)
@@ -896,12 +900,14 @@ def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=N
     return logp, lse, ent
 
 
-@_on_stream
 def token_logprob_bwd(logits, ids, lse, d_logp, *, scale=1.0, entropy=None, d_entropy=None,
-                      d_logits=None):
+                      d_logits=None, stream=None):
     """gdn_token_logprob_bwd: the gradient of token_logprob_fwd's logp, and of its entropy
     where entropy and d_entropy [M] are given, with respect to the logits. Returns d_logits
     [M, V] in the logits' dtype; d_logits=logits overwrites them."""
+    if stream is not None:
+        return _elsewhere(stream, token_logprob_bwd, logits, ids, lse, d_logp, scale=scale,
+                          entropy=entropy, d_entropy=d_entropy, d_logits=d_logits)
     f32 = _dtypes()[0]
     shape, dev = _logprob_args(logits, ids, scale)
     rows = (shape.rows,)
@@ -951,16 +957,22 @@ def policy_loss_workspace_bytes(shape: GdnPolicyShape) -> int:
     return n.value
 
 
-@_on_stream
 def policy_loss_fwd(logp, old_logp, advantages, *, ref_logp=None, entropy=None, mask=None,
                     cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=None, kl_coef=0.0,
                     entropy_coef=0.0, reduction="token", stats=None, weight=None,
-                    workspace=None):
+                    workspace=None, stream=None):
     """gdn_policy_loss_fwd: the clipped policy loss of a packed batch (logp, old_logp,
     advantages [T] float32; ref_logp adds the KL term, entropy the entropy term; mask [T]
     bool, None for all scored; cu_seqlens int32 [N + 1], None for one sequence).
     Returns (stats [5]: loss and the weighted means of policy loss, KL, entropy and share of
     tokens cut off; weight [N]: the weight of a scored token of each sequence), float32."""
+    if stream is not None:
+        return _elsewhere(stream, policy_loss_fwd, logp, old_logp, advantages,
+                          ref_logp=ref_logp, entropy=entropy, mask=mask,
+                          cu_seqlens=cu_seqlens, clip_low=clip_low, clip_high=clip_high,
+                          dual_clip=dual_clip, kl_coef=kl_coef, entropy_coef=entropy_coef,
+                          reduction=reduction, stats=stats, weight=weight,
+                          workspace=workspace)
     f32 = _dtypes()[0][0]
     shape, dev, ptrs = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask,
                                     cu_seqlens, clip_low, clip_high, dual_clip, kl_coef,
@@ -975,14 +987,20 @@ def policy_loss_fwd(logp, old_logp, advantages, *, ref_logp=None, entropy=None, 
     return stats, weight
 
 
-@_on_stream
 def policy_loss_bwd(logp, old_logp, advantages, weight, *, ref_logp=None, entropy=None,
                     mask=None, cu_seqlens=None, clip_low=0.2, clip_high=0.2, dual_clip=None,
                     kl_coef=0.0, entropy_coef=0.0, reduction="token", d_loss=1.0, d_logp=None,
-                    d_entropy=None):
+                    d_entropy=None, stream=None):
     """gdn_policy_loss_bwd: the gradient of d_loss * loss, given the weight [N] that
     policy_loss_fwd returned for the same arguments. Returns (d_logp [T], d_entropy [T], or
     None without an entropy), float32."""
+    if stream is not None:
+        return _elsewhere(stream, policy_loss_bwd, logp, old_logp, advantages, weight,
+                          ref_logp=ref_logp, entropy=entropy, mask=mask,
+                          cu_seqlens=cu_seqlens, clip_low=clip_low, clip_high=clip_high,
+                          dual_clip=dual_clip, kl_coef=kl_coef, entropy_coef=entropy_coef,
+                          reduction=reduction, d_loss=d_loss, d_logp=d_logp,
+                          d_entropy=d_entropy)
     f32 = _dtypes()[0]
     shape, dev, ptrs = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask,
                                     cu_seqlens, clip_low, clip_high, dual_clip, kl_coef,

@@ -16,95 +16,139 @@ using f32x4 = float __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------------- quantisation
 
-// max |x| that keeps a NaN.
-__device__ __forceinline__ float abs_max(float a, float b) {
-  b = fabsf(b);
-  return (b > a || b != b) ? b : a;
-}
+// The rounding of 127 x / a goes through the sum with 1.5 * 2^23, whose last place is 1: the
+// sum rounds to an integer, ties to even, and its low byte is that integer's.
+constexpr float kToInteger = 12582912.0f;
 
-// 127 x / a rounded to the nearest integer, ties to even, for |x| <= a, inv = 1 / a rounded.
-// The product with inv is within a unit or two of the quotient's last place, which matters
-// only where the exact quotient is a half: one step with the exact remainder then gives the
-// half itself, and rint decides the tie. bf16: 127 x is exact in binary32. A quotient q in
-// [2^k, 2^(k+1)) of 8-bit numerator and denominator significands that is no half lies at least
-// 2^(k-17) from one; the corrected quotient is off by less than 2^(k-23).
-__device__ __forceinline__ float quotient(float x, float a, float inv) {
-  const float n = 127.0f * x;
+// 127 x / a rounded to the nearest integer, ties to even, in the low byte, for |x| <= a;
+// n = 127 x (exact in binary32 for bf16 x), inv = 1 / a rounded. The product with inv is
+// within a unit or two of the quotient's last place, which matters only where the exact
+// quotient is a half: one step with the exact remainder then gives the half itself, and the
+// sum decides the tie. A quotient q in [2^k, 2^(k+1)) of 8-bit numerator and denominator
+// significands that is no half lies at least 2^(k-17) from one; the corrected quotient is off
+// by less than 2^(k-23).
+__device__ __forceinline__ uint32_t quotient(float n, float a, float inv) {
   float q = n * inv;
   q = fmaf(fmaf(-q, a, n), inv, q);
-  return rintf(q);
+  return __float_as_uint(q + kToInteger);
 }
 
-// binary32 inputs: 127 x takes 31 bits, so the same in binary64.
-__device__ __forceinline__ float quotient(double x, double a, double inv) {
-  const double n = 127.0 * x;
+// binary32 x: 127 x takes 31 bits, so the same in binary64.
+__device__ __forceinline__ uint32_t quotient(double n, double a, double inv) {
   double q = n * inv;
   q = fma(fma(-q, a, n), inv, q);
-  return (float)rint(q);
+  return __float_as_uint((float)rint(q) + kToInteger);
 }
 
-template <bool B16, int T, int NV>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void quantize_kernel(const QuantizeArgs p) {
-  constexpr int kThreads = T < 256 ? 256 : T, RPW = kThreads / T;
-  __shared__ float slot[kThreads / 64];
-  const int t = threadIdx.x % T;
-  int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / T;
-  const bool live = row < p.rows;
-  if (!live) row = p.rows - 1;
-  Vec8<B16> x[NV];
+// Bytes 0 of four words, the first lowest.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0C0C0400u);
+  const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
+  return ab | cd;
+}
+
+// Largest |x| of eight values as binary32 bits: those order like integers, a NaN above all.
+__device__ __forceinline__ uint32_t abs_top(const Vec8<true> &v) {
+  using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
+  u16x2 m = {0, 0};
 #pragma unroll
-  for (int j = 0; j < NV; ++j) load_row(x[j], p.x, row * p.x_stride, 8 * (j * T + t), p.k);
-  float a = 0.0f;
+  for (int i = 0; i < 4; ++i)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v.r[i] & 0x7FFF7FFFu));
+  return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+}
+__device__ __forceinline__ uint32_t abs_top(const Vec8<false> &v) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v.get(e)) & 0x7FFFFFFFu);
+  return m;
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t max_rotated(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 | N, 0xF, 0xF, true));
+}
+
+constexpr int kQuantizeGrid = 2048;  // workgroups; more rows are walked over
+
+// G lanes share a row: 16, or 64 (then row_threads / 64 waves do). NV runs of eight values a
+// thread. A workgroup walks over rows, the next row's loads in flight under this one.
+template <bool B16, int G, int NV>
+__global__ __launch_bounds__(1024) void quantize_kernel(const QuantizeArgs p) {
+  __shared__ uint32_t slot[2][16];
+  const int T = G == 64 ? p.row_threads : G, groups = (int)blockDim.x / T;
+  const int t = threadIdx.x % T, g = threadIdx.x / T, waves = T / 64;
+  auto load = [&](Vec8<B16> (&x)[NV], int64_t row) {  // past the end the last row, unwritten
+    if (row >= p.rows) row = p.rows - 1;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a = abs_max(a, x[j].get(e));
+    for (int j = 0; j < NV; ++j) load_row(x[j], p.x, row * p.x_stride, 8 * (j * T + t), p.k);
+  };
+  const int64_t step = (int64_t)gridDim.x * groups;
+  constexpr bool kAhead = NV <= 2;
+  Vec8<B16> x[NV], next[kAhead ? NV : 1];
+  if (kAhead) load(x, (int64_t)blockIdx.x * groups + g);
+  int par = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step, par ^= 1) {
+    const int64_t row = r0 + g;
+    if constexpr (kAhead) {
+      if (r0 + step < p.rows) load(next, row + step);
+    } else {
+      load(x, row);
+    }
+    uint32_t top = 0;
 #pragma unroll
-  for (int s = 1; s < (T < 64 ? T : 64); s *= 2) a = abs_max(a, __shfl_xor(a, s, 64));
-  if constexpr (T > 64) {
-    if (threadIdx.x % 64 == 0) slot[threadIdx.x / 64] = a;
-    __syncthreads();
-    a = slot[0];
-#pragma unroll
-    for (int i = 1; i < T / 64; ++i) a = abs_max(a, slot[i]);
-  }
-  if (live) {
-    if (t == 0) p.scale[row] = a / 127.0f;
-    const bool finite = a < __builtin_inff(), some = a > 0.0f;
-    // the inverse of a subnormal a is not finite and 127 times a large one neither: scale the
-    // row and its maximum by a power of two first
-    const float up = a < 0x1p-100f ? 0x1p+120f : a > 0x1p+100f ? 0x1p-100f : 1.0f, as = a * up;
-    const float inv = 1.0f / as;
-    const double inv64 = B16 ? 0.0 : 1.0 / (double)as;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int col = 8 * (j * T + t);
-      uint32_t o[2] = {0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = x[j].get(e);
-        float q;
-        if (finite)
-          q = B16 ? quotient(v * up, as, inv) : quotient((double)(v * up), (double)as, inv64);
-        else
-          q = a == a && fabsf(v) == a ? copysignf(127.0f, v) : 0.0f;
-        o[e / 4] |= ((uint32_t)(some ? (int)q : 0) & 0xFFu) << (8 * (e % 4));
+    for (int j = 0; j < NV; ++j) top = max(top, abs_top(x[j]));
+    top = max_rotated<8>(top);
+    top = max_rotated<4>(top);
+    top = max_rotated<2>(top);
+    top = max_rotated<1>(top);
+    if constexpr (G == 64) {
+      auto of = [&](int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)top, lane); };
+      top = max(max(of(0), of(16)), max(of(32), of(48)));
+      if (waves > 1) {
+        const int wave = threadIdx.x / 64, first = wave / waves * waves;
+        if (threadIdx.x % 64 == 0) slot[par][wave] = top;
+        __syncthreads();
+        for (int i = 0; i < waves; ++i) top = max(top, slot[par][first + i]);
       }
-      if (col < p.k_pad)
-        *reinterpret_cast<uint2 *>(p.q + row * p.k_pad + col) = make_uint2(o[0], o[1]);
+    }
+    if (row < p.rows) {
+      const float a = __uint_as_float(top);
+      if (t == 0) p.scale[row] = a / 127.0f;
+      // the inverse of a subnormal a is not finite and 127 times a large one neither: scale the
+      // row and its maximum by a power of two first
+      const float up = a < 0x1p-100f ? 0x1p+120f : a > 0x1p+100f ? 0x1p-100f : 1.0f, as = a * up;
+      const bool plain = a > 0.0f && a < __builtin_inff();
+      const float inv = 1.0f / as;
+      const double inv64 = B16 ? 0.0 : 1.0 / (double)as;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int col = 8 * (j * T + t);
+        if (col >= p.k_pad) break;
+        uint32_t q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = x[j].get(e);
+          if (plain)
+            q[e] = B16 ? quotient(127.0f * up * v, as, inv)
+                       : quotient(127.0 * (double)(v * up), (double)as, inv64);
+          else  // +-127 at the infinities of a row without NaN, else 0
+            q[e] = a > 0.0f && fabsf(v) == a ? (v > 0.0f ? 127 : -127) : 0;
+        }
+        *reinterpret_cast<uint2 *>(p.q + row * p.k_pad + col) =
+            make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
+      }
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) x[j] = next[j];
     }
   }
 }
 
-template <int T, int NV>
-hipError_t quantize_as(const QuantizeArgs &a, hipStream_t stream) {
-  constexpr int kThreads = T < 256 ? 256 : T, RPW = kThreads / T;
-  QuantizeArgs args = a;
-  void *kargs[] = {&args};
-  const void *fn = a.x_bf16 ? (const void *)quantize_kernel<true, T, NV>
-                            : (const void *)quantize_kernel<false, T, NV>;
-  return hipLaunchKernel(fn, dim3((unsigned)((a.rows + RPW - 1) / RPW)), dim3(kThreads), kargs, 0,
-                         stream);
+template <int G, int NV>
+const void *quantize_fn(const QuantizeArgs &a) {
+  return a.x_bf16 ? (const void *)quantize_kernel<true, G, NV>
+                  : (const void *)quantize_kernel<false, G, NV>;
 }
 
 // ------------------------------------------------------------------------------ product
@@ -453,11 +497,20 @@ Launch pick(const LinearI8Args &a) {
 
 hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  if (a.k_pad <= 512) return quantize_as<64, 1>(a, stream);
-  if (a.k_pad <= 2048) return quantize_as<64, 4>(a, stream);
-  if (a.k_pad <= 8192) return quantize_as<256, 4>(a, stream);
-  if (a.k_pad <= 32768) return quantize_as<1024, 4>(a, stream);
-  return quantize_as<1024, 8>(a, stream);
+  const int nv = a.k_pad <= 8192 ? 1 : a.k_pad <= 16384 ? 2 : a.k_pad <= 32768 ? 4 : 8;
+  const int vecs = (a.k_pad + 8 * nv - 1) / (8 * nv);
+  QuantizeArgs args = a;
+  args.row_threads = vecs <= 16 ? 16 : (vecs + 63) / 64 * 64;
+  const int groups = args.row_threads >= 256 ? 1 : 256 / args.row_threads;
+  const void *fn = vecs <= 16 ? quantize_fn<16, 1>(a)
+                   : nv == 1  ? quantize_fn<64, 1>(a)
+                   : nv == 2  ? quantize_fn<64, 2>(a)
+                   : nv == 4  ? quantize_fn<64, 4>(a)
+                              : quantize_fn<64, 8>(a);
+  const int64_t need = (a.rows + groups - 1) / groups;
+  void *kargs[] = {&args};
+  return hipLaunchKernel(fn, dim3((unsigned)(need < kQuantizeGrid ? need : kQuantizeGrid)),
+                         dim3(args.row_threads * groups), kargs, 0, stream);
 }
 
 int64_t linear_i8_grid(const LinearI8Args &a) { return pick(a).grid; }

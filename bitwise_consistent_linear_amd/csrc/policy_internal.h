@@ -28,6 +28,7 @@ hipError_t launch_norm_bwd(const NormArgs &args, hipStream_t stream);
 struct QuantizeArgs {
   int64_t rows, x_stride;
   int32_t k, k_pad, x_bf16;
+  int32_t row_threads;  // set by the launcher: threads that share a row
   const void *x;
   int8_t *q;
   float *scale;
