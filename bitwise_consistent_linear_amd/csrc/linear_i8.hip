@@ -297,13 +297,15 @@ __device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, in
 // out (arrive), and nothing else in the loop goes through the vector memory counter.
 //
 // A row's 64 bytes are four 16-byte chunks, chunk c of row r at place c ^ key(r), so that the
-// lanes of an operand read, which want one chunk of 16 rows, spread over the LDS banks (no
-// bank conflicts measured). The loads fill LDS in the order of their lanes, so the permutation
-// is in which chunk a lane fetches.
+// lanes of an operand read spread over the LDS banks. 16 lanes are served together, measured
+// by which keys conflict: 0 - 3, 12 - 15 and 20 - 27, that is chunk c of rows 0 - 3 and 12 - 15
+// with chunk c ^ 1 of rows 4 - 11, and the same for the other half of the wave; the keys 0, 0,
+// 3, 3 of four rows each give these 16 places of the 256 bytes that the banks hold. The loads
+// fill LDS in the order of their lanes, so the permutation is in which chunk a lane fetches.
 //
 // Results go through LDS as well, 16 rows of a wave at a time, so that neighbouring lanes
 // store neighbouring values; the stores bypass the caches, which hold the operands.
-__device__ __forceinline__ int chunk_key(int r) { return (r >> 2) & 3; }
+__device__ __forceinline__ int chunk_key(int r) { return (r >> 3 & 1) * 3; }
 
 // 16 bytes per lane from base + offset to LDS, lane after lane from `to` (uniform) on.
 __device__ __forceinline__ void load_to_lds(const int8_t *base, uint32_t offset, uint32_t to) {

@@ -118,14 +118,14 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[j][e] = db[j][e] = 0.0f;
-  const int64_t lo = (int64_t)p.block_rows * blockIdx.x;
-  const int64_t hi = lo + p.block_rows < p.rows ? lo + p.block_rows : p.rows;
+  // blocks take groups of rows in turn, so that together they walk through memory in order
+  const int64_t step = (int64_t)gridDim.x * groups;
   struct Row {
     Vec8<XB> x[NV], dy[NV];
     float mean, rstd;
   };
   auto load = [&](Row &r, int64_t row) {  // past the end the last one again, unused
-    if (row >= hi) row = hi - 1;
+    if (row >= p.rows) row = p.rows - 1;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       load_row(r.x[j], p.x, row * p.x_stride, 8 * (j * T + t), D);
@@ -135,12 +135,12 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
     r.rstd = p.rstd[row];
   };
   Row cur, next;
-  if (kAhead && lo < hi) load(cur, lo + g);
+  if (kAhead && p.rows > 0) load(cur, (int64_t)blockIdx.x * groups + g);
   int par = 0;
-  for (int64_t r0 = lo; r0 < hi; r0 += groups, par ^= 1) {
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step, par ^= 1) {
     const int64_t row = r0 + g;
     if (kAhead) {
-      load(next, row + groups);
+      if (r0 + step < p.rows) load(next, row + step);
     } else {
       load(cur, row);
       load_weight();
@@ -156,14 +156,14 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
         gw[j][e] = d * w[j].get(e);
         c[0] = fmaf(gw[j][e], xh[j][e], c[0]);
         c[1] += gw[j][e];
-        if (row < hi) {
+        if (row < p.rows) {
           dw[j][e] = fmaf(d, xh[j][e], dw[j][e]);
           db[j][e] += d;
         }
       }
     row_sums<G>(c, T / 64, slot[par]);
     const float c1 = c[0] * inv, c2 = layer ? c[1] * inv : 0.0f;
-    if (row < hi) {
+    if (row < p.rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float o[8];
@@ -257,21 +257,15 @@ hipError_t run(const void *fn, const NormArgs &a, dim3 grid, int threads, hipStr
   return hipLaunchKernel(fn, grid, dim3(threads), kargs, 0, stream);
 }
 
-// Rows of a backward block, by rows and width alone (the same bits on any device). More
-// blocks than compute units only add partial sums to write and read: 16384 x 4096 bf16 takes
-// 88.6 us with 256 blocks of two rows at a time, 93.0 with 512 and 99.9 with 1024.
-int64_t block_rows_of(int64_t rows, int32_t width) {
-  const int groups = split_of(width, 1024).groups;
-  const int64_t per = (rows + kBwdGrid - 1) / kBwdGrid;
-  return (per + groups - 1) / groups * groups;
-}
-
 }  // namespace
 
+// Blocks of a backward launch, by rows and width alone (the same bits on any device). More
+// blocks than compute units only add partial sums to write and read: 16384 x 4096 bf16 took
+// 88.6 us with 256 blocks of two rows at a time, 93.0 with 512 and 99.9 with 1024.
 int norm_bwd_blocks(int64_t rows, int32_t width) {
-  if (rows == 0) return 1;  // a block that writes zeros
-  const int64_t per = block_rows_of(rows, width);
-  return (int)((rows + per - 1) / per);
+  const int groups = split_of(width, 1024).groups;
+  const int64_t need = (rows + groups - 1) / groups;
+  return (int)(need < 1 ? 1 : need < kBwdGrid ? need : kBwdGrid);  // no rows: one writes zeros
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream) {
@@ -289,7 +283,6 @@ hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream) {
   const Split s = split_of(a.width, 1024);
   NormArgs args = a;
   args.row_threads = s.row_threads;
-  args.block_rows = (int32_t)block_rows_of(a.rows, a.width);
   const void *fn = s.row_threads == 16 ? bwd_fn<16, 1>(a) : s.nv == 1 ? bwd_fn<64, 1>(a)
                                                                       : bwd_fn<64, 2>(a);
   hipError_t e = run(fn, args, dim3((unsigned)a.blocks), s.threads(), stream);

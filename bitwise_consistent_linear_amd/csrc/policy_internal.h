@@ -18,7 +18,7 @@ struct NormArgs {
   // backward
   float *d_weight, *d_bias;
   float *partials;  // [blocks][2][width]: sums of dy * xh and of dy over a block's rows
-  int32_t blocks, block_rows;
+  int32_t blocks;
   int32_t row_threads;  // set by the launcher: threads that share a row
 };
 int norm_bwd_blocks(int64_t rows, int32_t width);
