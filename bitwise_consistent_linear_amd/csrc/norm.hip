@@ -162,13 +162,13 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
         }
       }
     row_sums<G>(c, T / 64, slot[par]);
-    const float c1 = c[0] * inv, c2 = layer ? c[1] * inv : 0.0f;
+    const float rs = cur.rstd, c1 = c[0] * inv * rs, c2 = layer ? c[1] * inv * rs : 0.0f;
     if (row < p.rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = (fmaf(-xh[j][e], c1, gw[j][e]) - c2) * cur.rstd;
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(-xh[j][e], c1, fmaf(gw[j][e], rs, -c2));
         store_row<XB>(p.y, row * D, 8 * (j * T + t), D, o);
       }
     }

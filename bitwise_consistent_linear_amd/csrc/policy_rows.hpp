@@ -148,23 +148,20 @@ __device__ __forceinline__ float lane_max(float v) {
 }
 
 // K sums at once over the `waves` waves that share a row (the wave's alone, or a row of 16
-// lanes, for G lanes a row): lanes first, then the waves in ascending order through `slot`,
-// which must not be written again before the workgroup's next barrier after this one.
-template <int G, int K, int N>
-__device__ __forceinline__ void row_sums(float (&v)[K], int waves, float (&slot)[K][N]) {
+// lanes, for G lanes a row): lanes first, then the waves, whose sums a row of 16 lanes adds.
+// `slot` must not be written again before the workgroup's next barrier after this one.
+template <int G, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], int waves, float (&slot)[K][16]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = lane_sum<G>(v[k]);
   if (G < 64 || waves == 1) return;
-  const int wave = threadIdx.x / 64, first = wave / waves * waves;
+  const int wave = threadIdx.x / 64, first = wave / waves * waves, at = threadIdx.x % 16;
   if (threadIdx.x % 64 == 0)
 #pragma unroll
     for (int k = 0; k < K; ++k) slot[k][wave] = v[k];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    v[k] = slot[k][first];
-    for (int i = 1; i < waves; ++i) v[k] += slot[k][first + i];
-  }
+  for (int k = 0; k < K; ++k) v[k] = lane_sum<16>(at < waves ? slot[k][first + at] : 0.0f);
 }
 
 }  // namespace gdn
