@@ -321,7 +321,8 @@ __device__ __forceinline__ void load_to_lds(const int8_t *base, uint32_t offset,
 template <int Loads>
 __device__ __forceinline__ void arrive() {
   static_assert(Loads < 64, "six bits of the counter");
-  __builtin_amdgcn_s_waitcnt(0x0070 | (Loads & 15) | Loads >> 4 << 14);  // lgkmcnt = 0
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Loads) : "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt = 0, which the compiler then knows
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");

@@ -524,6 +524,64 @@ def test_policy_bad_offsets_stay_inside():
         assert dl.shape == (T,) and weight.shape == (3,)
 
 
+# ------------------------------------------------------- element offsets past 2^31, bytes past 2^32
+
+def test_long_norm_and_quantize():
+    M, D = 540000, 4096
+    x = torch.full((M, D), 0.5, dtype=BF16, device=DEV)
+    tail = rand(gen(51), 70, D, dtype=BF16).to(DEV)
+    x[-70:] = tail
+    w = torch.ones(D, dtype=BF16, device=DEV)
+    y, mean, rstd = api.layer_norm_fwd(x, w, w)
+    y1, m1, r1 = api.layer_norm_fwd(tail, w, w)
+    for p, q in ((y[-70:], y1), (mean[-70:], m1), (rstd[-70:], r1)):
+        same_bits(p, q, "norm's last rows")
+    dx, dw, db = api.layer_norm_bwd(x, x, w, mean, rstd)
+    d1, dw1, _ = api.layer_norm_bwd(tail, tail, w, m1, r1)
+    same_bits(dx[-70:], d1, "dx's last rows")
+    # the constant rows' normalised values are 0: d_weight is the last rows' alone; the bound
+    # is the sums' own, twice (two orders of addition)
+    xh = (tail.double() - m1.double()[:, None]) * r1.double()[:, None]
+    bound = 2 * (R.ROWS_DEPTH + 4) * R.U * (tail.double() * xh).abs().sum(0).cpu()
+    R.check(dw, dw1.cpu().double(), bound, "d_weight")
+    q, s = api.quantize_rows(x)
+    q1, s1 = api.quantize_rows(tail)
+    same_bits(q[-70:], q1, "q's last rows")
+    same_bits(s[-70:], s1, "scale's last rows")
+
+
+def test_long_product():
+    g = gen(52)
+    M, N = 33000, 66000
+    xq = torch.randint(-127, 128, (M, 128), generator=g, dtype=torch.int8).to(DEV)
+    wq = torch.randint(-127, 128, (N, 128), generator=g, dtype=torch.int8).to(DEV)
+    xs, ws = torch.rand(M, generator=g).to(DEV), torch.rand(N, generator=g).to(DEV)
+    y = api.linear_i8_fwd(xq, xs, wq, ws, out_dtype=BF16)
+    z = api.linear_i8_fwd(xq[-90:], xs[-90:], wq, ws, out_dtype=BF16)
+    same_bits(y[-90:], z, "last rows")
+    want = R.linear_i8(xq[-90:].cpu(), xs[-90:].cpu(), wq[-200:].cpu(), ws[-200:].cpu(), BF16)
+    same_bits(z[:, -200:].contiguous().cpu(), want, "last rows and columns")
+
+
+def test_long_logits():
+    M, V = 33000, 65537
+    z = torch.zeros((M, V), dtype=BF16, device=DEV)
+    tail, ids, dlp, de = (t.to(DEV) for t in lp_inputs(60, V, BF16, 53))
+    z[-60:] = tail
+    every = torch.full((M,), -1, dtype=torch.int64, device=DEV)
+    every[-60:] = ids
+    dl = torch.zeros(M, device=DEV)
+    dl[-60:] = dlp
+    logp, lse, _ = api.token_logprob_fwd(z, every)
+    logp1, lse1, _ = api.token_logprob_fwd(tail, ids)
+    same_bits(logp[-60:], logp1, "logp's last rows")
+    same_bits(lse[-60:], lse1, "lse's last rows")
+    assert float(logp[:-60].abs().sum()) == 0.0
+    d1 = api.token_logprob_bwd(tail, ids, lse1, dlp)
+    d = api.token_logprob_bwd(z, every, lse, dl, d_logits=z)
+    same_bits(d[-60:], d1, "d_logits' last rows")
+
+
 # ------------------------------------------------------------ graphs, streams and refusals
 
 def head_step(s):
