@@ -5,6 +5,8 @@
 // of rows changes a bit of Y; only the epilogue rounds (integer to binary32, two products,
 // and the rounding to Y's type).
 
+#include <algorithm>
+
 #include "policy_internal.h"
 #include "policy_rows.hpp"
 
@@ -179,7 +181,7 @@ __device__ __forceinline__ f32x4 column_scales(const LinearI8Args &p, int64_t n)
 // lines of K in turn and their integer sums are added in LDS.
 template <int MT, int NT, bool YB>
 __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args p) {
-  constexpr int U = MT == 2 ? 2 : 4;  // lines of K in flight
+  constexpr int U = MT * NT == 4 ? 1 : 2;  // lines of K a turn, the next in flight
   __shared__ i32x4 part[8][NT * MT][64];
   const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t tiles_n = (p.n + 16 * NT - 1) / (16 * NT);
@@ -202,19 +204,23 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
     for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
   auto at = [](const int8_t *b, int k) { return *reinterpret_cast<const i32x4 *>(b + k); };
   const int lines = p.k / 128;
-  int line = wave;
-  for (; line + 8 * (U - 1) < lines; line += 8 * U) {
-    i32x4 wf[U][2][NT], xf[U][2][MT];
+  struct Turn {
+    i32x4 w[U][2][NT], x[U][2][MT];
+  };
+  auto load = [&](Turn &t, int line) {  // a line past the end is zeros
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k = (line + 8 * u) * 128 + 64 * h;
+        const bool in = line + 8 * u < lines;
+        const int k = in ? (line + 8 * u) * 128 + 64 * h : 0;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) wf[u][h][j] = at(w[j], k);
+        for (int j = 0; j < NT; ++j) t.w[u][h][j] = in ? at(w[j], k) : i32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < MT; ++i) xf[u][h][i] = at(x[i], k);
+        for (int i = 0; i < MT; ++i) t.x[u][h][i] = in ? at(x[i], k) : i32x4{0, 0, 0, 0};
       }
+  };
+  auto multiply = [&](const Turn &t) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -222,19 +228,16 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int i = 0; i < MT; ++i) acc[j][i] = mfma(wf[u][h][j], xf[u][h][i], acc[j][i]);
+          for (int i = 0; i < MT; ++i) acc[j][i] = mfma(t.w[u][h][j], t.x[u][h][i], acc[j][i]);
+  };
+  Turn t0, t1;
+  load(t0, wave);
+  for (int line = wave; line < lines; line += 16 * U) {
+    load(t1, line + 8 * U);
+    multiply(t0);
+    load(t0, line + 16 * U);
+    multiply(t1);
   }
-  for (; line < lines; line += 8)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = line * 128 + 64 * h;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const i32x4 wf = at(w[j], k);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[j][i] = mfma(wf, at(x[i], k), acc[j][i]);
-      }
-    }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -261,16 +264,16 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
 
 // Sixteen bytes of row m of Y from column n on: 4 binary32 or 8 bf16 values.
 template <bool YB>
-__device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, int64_t n, i32x4 v) {
+__device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, int64_t n, i32x4 v,
+                                            bool through) {
   using unaligned = int __attribute__((ext_vector_type(4), aligned(YB ? 2 : 4)));
   constexpr int kChunk = YB ? 8 : 4;
   if (n + kChunk <= p.n) {
-    if (YB)
-      __builtin_nontemporal_store(
-          v, reinterpret_cast<unaligned *>(static_cast<uint16_t *>(p.y) + m * p.n + n));
+    char *y = static_cast<char *>(p.y) + (m * p.n + n) * (YB ? 2 : 4);
+    if (through)
+      __builtin_nontemporal_store(v, reinterpret_cast<unaligned *>(y));
     else
-      __builtin_nontemporal_store(
-          v, reinterpret_cast<unaligned *>(static_cast<float *>(p.y) + m * p.n + n));
+      *reinterpret_cast<unaligned *>(y) = v;
   } else {
 #pragma unroll
     for (int e = 0; e < kChunk; ++e)
@@ -304,7 +307,9 @@ __device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, in
 // fill LDS in the order of their lanes, so the permutation is in which chunk a lane fetches.
 //
 // Results go through LDS as well, 16 rows of a wave at a time, so that neighbouring lanes
-// store neighbouring values; the stores bypass the caches, which hold the operands.
+// store neighbouring values; the stores bypass the caches, which hold the operands, unless
+// rows start inside a 16-byte chunk: then the caches put the parts of a line together (597 x
+// 38941 x 293 to binary32 took 47 us past them, 32 with a row of 38944).
 __device__ __forceinline__ int chunk_key(int r) { return (r >> 3 & 1) * 3; }
 
 // 16 bytes per lane from base + offset to LDS, lane after lane from `to` (uniform) on.
@@ -425,6 +430,7 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
 
   arrive<0>();  // every load has landed and every operand been read: LDS is free
   int8_t *own = lds + wave * (kStage * 4 / kWaves);
+  const bool through = p.n % (YB ? 8 : 4) == 0;  // rows of whole chunks
   f32x4 ws[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) ws[j] = column_scales(p, n0 + wn + 16 * j + 4 * (l / 16));
@@ -452,7 +458,7 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
       const int q = 64 * g + l, r = q / kChunks, c = q % kChunks;
       const i32x4 v = *reinterpret_cast<const i32x4 *>(own + (r * kChunks + (c ^ (r % kChunks))) * 16);
       const int64_t m = mi + r, n = n0 + wn + kChunk * c;
-      if (m < p.m) store_chunk<YB>(p, m, n, v);
+      if (m < p.m) store_chunk<YB>(p, m, n, v, through);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -479,25 +485,32 @@ Launch tile_launch(const LinearI8Args &a) {
           BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
 }
 
-// The kernel of a size, by how many workgroups each would have. Up to 256 (one for each
-// compute unit) the rows kernels' split of K over the waves pays: 16 x 4096 x 4096 takes
-// 9.8 us in 256 workgroups of 16 x 16 against 13.4 in 64 of 64 x 64 tiles, and twice the
-// columns or rows for a workgroup costs 1 to 3 us. Past that, the largest tile that still
-// gives every unit one: 512 x 4096 x 4096 takes 20.4 us in tiles of 64 x 128 (256), 24.7 of
-// 128 x 128 (128), 50 of 256 x 256 (32); 4096 x 4096 x 4096 takes 130, 83 and 66. A tile is
-// not taller than twice the rows: 16 x 65536 x 4096 takes 63 us in tiles of 64 rows, 77 of 256.
+// The kernel of a size. Up to 256 workgroups (one for each compute unit) the rows kernels'
+// split of K over the waves pays: 16 x 4096 x 4096 takes 9.8 us in 256 workgroups of 16 x 16
+// against 13.4 in 64 of 64 x 64 tiles, and twice the columns or rows for a workgroup costs 1
+// to 3 us. Past that, the tile whose rounds over the units take the least: a round of 4096
+// k takes 10.5 us in tiles of 64 x 64, 17 of 64 x 128, 23 of 128 x 128, 37 of 128 x 256 and
+// 62 of 256 x 256 (measured from 512 x 4096 x 4096 to 16384 x 4096 x 4096).
 Launch pick(const LinearI8Args &a) {
   auto count = [&](int rows, int cols) {
     return (a.m + rows - 1) / rows * ((a.n + cols - 1) / cols);
   };
   if (count(16, 16) <= 256) return rows_launch<1, 1>(a);
-  if (a.m <= 16 && count(16, 32) <= 256) return rows_launch<1, 2>(a);
+  if (count(16, 32) <= 256) return rows_launch<1, 2>(a);
   if (count(32, 16) <= 256) return rows_launch<2, 1>(a);
   if (count(32, 32) <= 256) return rows_launch<2, 2>(a);
-  if (a.m > 128 && count(256, 256) >= 200) return tile_launch<256, 256, 64, 128>(a);
-  if (a.m > 64 && count(128, 128) >= 256) return tile_launch<128, 128, 64, 64>(a);
-  if (count(64, 128) >= 256) return tile_launch<64, 128, 32, 64>(a);
-  return tile_launch<64, 64, 32, 32>(a);
+  auto time = [&](int rows, int cols, double round) {
+    return (double)((count(rows, cols) + 255) / 256) * round;
+  };
+  const double t[5] = {time(256, 256, 62.0), time(128, 256, 37.0), time(128, 128, 23.0),
+                       time(64, 128, 17.0), time(64, 64, 10.5)};
+  switch (std::min_element(t, t + 5) - t) {
+    case 0: return tile_launch<256, 256, 64, 128>(a);
+    case 1: return tile_launch<128, 256, 64, 64>(a);
+    case 2: return tile_launch<128, 128, 64, 64>(a);
+    case 3: return tile_launch<64, 128, 32, 64>(a);
+    default: return tile_launch<64, 64, 32, 32>(a);
+  }
 }
 
 }  // namespace

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(const NormArgs p) {
 template <bool XB, bool WB, int G, int NV>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
   __shared__ float slot[2][2][16];
-  __shared__ float share[4096];  // the columns of a group, where there are several
+  __shared__ float share[8192];  // every thread's columns, where there are several groups
   const int T = G == 64 ? p.row_threads : G, groups = (int)blockDim.x / T;
   const int t = threadIdx.x % T, g = threadIdx.x / T, D = p.width;
   const bool layer = p.layer;
@@ -174,33 +174,29 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
     }
     if (kAhead) cur = next;
   }
-  // groups in ascending order
-  auto gather = [&](float (&acc)[NV][8]) {
-    for (int k = 1; k < groups; ++k) {
-      if (g == k)
+  // the columns of all groups, groups in ascending order, into the block's row of sums
+  auto put = [&](float (&acc)[NV][8], int64_t at) {
+    if (groups == 1) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) store_row<false>(p.partials, at, 8 * (j * T + t), D, acc[j]);
+      return;
+    }
+    // several groups hold one run of eight columns a thread (NV = 1)
+    __syncthreads();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) share[(j * 8 + e) * T + t] = acc[j][e];
-      __syncthreads();
-      if (g == 0)
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[j][e] += share[(j * 8 + e) * T + t];
-      __syncthreads();
+    for (int e = 0; e < 8; ++e) share[e * blockDim.x + threadIdx.x] = acc[0][e];
+    __syncthreads();
+    for (int q = threadIdx.x; q < 8 * T; q += blockDim.x) {  // column 8 (q % T) + q / T
+      const float *own = share + q / T * blockDim.x + q % T;
+      float s = own[0];
+#pragma unroll 8
+      for (int k = 1; k < groups; ++k) s += own[k * T];
+      const int col = 8 * (q % T) + q / T;
+      if (col < D) p.partials[at + col] = s;
     }
   };
-  gather(dw);
-  gather(db);
-  if (g == 0) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      store_row<false>(p.partials, (int64_t)blockIdx.x * 2 * D, 8 * (j * T + t), D, dw[j]);
-      if (p.d_bias)
-        store_row<false>(p.partials, (int64_t)(blockIdx.x * 2 + 1) * D, 8 * (j * T + t), D, db[j]);
-    }
-  }
+  put(dw, (int64_t)blockIdx.x * 2 * D);
+  if (p.d_bias) put(db, (int64_t)(blockIdx.x * 2 + 1) * D);
 }
 
 // The blocks' column sums, added: 64 columns per workgroup, wave i takes the blocks
