@@ -670,6 +670,18 @@ def _dtypes():
             (t.bool, t.uint8))
 
 
+@lru_cache(maxsize=None)
+def _empty():
+    return _torch().empty
+
+
+@lru_cache(maxsize=None)
+def _stream_calls():
+    """(current device, raw current stream of a device)"""
+    torch = _torch()
+    return torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 # These calls take microseconds on the GPU, so their checks are one expression each; what is
 # wrong is found out only where something is.
 
@@ -682,10 +694,13 @@ def _refuse(t, name, dtypes, shape, index):
 
 def _take(t, name, dtypes, shape, index):
     """The pointer of a dense tensor of `shape` on GPU `index`."""
-    if not (hasattr(t, "get_device") and t.get_device() == index and t.dtype in dtypes
-            and t.shape == shape and t.is_contiguous()):
-        _refuse(t, name, dtypes, shape, index)
-    return t.data_ptr()
+    try:
+        if (t.dtype in dtypes and t.shape == shape and t.get_device() == index
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        pass
+    _refuse(t, name, dtypes, shape, index)
 
 
 def _rows(t, name, dtypes):
@@ -710,7 +725,7 @@ def _rows(t, name, dtypes):
 def _place(t, name, dtype, shape, like, index):
     """The caller's output, checked, or a new one."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=like.device)
+        return _empty()(shape, dtype=dtype, device=like.device)
     _take(t, name, (dtype,), shape, index)
     return t
 
@@ -718,19 +733,21 @@ def _place(t, name, dtype, shape, like, index):
 def _raw_stream(index):
     """The current stream of GPU `index`, which has to be the current device: the library
     launches there."""
-    torch = _torch()
-    if torch.cuda.current_device() != index:
-        raise ValueError(f"the tensors are on GPU {index}, the current device is "
-                         f"{torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(index)
+    device, stream = _stream_calls()
+    if device() != index:
+        raise ValueError(f"the tensors are on GPU {index}, the current device is {device()}")
+    return stream(index)
 
 
 def _workspace_ptr(t, need, like, index):
-    """(tensor to keep, pointer, bytes) of a uint8 workspace, the caller's or a new one."""
+    """(tensor to keep, pointer, bytes) of a uint8 workspace, the caller's or a new one of
+    need() bytes."""
     torch = _torch()
     if t is None:
-        t = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif _need(t, "workspace", (torch.uint8,), 1).get_device() != index:
+        n = need()
+        t = torch.empty(n, dtype=torch.uint8, device=like.device)
+        return t, t.data_ptr(), n
+    if _need(t, "workspace", (torch.uint8,), 1).get_device() != index:
         raise ValueError(f"workspace is on {t.device}, expected GPU {index}")
     return t, t.data_ptr(), t.numel()
 
@@ -817,8 +834,8 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, kind="layer", bias=None, dx=Non
     elif d_bias is not None:
         raise ValueError("d_bias is given but bias is False")
     shape = GdnNormShape(M, D, k, _code(x.dtype), _code(weight.dtype))
-    need = 0 if workspace is not None else layer_norm_bwd_workspace_bytes(shape)
-    ws, ws_ptr, ws_bytes = _workspace_ptr(workspace, need, x, dev)
+    ws, ws_ptr, ws_bytes = _workspace_ptr(
+        workspace, lambda: layer_norm_bwd_workspace_bytes(shape), x, dev)
     _policy_check(policy_lib().gdn_layer_norm_bwd(
         ctypes.byref(shape), dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, w, _ptr(mean),
         rs, dx.data_ptr(), d_weight.data_ptr(), _ptr(d_bias), ws_ptr, ws_bytes,
@@ -979,8 +996,8 @@ def policy_loss_fwd(logp, old_logp, advantages, *, ref_logp=None, entropy=None, 
                                     entropy_coef, reduction)
     stats = _place(stats, "stats", f32, (5,), logp, dev)
     weight = _place(weight, "weight", f32, (shape.seqs,), logp, dev)
-    need = 0 if workspace is not None else policy_loss_workspace_bytes(shape)
-    ws, ws_ptr, ws_bytes = _workspace_ptr(workspace, need, logp, dev)
+    ws, ws_ptr, ws_bytes = _workspace_ptr(
+        workspace, lambda: policy_loss_workspace_bytes(shape), logp, dev)
     _policy_check(policy_lib().gdn_policy_loss_fwd(
         ctypes.byref(shape), *ptrs, stats.data_ptr(), weight.data_ptr(), ws_ptr, ws_bytes,
         _raw_stream(dev)))
