@@ -8,9 +8,8 @@
 // logits would lose. The order depends on the vocabulary alone, so a row has the same bits
 // in any batch.
 //
-// Backward: elementwise in the logits, bound by reading them and writing the gradient, 16
-// values a thread: 8192 x 65536 bf16 with the entropy's term 348 us (6.0 TB/s), 1021 x 50021
-// binary32 79 us (5.1 TB/s).
+// Backward: elementwise in the logits, bound by reading them and writing the gradient: 8192 x
+// 65536 bf16 with the entropy's term 348 us (6.0 TB/s), 1021 x 50021 binary32 74 us (5.3 TB/s).
 
 #include "policy_internal.h"
 #include "policy_rows.hpp"
@@ -140,12 +139,17 @@ int fwd_threads(int64_t vocab) {
   return vocab <= 2048 ? 64 : vocab <= 4096 ? 128 : vocab <= 8192 ? 256 : 512;
 }
 
-constexpr int kBwdThreads = 256, kBwdVecs = 2, kBwdSpan = kBwdThreads * 8 * kBwdVecs;
+// Runs of eight values a thread: 32 bytes of either type (4096 x 65536 binary32 takes 344 us
+// with one run and 372 with two, 8192 x 65536 bf16 355 with two and 402 with one).
+constexpr int kBwdThreads = 256;
+constexpr int bwd_vecs(bool bf16) { return bf16 ? 2 : 1; }
+constexpr int bwd_span(bool bf16) { return kBwdThreads * 8 * bwd_vecs(bf16); }
 
 template <bool B16, bool ENT>
 __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobArgs p) {
-  const int64_t V = p.vocab, spans = (V + kBwdSpan - 1) / kBwdSpan;
-  const int64_t row = blockIdx.x / spans, c0 = (blockIdx.x % spans) * kBwdSpan;
+  constexpr int J = bwd_vecs(B16), kSpan = bwd_span(B16);
+  const int64_t V = p.vocab, spans = (V + kSpan - 1) / kSpan;
+  const int64_t row = blockIdx.x / spans, c0 = (blockIdx.x % spans) * kSpan;
   const int64_t id = id_of(p, row);
   const float lse = p.lse[row];
   const bool use = id >= 0 && id < V && lse != kNegInf;
@@ -153,14 +157,14 @@ __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobA
   const float g = use ? p.d_logp[row] * scale : 0.0f;
   const float h = ENT && use ? p.d_entropy[row] * scale : 0.0f;
   const float H = ENT && use ? p.entropy[row] : 0.0f;
-  Vec8<B16> x[kBwdVecs];
+  Vec8<B16> x[J];
   if (use) {
 #pragma unroll
-    for (int j = 0; j < kBwdVecs; ++j)
+    for (int j = 0; j < J; ++j)
       load_row(x[j], p.logits, row * p.stride, c0 + 8 * (j * kBwdThreads + threadIdx.x), V);
   }
 #pragma unroll
-  for (int j = 0; j < kBwdVecs; ++j) {
+  for (int j = 0; j < J; ++j) {
     const int64_t c = c0 + 8 * (j * kBwdThreads + threadIdx.x);
     float d[8];
 #pragma unroll
@@ -198,7 +202,8 @@ hipError_t launch_logprob_fwd(const LogprobArgs &a, hipStream_t stream) {
 }
 
 int64_t logprob_bwd_grid(const LogprobArgs &a) {
-  return a.rows * ((a.vocab + kBwdSpan - 1) / kBwdSpan);
+  const int64_t span = bwd_span(a.bf16);
+  return a.rows * ((a.vocab + span - 1) / span);
 }
 
 hipError_t launch_logprob_bwd(const LogprobArgs &a, hipStream_t stream) {
