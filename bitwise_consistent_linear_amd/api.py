@@ -654,10 +654,10 @@ def policy_abi_version() -> int:
 
 
 def _code(dtype, name="out_dtype"):
-    torch = _torch()
-    if dtype is torch.float32:
+    f32, bf16 = _dtypes()[1]
+    if dtype is f32:
         return GDN_DTYPE_F32
-    if dtype is torch.bfloat16:
+    if dtype is bf16:
         return GDN_DTYPE_BF16
     raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
 
@@ -706,26 +706,25 @@ def _take(t, name, dtypes, shape, index):
 def _rows(t, name, dtypes):
     """Row stride, device index of a GPU matrix whose rows are contiguous (stride 0 repeats a
     row)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    index = t.get_device()
+    try:
+        index, dtype, shape, strides = t.get_device(), t.dtype, t.shape, t.stride()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
     if index < 0:
         raise ValueError(f"{name} must be on a GPU device")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions, got {tuple(t.shape)}")
-    stride, inner = t.stride()
-    if inner != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name} must be contiguous inside a row, got strides {t.stride()}")
-    return (stride if t.shape[0] > 1 else t.shape[1]), index
+    if dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {dtype}, expected one of {dtypes}")
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {tuple(shape)}")
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be contiguous inside a row, got strides {strides}")
+    return (strides[0] if shape[0] > 1 else shape[1]), index
 
 
 def _place(t, name, dtype, shape, like, index):
     """The caller's output, checked, or a new one."""
     if t is None:
-        return _empty()(shape, dtype=dtype, device=like.device)
+        return _empty()(*shape, dtype=dtype, device=like.device)
     _take(t, name, (dtype,), shape, index)
     return t
 
