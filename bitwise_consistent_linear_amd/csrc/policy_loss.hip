@@ -11,10 +11,10 @@
 // same bits on every launch. Backward: elementwise, each token's sequence found from its
 // wave's first.
 //
-// What a wave waits for is memory: it issues all loads of its tokens first, finds its first
-// sequence by a search of 64 lanes (one round of loads for 64 sequences, two for 4096), and
-// then holds the next 64 starts in its lanes. 262144 tokens in 64 sequences: tokens 6.2 us,
-// finish 9.7, gradient 6.3; 16384 in 4: 5.6, 6.2 and 5.7, of which a kernel that does nothing
+// What a wave waits for is memory: it issues all loads of its tokens first and finds its first
+// sequence by a search of 64 lanes (one round of loads for 64 sequences, two for 4096), the
+// last round's starts held in its lanes. 262144 tokens in 64 sequences: tokens 6.0 us,
+// finish 7.0, gradient 6.4; 16384 in 4: 5.5, 4.5 and 5.8, of which a kernel that does nothing
 // would take 2 to 3 each.
 
 #include "policy_internal.h"
@@ -88,20 +88,6 @@ __device__ __forceinline__ int64_t start_of(const PolicyArgs &p, int64_t n) {
   return v < 0 ? 0 : (v > p.tokens ? p.tokens : v);
 }
 
-// The last sequence that starts at or before token t (sequences of no tokens before it are
-// passed over): the one that holds t if any does. Uniform over the wave; 64 starts a round.
-__device__ __forceinline__ int64_t find_seq(const PolicyArgs &p, int64_t t) {
-  int64_t lo = 0, len = p.seqs;  // the answer is in [lo, lo + len)
-  while (len > 1) {
-    const int64_t step = (len + 63) / 64, at = lo + step * (int64_t)(threadIdx.x % 64);
-    const int below = __popcll(__ballot(at < lo + len && start_of(p, at) <= t));
-    const int64_t end = lo + len;
-    lo += step * (below > 0 ? below - 1 : 0);
-    len = end - lo < step ? end - lo : step;
-  }
-  return lo;
-}
-
 // A cursor over the sequences that meet a wave's tokens: lane i holds the start of sequence
 // first + i.
 struct Starts {
@@ -111,9 +97,31 @@ struct Starts {
     first = n;
     held = (int)start_of(p, n + threadIdx.x % 64);
   }
+  // The last sequence that starts at or before token t (sequences of no tokens before it are
+  // passed over): the one that holds t if any does. Uniform over the wave; 64 starts a round,
+  // those of the last round held.
+  __device__ __forceinline__ int64_t seek(const PolicyArgs &p, int64_t t) {
+    int64_t lo = 0, len = p.seqs;  // the answer is in [lo, lo + len)
+    while (len > 64) {
+      const int64_t step = (len + 63) / 64, at = lo + step * (int64_t)(threadIdx.x % 64);
+      const int below = __popcll(__ballot(at < lo + len && start_of(p, at) <= t));
+      const int64_t end = lo + len;
+      lo += step * (below > 0 ? below - 1 : 0);
+      len = end - lo < step ? end - lo : step;
+    }
+    load(p, lo);
+    const int below = __popcll(__ballot((int64_t)(threadIdx.x % 64) < len && held <= t));
+    return lo + (below > 0 ? below - 1 : 0);
+  }
   // start of sequence n in [first, first + 64)
   __device__ __forceinline__ int64_t at(int64_t n) const {
     return __builtin_amdgcn_readlane(held, __builtin_amdgcn_readfirstlane((int)(n - first)));
+  }
+  // starts of n and of the next one, with the 64 from n on held if they are not yet
+  __device__ __forceinline__ void span(const PolicyArgs &p, int64_t n, int64_t &s, int64_t &e) {
+    if (n - first >= 63) load(p, n);
+    s = at(n);
+    e = at(n + 1);
   }
 };
 
@@ -126,12 +134,17 @@ __device__ __forceinline__ double plus_moved(double v) {
   return v + __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
 
-// Sum over the wave's lanes, in lane 63: runs of 2, 4, 8, 16 lanes, then the rows of 16.
-__device__ __forceinline__ double wave_total(double v) {
-  v = plus_moved<0x111, 0xF>(v);  // from one lane below in the row of 16, two, four, eight
+// Sum over each row of 16 lanes, in its last lane: runs of 2, 4, 8, 16 lanes.
+__device__ __forceinline__ double row_total(double v) {
+  v = plus_moved<0x111, 0xF>(v);  // from one lane below in the row, two, four, eight
   v = plus_moved<0x112, 0xF>(v);
   v = plus_moved<0x114, 0xF>(v);
-  v = plus_moved<0x118, 0xF>(v);
+  return plus_moved<0x118, 0xF>(v);
+}
+
+// Sum over the wave's lanes, in lane 63: the rows of 16, then their sums.
+__device__ __forceinline__ double wave_total(double v) {
+  v = row_total(v);
   v = plus_moved<0x142, 0xA>(v);  // the row before, into rows 1 and 3
   return plus_moved<0x143, 0xC>(v);  // the first two rows, into the others
 }
@@ -148,10 +161,9 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(const PolicyArgs p) 
     for (int j = 0; j < kPer; ++j) in[j] = load_token(p, c0 + 64 * j + lane, end, true);
   };
   load(t0);
-  int64_t n = find_seq(p, t0);
   Starts starts;
-  starts.load(p, n);
-  int64_t s = starts.at(n), e = starts.at(n + 1);
+  int64_t n = starts.seek(p, t0), s, e;
+  starts.span(p, n, s, e);
   double sum[3] = {0.0, 0.0, 0.0};  // of the lane's tokens of sequence n so far
   int cut = 0, count = 0;           // of the wave's
   auto flush = [&]() {
@@ -196,9 +208,7 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(const PolicyArgs p) 
         s = e = p.tokens;
         break;
       }
-      if (n - starts.first >= 63) starts.load(p, n);
-      s = e;
-      e = starts.at(n + 1);
+      starts.span(p, n, s, e);
     }
   }
   if (s < end && e > end) flush();
@@ -225,23 +235,35 @@ constexpr int kInLds = 512;  // sequences whose sums stay in LDS
 
 __global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p) {
   __shared__ double held[kInLds * kSums], slot2[16][2], slot4[16][4];
+  __shared__ int starts[kInLds + 1];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  constexpr int kFew = 64;  // a sequence of at most so many slots is summed by single threads
+  constexpr int kFew = 256;  // a sequence of at most so many slots is 16 lanes', else a wave's
   double *sums = p.seqs <= kInLds ? held : p.seq_sums;  // [seqs][kSums]
+  const bool few = p.seqs <= kInLds;
+  if (few) {
+    for (int n = tid; n <= (int)p.seqs; n += 1024) starts[n] = (int)start_of(p, n);
+    __syncthreads();
+  }
   auto slots = [&](int64_t n, int64_t &lo, int64_t &hi) {  // [lo, hi) of sequence n
-    const int64_t s = start_of(p, n), e = start_of(p, n + 1);
+    const int64_t s = few ? starts[n] : start_of(p, n);
+    const int64_t e = few ? starts[n + 1] : start_of(p, n + 1);
     lo = s / p.span + n;
     hi = e > s ? (e - 1) / p.span + n + 1 : lo;
   };
-  for (int64_t q = tid; q < p.seqs * kSums; q += 1024) {
+  for (int64_t n = tid / 16; n < p.seqs; n += 64) {
     int64_t lo, hi;
-    slots(q / kSums, lo, hi);
+    slots(n, lo, hi);
     if (hi - lo > kFew) continue;
-    const double *part = p.partials + q % kSums;
-    double v = 0.0;
-#pragma unroll 8
-    for (int64_t i = lo; i < hi; ++i) v += part[i * kSums];
-    sums[q] = v;
+    double v[kSums] = {};
+#pragma unroll 2
+    for (int64_t i = lo + tid % 16; i < hi; i += 16)
+#pragma unroll
+      for (int k = 0; k < kSums; ++k) v[k] += p.partials[i * kSums + k];
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+      v[k] = row_total(v[k]);
+      if (tid % 16 == 15) sums[n * kSums + k] = v[k];
+    }
   }
   for (int64_t n = wave; n < p.seqs; n += 16) {
     int64_t lo, hi;
@@ -292,17 +314,17 @@ __global__ __launch_bounds__(256) void policy_grad_kernel(const PolicyArgs p) {
   Inputs in[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) in[j] = load_token(p, t0 + 64 * j + lane, end, false);
-  int64_t n = find_seq(p, t0);
   Starts starts;
-  starts.load(p, n);
-  float weight = n + lane < p.seqs ? p.weight[n + lane] : 0.0f;  // of sequence first + lane
-  float w[kPer] = {};
-  for (int64_t s = starts.at(n); n < p.seqs && s < end; ++n) {
-    if (n - starts.first >= 63) {
-      starts.load(p, n);
-      weight = n + lane < p.seqs ? p.weight[n + lane] : 0.0f;
+  int64_t n = starts.seek(p, t0), held = -1;
+  float weight = 0.0f, w[kPer] = {};  // weight: of sequence first + lane
+  for (; n < p.seqs; ++n) {
+    int64_t s, e;
+    starts.span(p, n, s, e);
+    if (s >= end) break;
+    if (starts.first != held) {
+      held = starts.first;
+      weight = held + lane < p.seqs ? p.weight[held + lane] : 0.0f;
     }
-    const int64_t e = starts.at(n + 1);
     const float wn = __int_as_float(__builtin_amdgcn_readlane(
         __float_as_int(weight), __builtin_amdgcn_readfirstlane((int)(n - starts.first))));
 #pragma unroll
@@ -310,7 +332,6 @@ __global__ __launch_bounds__(256) void policy_grad_kernel(const PolicyArgs p) {
       const int64_t t = t0 + 64 * j + lane;
       if (t >= s && t < e) w[j] = wn;
     }
-    s = e;
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
