@@ -110,7 +110,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(const NormArgs p) {
 template <bool XB, bool WB, int G, int NV>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
   __shared__ float slot[2][2][16];
-  __shared__ float share[8192];  // every thread's columns, where there are several groups
+  __shared__ float share[8 * (1024 + 8)];  // all threads' columns, where there are several groups
   const int T = G == 64 ? p.row_threads : G, groups = (int)blockDim.x / T;
   const int t = threadIdx.x % T, g = threadIdx.x / T, D = p.width;
   const bool layer = p.layer;
@@ -190,18 +190,19 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
       for (int j = 0; j < NV; ++j) store_row<false>(p.partials, at, 8 * (j * T + t), D, acc[j]);
       return;
     }
-    // several groups hold one run of eight columns a thread (NV = 1)
+    // several groups hold one run of eight columns a thread (NV = 1): value e of a thread at
+    // e * (threads + 8), so that neither its neighbours' nor a column's neighbours share banks
+    const int stride = (int)blockDim.x + 8;
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) share[e * blockDim.x + threadIdx.x] = acc[0][e];
+    for (int e = 0; e < 8; ++e) share[e * stride + threadIdx.x] = acc[0][e];
     __syncthreads();
-    for (int q = threadIdx.x; q < 8 * T; q += blockDim.x) {  // column 8 (q % T) + q / T
-      const float *own = share + q / T * blockDim.x + q % T;
+    for (int col = threadIdx.x; col < D; col += blockDim.x) {
+      const float *own = share + col % 8 * stride + col / 8;
       float s = own[0];
 #pragma unroll 8
       for (int k = 1; k < groups; ++k) s += own[k * T];
-      const int col = 8 * (q % T) + q / T;
-      if (col < D) p.partials[at + col] = s;
+      p.partials[at + col] = s;
     }
   };
   put(dw, (int64_t)blockIdx.x * 2 * D);
