@@ -94,7 +94,7 @@ gdn_status_t policy_shape(const char *fn, const gdn_policy_shape_t *sh, PolicyAr
   if (!sh) return no(GDN_E_NULL, fn, "shape is NULL");
   if (sh->tokens < 0 || sh->tokens > kMaxInt32)
     return no(GDN_E_SHAPE, fn, "tokens must be in [0, 2^31)");
-  if (sh->seqs < 1 || sh->seqs > kMaxInt32) return no(GDN_E_SHAPE, fn, "seqs must be in [1, 2^31)");
+  if (sh->seqs < 0 || sh->seqs > kMaxInt32) return no(GDN_E_SHAPE, fn, "seqs must be in [0, 2^31)");
   if (sh->reduction != GDN_REDUCE_TOKEN && sh->reduction != GDN_REDUCE_SEQUENCE)
     return no(GDN_E_UNSUPPORTED, fn, "reduction must be GDN_REDUCE_TOKEN or GDN_REDUCE_SEQUENCE");
   if (!(sh->clip_low >= 0.0 && sh->clip_low <= 1.0))
@@ -123,7 +123,7 @@ size_t policy_partial_bytes(const PolicyArgs &a) {
   return (size_t)(5 * a.slots * 8 + 255) / 256 * 256;
 }
 size_t policy_workspace(const PolicyArgs &a) {
-  return policy_partial_bytes(a) + (size_t)(5 * a.seqs * 8 + 255) / 256 * 256;
+  return policy_partial_bytes(a) + (size_t)(5 * a.seqs * 8 + 255) / 256 * 256 + 256;
 }
 
 gdn_status_t policy_inputs(const char *fn, const gdn_policy_shape_t *sh, const float *logp,
@@ -132,7 +132,7 @@ gdn_status_t policy_inputs(const char *fn, const gdn_policy_shape_t *sh, const f
   if (sh->tokens > 0 && (!logp || !old_logp || !adv))
     return no(GDN_E_NULL, fn, "logp, old_logp and advantages are required");
   if (!cu && sh->seqs != 1)
-    return no(GDN_E_NULL, fn, "cu_seqlens is required for more than one sequence");
+    return no(GDN_E_NULL, fn, "cu_seqlens is required unless there is one sequence");
   if (any_misaligned({logp, old_logp, adv, ref, cu}, 4))
     return no(GDN_E_SHAPE, fn, "inputs must be 4-byte aligned");
   a.logp = logp;
@@ -182,6 +182,8 @@ GDN_EXPORT gdn_status_t gdn_layer_norm_fwd(const gdn_norm_shape_t *shape, const 
       gdn::any_misaligned({weight, bias}, gdn::bytes_of(shape->w_dtype)) ||
       gdn::any_misaligned({mean, rstd}, 4))
     return gdn::no(GDN_E_SHAPE, fn, "a buffer is not aligned to its element");
+  if (y == x && x_stride != shape->width)
+    return gdn::no(GDN_E_SHAPE, fn, "y can be x only where x_stride is width");
   gdn::NormArgs a = gdn::norm_args(shape);
   a.x = x;
   a.x_stride = x_stride;
@@ -228,6 +230,8 @@ GDN_EXPORT gdn_status_t gdn_layer_norm_bwd(const gdn_norm_shape_t *shape, const 
     return gdn::no(GDN_E_SHAPE, fn, "workspace must be 256-byte aligned");
   if (workspace_bytes < gdn::norm_workspace(shape))
     return gdn::no(GDN_E_SHAPE, fn, "workspace smaller than gdn_layer_norm_bwd_workspace reports");
+  if (shape->rows > 0 && ((dx == dy && dy_stride != shape->width) || dx == x))
+    return gdn::no(GDN_E_SHAPE, fn, "dx can be dy only where dy_stride is width, and never x");
   gdn::NormArgs a = gdn::norm_args(shape);
   a.x = x;
   a.x_stride = x_stride;
@@ -377,7 +381,7 @@ GDN_EXPORT gdn_status_t gdn_policy_loss_fwd(const gdn_policy_shape_t *shape, con
   if (st != GDN_OK) return st;
   st = gdn::policy_inputs(fn, shape, logp, old_logp, advantages, ref_logp, cu_seqlens, a, mask);
   if (st != GDN_OK) return st;
-  if (!stats || !seq_weight || !workspace)
+  if (!stats || (!seq_weight && shape->seqs > 0) || !workspace)
     return gdn::no(GDN_E_NULL, fn, "stats, seq_weight and workspace are required");
   if (gdn::any_misaligned({entropy, stats, seq_weight}, 4))
     return gdn::no(GDN_E_SHAPE, fn, "a buffer is not aligned to its element");
@@ -407,7 +411,8 @@ GDN_EXPORT gdn_status_t gdn_policy_loss_bwd(const gdn_policy_shape_t *shape, con
   st = gdn::policy_inputs(fn, shape, logp, old_logp, advantages, ref_logp, cu_seqlens, a, mask);
   if (st != GDN_OK) return st;
   if (!std::isfinite(d_loss)) return gdn::no(GDN_E_SHAPE, fn, "d_loss must be finite");
-  if (!seq_weight) return gdn::no(GDN_E_NULL, fn, "seq_weight is required");
+  if (!seq_weight && shape->seqs > 0)
+    return gdn::no(GDN_E_NULL, fn, "seq_weight is required");
   if (shape->tokens > 0 && !d_logp) return gdn::no(GDN_E_NULL, fn, "d_logp is required");
   if (gdn::any_misaligned({seq_weight, d_logp, d_entropy}, 4))
     return gdn::no(GDN_E_SHAPE, fn, "a buffer is not aligned to its element");

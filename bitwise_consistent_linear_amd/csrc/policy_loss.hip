@@ -7,14 +7,14 @@
 // Forward: a wave takes a span of consecutive tokens, 256 at a time and 4 per lane, and adds
 // them up for each sequence that meets the span; a pair (span, sequence) has the slot span +
 // sequence, which no other pair has, since the pairs that meet form a staircase. One workgroup
-// then adds each sequence's slots in order, forms the weights and the loss. No atomics: the
-// same bits on every launch. Backward: elementwise, each token's sequence found from its
+// then adds each sequence's slots (a grid before it, of more than 512 sequences), forms the
+// weights and the loss. No atomics: the same bits on every launch. Backward: elementwise, each token's sequence found from its
 // wave's first.
 //
 // What a wave waits for is memory: it issues all loads of its tokens first and finds its first
 // sequence by a search of 64 lanes (one round of loads for 64 sequences, two for 4096), the
 // last round's starts held in its lanes. 262144 tokens in 64 sequences: tokens 6.0 us,
-// finish 7.0, gradient 6.4; 16384 in 4: 5.5, 4.5 and 5.8, of which a kernel that does nothing
+// finish 6.2, gradient 6.3; 16384 in 4: 5.5, 4.5 and 5.8, of which a kernel that does nothing
 // would take 2 to 3 each.
 
 #include "policy_internal.h"
@@ -231,26 +231,23 @@ __device__ __forceinline__ void group_total(double (&v)[K], double (&slot)[16][K
   }
 }
 
-constexpr int kInLds = 512;  // sequences whose sums stay in LDS
+constexpr int kInLds = 512;  // sequences whose sums the finish forms itself, in LDS
+constexpr int kGroup = 64;   // sequences of a workgroup of the sums kernel otherwise
 
-__global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p) {
-  __shared__ double held[kInLds * kSums], slot2[16][2], slot4[16][4];
-  __shared__ int starts[kInLds + 1];
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  constexpr int kFew = 256;  // a sequence of at most so many slots is 16 lanes', else a wave's
-  double *sums = p.seqs <= kInLds ? held : p.seq_sums;  // [seqs][kSums]
-  const bool few = p.seqs <= kInLds;
-  if (few) {
-    for (int n = tid; n <= (int)p.seqs; n += 1024) starts[n] = (int)start_of(p, n);
-    __syncthreads();
-  }
-  auto slots = [&](int64_t n, int64_t &lo, int64_t &hi) {  // [lo, hi) of sequence n
-    const int64_t s = few ? starts[n] : start_of(p, n);
-    const int64_t e = few ? starts[n + 1] : start_of(p, n + 1);
-    lo = s / p.span + n;
-    hi = e > s ? (e - 1) / p.span + n + 1 : lo;
+// Sums of the slots of sequences [n0, n1) by a workgroup of 1024 threads: 16 lanes for a
+// sequence of up to kFew slots, a wave for a longer one. `start` gives a sequence's start.
+template <class Start>
+__device__ __forceinline__ void add_slots(const PolicyArgs &p, int64_t n0, int64_t n1,
+                                          Start start, double *sums) {
+  constexpr int kFew = 256;
+  const int tid = threadIdx.x, lane = tid % 64;
+  const uint32_t span = (uint32_t)p.span;  // starts are below 2^31
+  auto slots = [&](int64_t n, int64_t &lo, int64_t &hi) {
+    const uint32_t s = (uint32_t)start(n), e = (uint32_t)start(n + 1);
+    lo = s / span + n;
+    hi = e > s ? (e - 1) / span + n + 1 : lo;
   };
-  for (int64_t n = tid / 16; n < p.seqs; n += 64) {
+  for (int64_t n = n0 + tid / 16; n < n1; n += 64) {
     int64_t lo, hi;
     slots(n, lo, hi);
     if (hi - lo > kFew) continue;
@@ -265,7 +262,7 @@ __global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p)
       if (tid % 16 == 15) sums[n * kSums + k] = v[k];
     }
   }
-  for (int64_t n = wave; n < p.seqs; n += 16) {
+  for (int64_t n = n0 + tid / 64; n < n1; n += 16) {
     int64_t lo, hi;
     slots(n, lo, hi);
     if (hi - lo <= kFew) continue;
@@ -280,7 +277,27 @@ __global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p)
       if (lane == 63) sums[n * kSums + k] = v[k];
     }
   }
-  __syncthreads();
+}
+
+// Many sequences: their sums by a grid, before the finish.
+__global__ __launch_bounds__(1024) void policy_sums_kernel(const PolicyArgs p) {
+  const int64_t n0 = (int64_t)blockIdx.x * kGroup;
+  add_slots(p, n0, n0 + kGroup < p.seqs ? n0 + kGroup : p.seqs,
+            [&](int64_t n) { return start_of(p, n); }, p.seq_sums);
+}
+
+__global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p) {
+  __shared__ double held[kInLds * kSums], slot2[16][2], slot4[16][4];
+  __shared__ int starts[kInLds + 1];
+  const int tid = threadIdx.x;
+  const double *sums = p.seq_sums;  // [seqs][kSums]
+  if (p.seqs <= kInLds) {
+    for (int n = tid; n <= (int)p.seqs; n += 1024) starts[n] = (int)start_of(p, n);
+    __syncthreads();
+    add_slots(p, 0, p.seqs, [&](int64_t n) { return (int64_t)starts[n]; }, held);
+    __syncthreads();
+    sums = held;
+  }
   double all[2] = {0.0, 0.0};  // scored tokens, sequences with any
   for (int64_t n = tid; n < p.seqs; n += 1024) {
     const double c = sums[n * kSums + 4];
@@ -369,6 +386,11 @@ hipError_t launch_policy_fwd(const PolicyArgs &a, hipStream_t stream) {
   const int64_t spans = (a.tokens + a.span - 1) / a.span;
   if (spans > 0) {
     const hipError_t e = run((const void *)policy_tokens_kernel, a, (spans + 3) / 4, 256, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (a.seqs > kInLds) {
+    const hipError_t e = run((const void *)policy_sums_kernel, a, (a.seqs + kGroup - 1) / kGroup,
+                             1024, stream);
     if (e != hipSuccess) return e;
   }
   return run((const void *)policy_finish_kernel, a, 1, 1024, stream);

@@ -156,7 +156,7 @@ gdn_status_t gdn_token_logprob_bwd(const gdn_logprob_shape_t *shape, const void 
                                    const float *entropy, const float *d_entropy,
                                    void *d_logits, void *stream);
 
-/* Host struct of the policy loss. Admitted: 0 <= tokens < 2^31; 1 <= seqs < 2^31;
+/* Host struct of the policy loss. Admitted: 0 <= tokens < 2^31; 0 <= seqs < 2^31;
  * 0 <= clip_low <= 1; clip_high >= 0; dual_clip 0 (off) or >= 1; coefficients finite. */
 typedef struct gdn_policy_shape {
   int64_t tokens, seqs;

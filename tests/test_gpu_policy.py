@@ -400,7 +400,7 @@ def cut(lengths):
     return np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
 
 
-POLICY_CASES = [("one", [1]), ("none scored", [5, 3]), ("tiny", [0, 1, 0, 0, 2, 1]),
+POLICY_CASES = [("many", [37] * 513 + [0, 2, 70000] + [5] * 700), ("one", [1]), ("none scored", [5, 3]), ("tiny", [0, 1, 0, 0, 2, 1]),
                 ("block edges", [256, 256, 255, 1, 257, 0, 513]), ("many short", [1] * 700),
                 ("many empty", [0] * 300 + [40] + [0] * 300 + [1, 0]), ("long", [5000, 1, 9000]),
                 ("mixed", [0, 3, 1000, 17, 2, 2, 2, 2500, 0])]
@@ -461,6 +461,13 @@ def test_policy_without_mask_and_offsets():
     no = torch.empty(0, device=DEV)
     stats, weight = api.policy_loss_fwd(no, no, no)
     assert stats.tolist() == [0.0] * 5 and weight.tolist() == [0.0]
+    none = torch.zeros(1, dtype=torch.int32, device=DEV)
+    stats, weight = api.policy_loss_fwd(no, no, no, cu_seqlens=none)
+    assert stats.tolist() == [0.0] * 5 and weight.tolist() == []
+    # no sequences and some tokens: none is any sequence's
+    stats, weight = api.policy_loss_fwd(up(logp), up(old), up(adv), cu_seqlens=none)
+    dl, _ = api.policy_loss_bwd(up(logp), up(old), up(adv), weight, cu_seqlens=none)
+    assert stats.tolist() == [0.0] * 5 and float(dl.abs().sum()) == 0.0
 
 
 def test_policy_long_batch():
@@ -522,6 +529,60 @@ def test_policy_bad_offsets_stay_inside():
         dl, _ = api.policy_loss_bwd(up(z), up(z), up(z), weight, cu_seqlens=c)
         torch.cuda.synchronize()
         assert dl.shape == (T,) and weight.shape == (3,)
+
+
+# ------------------------------------------------------------- buffers at odd elements
+
+def odd(t):
+    """The same values in a dense buffer that starts one element past an aligned place."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:]
+    flat.copy_(t.reshape(-1))
+    return flat.view(t.shape)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_buffers_at_odd_elements(dt):
+    dt = DTYPES[dt]
+    x, w, b, dy = (t.to(DEV) for t in norm_inputs(70, 1032, dt, dt, 61))
+    y, mean, rstd = api.layer_norm_fwd(x, w, b)
+    y1, _, _ = api.layer_norm_fwd(odd(x), odd(w), odd(b), y=odd(x))
+    same_bits(y1, y, "norm")
+    dx, dw, db = api.layer_norm_bwd(dy, x, w, mean, rstd)
+    out = dict(dx=odd(x), d_weight=odd(dw), d_bias=odd(db))
+    for p, q in zip(api.layer_norm_bwd(odd(dy), odd(x), odd(w), odd(mean), odd(rstd), **out),
+                    (dx, dw, db)):
+        same_bits(p, q, "norm backward")
+    xq, xs = api.quantize_rows(x)
+    xq1, xs1 = api.quantize_rows(odd(x), scale=odd(xs))
+    same_bits(xq1, xq, "quantised")
+    same_bits(xs1, xs, "scale")
+    for rows, cols in ((5, 70), (70, 3000), (3000, 3000)):
+        q = torch.randint(-127, 128, (max(rows, cols), 128), dtype=torch.int8).to(DEV)
+        s = torch.rand(max(rows, cols)).to(DEV)
+        want = api.linear_i8_fwd(q[:rows], s[:rows], q[:cols], s[:cols], out_dtype=dt)
+        got = api.linear_i8_fwd(q[:rows], odd(s[:rows]), q[:cols], odd(s[:cols]), y=odd(want))
+        same_bits(got, want, f"product {rows} x {cols}")
+    z, ids, dlp, de = (t.to(DEV) for t in lp_inputs(9, 5000, dt, 62))
+    logp, lse, ent = api.token_logprob_fwd(z, ids, entropy=True)
+    for p, q in zip(api.token_logprob_fwd(odd(z), odd(ids), entropy=True, logp=odd(lse),
+                                          lse=odd(lse)), (logp, lse, ent)):
+        same_bits(p, q, "logp")
+    kw = dict(entropy=ent, d_entropy=de)
+    same_bits(api.token_logprob_bwd(odd(z), odd(ids), odd(lse), odd(dlp), d_logits=odd(z), **kw),
+              api.token_logprob_bwd(z, ids, lse, dlp, **kw), "d_logits")
+
+
+def test_product_of_tiny_scales():
+    """Results among binary32's and bfloat16's subnormals are rounded, not flushed."""
+    g = gen(63)
+    xq = torch.randint(-127, 128, (300, 128), generator=g, dtype=torch.int8)
+    wq = torch.randint(-127, 128, (500, 128), generator=g, dtype=torch.int8)
+    xs, ws = torch.rand(300, generator=g) * 1e-20, torch.rand(500, generator=g) * 1e-23
+    for m in (3, 300):
+        for dt in (F32, BF16):
+            y = api.linear_i8_fwd(xq[:m].to(DEV), xs[:m].to(DEV), wq.to(DEV), ws.to(DEV),
+                                  out_dtype=dt)
+            same_bits(y.cpu(), R.linear_i8(xq[:m], xs[:m], wq, ws, dt), f"y {m} {dt}")
 
 
 # ------------------------------------------------------- element offsets past 2^31, bytes past 2^32

@@ -43,12 +43,12 @@ def norm_shape(rows=4, width=64, kind=0, x=F32, w=F32):
     return ctypes.byref(api.GdnNormShape(rows, width, kind, x, w))
 
 
-def nf(L, sh=None, x=FAKE, stride=64, w=FAKE, b=FAKE, eps=1e-5, y=FAKE, mean=FAKE, rstd=FAKE):
+def nf(L, sh=None, x=2 * FAKE, stride=64, w=FAKE, b=FAKE, eps=1e-5, y=FAKE, mean=FAKE, rstd=FAKE):
     return L.gdn_layer_norm_fwd(norm_shape() if sh is None else sh, x, stride, w, b, eps, y,
                                 mean, rstd, None)
 
 
-def nb(L, sh=None, dy=FAKE, ds=64, x=FAKE, xs=64, w=FAKE, mean=FAKE, rstd=FAKE, dx=FAKE,
+def nb(L, sh=None, dy=FAKE, ds=64, x=2 * FAKE, xs=64, w=FAKE, mean=FAKE, rstd=FAKE, dx=FAKE,
        dw=FAKE, db=FAKE, ws=FAKE, n=1 << 30):
     return L.gdn_layer_norm_bwd(norm_shape() if sh is None else sh, dy, ds, x, xs, w, mean,
                                 rstd, dx, dw, db, ws, n, None)
@@ -120,6 +120,9 @@ REFUSALS = [
     ("norm misaligned y", lambda L: nf(L, y=FAKE + 2), SHAPE),
     ("norm misaligned bf16 x", lambda L: nf(L, norm_shape(x=BF16), x=FAKE + 1), SHAPE),
     ("norm misaligned bias", lambda L: nf(L, b=FAKE + 2), SHAPE),
+    ("norm in place with a stride", lambda L: nf(L, x=FAKE, stride=80), SHAPE),
+    ("norm bwd in place with a stride", lambda L: nb(L, ds=80), SHAPE),
+    ("norm bwd dx is x", lambda L: nb(L, dx=2 * FAKE), SHAPE),
     ("norm bwd null dy", lambda L: nb(L, dy=None), NULL),
     ("norm bwd null d_weight", lambda L: nb(L, dw=None), NULL),
     ("norm bwd null mean", lambda L: nb(L, mean=None), NULL),
@@ -166,7 +169,8 @@ REFUSALS = [
     ("logprob bwd too large", lambda L: lb(L, lp_shape(rows=2**31 - 1, vocab=2**31 - 1)), SHAPE),
     ("policy null shape", lambda L: pf(L, NO_PO), NULL),
     ("policy tokens", lambda L: pf(L, po_shape(tokens=-1)), SHAPE),
-    ("policy no sequence", lambda L: pf(L, po_shape(seqs=0)), SHAPE),
+    ("policy negative sequences", lambda L: pf(L, po_shape(seqs=-1)), SHAPE),
+    ("policy no sequence, no cu_seqlens", lambda L: pf(L, po_shape(seqs=0), cu=None), NULL),
     ("policy reduction", lambda L: pf(L, po_shape(reduction=2)), UNSUP),
     ("policy clip_low over 1", lambda L: pf(L, po_shape(clip_low=1.5)), SHAPE),
     ("policy clip_high negative", lambda L: pf(L, po_shape(clip_high=-0.1)), SHAPE),
