@@ -544,7 +544,10 @@ hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t stream) {
                          dim3(args.row_threads * groups), kargs, 0, stream);
 }
 
-int64_t linear_i8_grid(const LinearI8Args &a) { return pick(a).grid; }
+int64_t linear_i8_threads(const LinearI8Args &a) {
+  const Launch go = pick(a);
+  return go.grid * go.threads;
+}
 
 hipError_t launch_linear_i8(const LinearI8Args &a, hipStream_t stream) {
   if (a.m == 0 || a.n == 0) return hipSuccess;

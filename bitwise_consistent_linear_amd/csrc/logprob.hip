@@ -183,36 +183,60 @@ __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobA
   }
 }
 
-hipError_t run(const void *fn, const LogprobArgs &a, int64_t grid, int threads,
+// A launch holds at most 2^32 - 1 threads, so more rows go in several: `fn` over runs of rows
+// of at most kMostThreads threads, `per` workgroups of `threads` for each row.
+constexpr int64_t kMostThreads = int64_t(1) << 31;
+
+hipError_t run(const void *fn, const LogprobArgs &a, int64_t per, int threads,
                hipStream_t stream) {
-  LogprobArgs args = a;
-  void *kargs[] = {&args};
-  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(threads), kargs, 0, stream);
+  const int64_t most = kMostThreads / (per * threads);  // at least 8: per is at most 2^20
+  const int64_t bytes = a.bf16 ? 2 : 4;
+  for (int64_t r = 0; r < a.rows; r += most) {
+    LogprobArgs args = a;
+    args.rows = a.rows - r < most ? a.rows - r : most;
+    auto past = [&](const void *p, int64_t by) {
+      return p ? static_cast<const char *>(p) + r * by : nullptr;
+    };
+    auto out = [&](float *p) { return p ? p + r : nullptr; };
+    args.logits = past(a.logits, a.stride * bytes);
+    args.ids = past(a.ids, a.id64 ? 8 : 4);
+    args.logp = out(a.logp);
+    args.lse = out(a.lse);
+    args.entropy = out(a.entropy);
+    args.d_logp = reinterpret_cast<const float *>(past(a.d_logp, 4));
+    args.d_entropy = reinterpret_cast<const float *>(past(a.d_entropy, 4));
+    args.d_logits = const_cast<char *>(past(a.d_logits, a.vocab * bytes));
+    void *kargs[] = {&args};
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(args.rows * per)), dim3(threads),
+                                         kargs, 0, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+int64_t bwd_spans(const LogprobArgs &a) {
+  const int64_t span = bwd_span(a.bf16);
+  return (a.vocab + span - 1) / span;
 }
 
 }  // namespace
 
 hipError_t launch_logprob_fwd(const LogprobArgs &a, hipStream_t stream) {
-  if (a.rows == 0) return hipSuccess;
   const void *fn = a.bf16 ? (a.entropy ? (const void *)logprob_fwd_kernel<true, true>
                                        : (const void *)logprob_fwd_kernel<true, false>)
                           : (a.entropy ? (const void *)logprob_fwd_kernel<false, true>
                                        : (const void *)logprob_fwd_kernel<false, false>);
-  return run(fn, a, a.rows, fwd_threads(a.vocab), stream);
+  return run(fn, a, 1, fwd_threads(a.vocab), stream);
 }
 
-int64_t logprob_bwd_grid(const LogprobArgs &a) {
-  const int64_t span = bwd_span(a.bf16);
-  return a.rows * ((a.vocab + span - 1) / span);
-}
+int64_t logprob_bwd_grid(const LogprobArgs &a) { return a.rows * bwd_spans(a); }
 
 hipError_t launch_logprob_bwd(const LogprobArgs &a, hipStream_t stream) {
-  if (a.rows == 0) return hipSuccess;
   const void *fn = a.bf16 ? (a.d_entropy ? (const void *)logprob_bwd_kernel<true, true>
                                          : (const void *)logprob_bwd_kernel<true, false>)
                           : (a.d_entropy ? (const void *)logprob_bwd_kernel<false, true>
                                          : (const void *)logprob_bwd_kernel<false, false>);
-  return run(fn, a, logprob_bwd_grid(a), kBwdThreads, stream);
+  return run(fn, a, bwd_spans(a), kBwdThreads, stream);
 }
 
 }  // namespace gdn

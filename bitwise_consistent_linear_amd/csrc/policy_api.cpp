@@ -3,14 +3,15 @@
 // untouched.
 
 #include <cmath>
-#include <string>
+#include <cstdio>
 
 #include "policy_internal.h"
 
 namespace gdn {
 namespace {
 
-thread_local std::string g_last_error;
+// A buffer of fixed size: an error's text allocates nothing, so no entry point can throw.
+thread_local char g_last_error[256];
 
 constexpr int64_t kMaxInt32 = 2147483647;
 // Strides are bounded so that rows * stride elements stay within 64-bit byte offsets.
@@ -21,13 +22,15 @@ bool known_dtype(int32_t d) { return d == GDN_DTYPE_F32 || d == GDN_DTYPE_BF16; 
 size_t bytes_of(int32_t d) { return d == GDN_DTYPE_BF16 ? 2 : 4; }
 
 gdn_status_t no(gdn_status_t st, const char *fn, const char *what) {
-  return fail(st, std::string(fn) + ": " + what);
+  std::snprintf(g_last_error, sizeof g_last_error, "%s: %s", fn, what);
+  return st;
 }
 
 gdn_status_t launched(const char *fn, hipError_t e) {
-  if (e != hipSuccess)
-    return fail(GDN_E_DEVICE, std::string(fn) + ": launch failed: " + hipGetErrorString(e));
-  return ok();
+  if (e == hipSuccess) return ok();
+  std::snprintf(g_last_error, sizeof g_last_error, "%s: launch failed: %s", fn,
+                hipGetErrorString(e));
+  return GDN_E_DEVICE;
 }
 
 bool any_misaligned(std::initializer_list<const void *> list, size_t bytes) {
@@ -146,13 +149,8 @@ gdn_status_t policy_inputs(const char *fn, const gdn_policy_shape_t *sh, const f
 
 }  // namespace
 
-gdn_status_t fail(gdn_status_t status, const std::string &message) {
-  g_last_error = message;
-  return status;
-}
-
 gdn_status_t ok() {
-  g_last_error.clear();
+  g_last_error[0] = 0;
   return GDN_OK;
 }
 
@@ -162,7 +160,7 @@ extern "C" {
 
 GDN_EXPORT int32_t gdn_policy_abi_version(void) { return GDN_POLICY_ABI_VERSION; }
 
-GDN_EXPORT const char *gdn_policy_last_error(void) { return gdn::g_last_error.c_str(); }
+GDN_EXPORT const char *gdn_policy_last_error(void) { return gdn::g_last_error; }
 
 GDN_EXPORT gdn_status_t gdn_layer_norm_fwd(const gdn_norm_shape_t *shape, const void *x,
                                            int64_t x_stride, const void *weight, const void *bias,
@@ -301,7 +299,7 @@ GDN_EXPORT gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, c
   a.x_scale = x_scale;
   a.w_scale = w_scale;
   a.y = y;
-  if (gdn::linear_i8_grid(a) > gdn::kMaxInt32)
+  if (gdn::linear_i8_threads(a) > int64_t(0xFFFFFFFF))
     return gdn::no(GDN_E_SHAPE, fn, "m * n is too large for one launch");
   return gdn::launched(fn, gdn::launch_linear_i8(a, static_cast<hipStream_t>(stream)));
 }

@@ -42,7 +42,7 @@ struct LinearI8Args {
   const float *x_scale, *w_scale;
   void *y;
 };
-int64_t linear_i8_grid(const LinearI8Args &args);
+int64_t linear_i8_threads(const LinearI8Args &args);  // of the launch; at most 2^32 - 1 fit one
 hipError_t launch_linear_i8(const LinearI8Args &args, hipStream_t stream);
 
 struct LogprobArgs {

@@ -37,7 +37,7 @@ struct Inputs {  // of one token
 };
 
 struct Token {
-  double ratio_adv, pg, kl, kl_slope;  // r A, -gain, exp(u) - u - 1, 1 - exp(u)
+  double ratio_adv, pg, kl, kl_slope;  // r A, -gain, exp(u) - 1 - u, 1 - exp(u)
   bool moves;
 };
 
@@ -63,7 +63,7 @@ __device__ __forceinline__ Token token_terms(const PolicyArgs &p, const Inputs &
   const double clamped = r < p.lo ? p.lo : (r > p.hi ? p.hi : r);
   const double plain = r * adv, clipped = clamped * adv;
   o.ratio_adv = plain;
-  o.moves = plain <= clipped;
+  o.moves = !(plain > clipped);  // a NaN stays one, in the loss and in the gradient
   double gain = o.moves ? plain : clipped;
   if (p.dual > 0.0 && adv < 0.0 && gain < p.dual * adv) {
     gain = p.dual * adv;
@@ -73,9 +73,15 @@ __device__ __forceinline__ Token token_terms(const PolicyArgs &p, const Inputs &
   o.kl = 0.0;
   o.kl_slope = 0.0;
   if (p.ref) {
+    // Policies near their reference have u next to 0, where exp(u) - 1 - u loses u^2 / 2 among
+    // the roundings of 1: below 2^-6 six terms of the series, the next under 2^-49 of the sum.
     const double u = (double)v.ref - lp, e = exp(u);
-    o.kl = e - u - 1.0;
-    o.kl_slope = 1.0 - e;
+    const double series =
+        u * u * fma(u, fma(u, fma(u, fma(u, fma(u, 1.0 / 5040, 1.0 / 720), 1.0 / 120), 1.0 / 24),
+                           1.0 / 6), 0.5);
+    const bool near = fabs(u) < 0x1p-6;
+    o.kl = near ? series : e - u - 1.0;
+    o.kl_slope = near ? -(u + series) : 1.0 - e;
   }
   return o;
 }
@@ -280,10 +286,13 @@ __device__ __forceinline__ void add_slots(const PolicyArgs &p, int64_t n0, int64
 }
 
 // Many sequences: their sums by a grid, before the finish.
+constexpr int64_t kSumsGrid = 1 << 16;  // workgroups; more sequences are walked over
+
 __global__ __launch_bounds__(1024) void policy_sums_kernel(const PolicyArgs p) {
-  const int64_t n0 = (int64_t)blockIdx.x * kGroup;
-  add_slots(p, n0, n0 + kGroup < p.seqs ? n0 + kGroup : p.seqs,
-            [&](int64_t n) { return start_of(p, n); }, p.seq_sums);
+  const int64_t step = (int64_t)gridDim.x * kGroup;
+  for (int64_t n0 = (int64_t)blockIdx.x * kGroup; n0 < p.seqs; n0 += step)
+    add_slots(p, n0, n0 + kGroup < p.seqs ? n0 + kGroup : p.seqs,
+              [&](int64_t n) { return start_of(p, n); }, p.seq_sums);
 }
 
 __global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p) {
@@ -389,8 +398,9 @@ hipError_t launch_policy_fwd(const PolicyArgs &a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (a.seqs > kInLds) {
-    const hipError_t e = run((const void *)policy_sums_kernel, a, (a.seqs + kGroup - 1) / kGroup,
-                             1024, stream);
+    const int64_t need = (a.seqs + kGroup - 1) / kGroup;
+    const hipError_t e = run((const void *)policy_sums_kernel, a,
+                             need < kSumsGrid ? need : kSumsGrid, 1024, stream);
     if (e != hipSuccess) return e;
   }
   return run((const void *)policy_finish_kernel, a, 1, 1024, stream);

@@ -113,7 +113,8 @@ gdn_status_t gdn_quantize_rows(const void *x, int64_t rows, int64_t k, int64_t x
  *   x_scale float [m], w_scale float [n]
  *   y [m, n]  : F32 or BF16
  * Admitted: 0 <= m, n < 2^31; k_pad a multiple of GDN_I8_K_ALIGN in [128, 65536] (the sum of
- * 65536 products of 8 bits fits 32 bits). m == 0 or n == 0 does nothing. */
+ * 65536 products of 8 bits fits 32 bits). m == 0 or n == 0 does nothing. GDN_E_SHAPE also where
+ * the tiles are too many for one launch (not under 2^30 rows or columns). */
 gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, const int8_t *xq,
                                const float *x_scale, const int8_t *wq, const float *w_scale,
                                int32_t y_dtype, void *y, void *stream);
@@ -172,7 +173,7 @@ gdn_status_t gdn_policy_loss_workspace(const gdn_policy_shape_t *shape, size_t *
 /* Clipped policy loss of a packed batch, per scored token, in binary64:
  *   r = exp(logp - old_logp),  gain = min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A)
  *   where A < 0 and dual_clip > 0: gain = max(gain, dual_clip A);  pg = -gain
- *   u = ref_logp - logp,  kl = exp(u) - u - 1
+ *   u = ref_logp - logp,  kl = exp(u) - u - 1 (next to u = 0 by its series)
  *   cut = 1 where gain is not r A (the token has no policy gradient), else 0
  * GDN_REDUCE_TOKEN: each scored token weighs 1 / (scored tokens); GDN_REDUCE_SEQUENCE: each
  * sequence with scored tokens weighs the same, and its scored tokens share its weight.

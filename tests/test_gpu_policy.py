@@ -517,6 +517,51 @@ def test_policy_at_the_clip_borders():
     R.check(dl, wl, torch.from_numpy(np.abs(wl) * R.POLICY_REL), "d_logp")
 
 
+def test_policy_next_to_the_reference():
+    """A policy a few steps of binary32 from its reference: the KL term and its slope keep
+    their relative accuracy, which exp(u) - u - 1 and 1 - exp(u) lose. Without an advantage
+    nothing else is in the gradient. u in binary64 is exact, the KL's series too, so what is
+    left are the outputs' roundings."""
+    logp = np.full(64, -1e-4, np.float32)
+    ref = logp.copy()
+    for i in range(1, 64):
+        ref[i] = np.nextafter(ref[i - 1], np.float32(0.0))
+    ref[-9:] = logp[-9:] + np.float32([2**-7, -2**-7, 2**-6, -2**-6, 0.0157, -0.0157, 0.1, -1, 2])
+    zero = np.zeros_like(logp)
+    up = lambda v: torch.from_numpy(v).to(DEV)  # noqa: E731
+    u = ref.astype(np.float64) - logp.astype(np.float64)
+    near = np.abs(u) < 0.1
+    kl = np.where(near, u**2 / 2 + u**3 / 6 + u**4 / 24 + u**5 / 120 + u**6 / 720 + u**7 / 5040
+                  + u**8 / 40320 + u**9 / 362880, np.expm1(u) - u)
+    for part in (slice(0, 55), slice(55, 64)):
+        kw = dict(ref_logp=up(ref[part].copy()), kl_coef=1.0)
+        args = [up(v[part].copy()) for v in (logp, logp, zero)]
+        stats, weight = api.policy_loss_fwd(*args, **kw)
+        dl, _ = api.policy_loss_bwd(*args, weight, **kw)
+        n = len(logp[part])
+        want = -np.expm1(u[part]) / n
+        R.check(dl, want, torch.from_numpy(np.abs(want) * R.POLICY_REL), "d_logp")
+        mean = float(kl[part].mean())
+        R.check(stats[2:3], torch.tensor([mean]), torch.tensor([mean * R.POLICY_REL]), "kl")
+
+
+def test_policy_nan_stays():
+    """A NaN among a scored token's inputs reaches the loss and that token's gradient alone."""
+    _, logp, old, adv, _, _, _ = policy_inputs("x", [300], 71)
+    up = lambda v: torch.from_numpy(v).to(DEV)  # noqa: E731
+    clean, weight = api.policy_loss_fwd(up(logp), up(old), up(adv))
+    want, _ = api.policy_loss_bwd(up(logp), up(old), up(adv), weight)
+    for k in range(3):
+        args = [v.copy() for v in (logp, old, adv)]
+        args[k][77] = np.nan
+        args = [up(v) for v in args]
+        stats, weight = api.policy_loss_fwd(*args)
+        dl, _ = api.policy_loss_bwd(*args, weight)
+        assert bool(stats[0].isnan()) and bool(stats[1].isnan()) and bool(dl[77].isnan())
+        dl[77] = want[77]
+        same_bits(dl, want, "the other tokens")
+
+
 def test_policy_bad_offsets_stay_inside():
     """Offsets that fall, go below zero or past the end give wrong numbers, nothing else: the
     kernels clamp every start to [0, T] and every slot is below the number of slots."""
@@ -641,6 +686,29 @@ def test_long_logits():
     d1 = api.token_logprob_bwd(tail, ids, lse1, dlp)
     d = api.token_logprob_bwd(z, every, lse, dl, d_logits=z)
     same_bits(d[-60:], d1, "d_logits' last rows")
+
+
+def test_more_rows_than_one_launch_holds():
+    """2^26 rows and some of a small vocabulary: more threads than one launch can have."""
+    M, V = 2**26 + 70, 5
+    z = torch.zeros((M, V), dtype=BF16, device=DEV)
+    tail, ids, dlp, de = (t.to(DEV) for t in lp_inputs(70, V, BF16, 54))
+    z[-70:] = tail
+    every = torch.zeros(M, dtype=torch.int32, device=DEV)
+    every[-70:] = ids
+    dl = torch.ones(M, device=DEV)
+    dl[-70:] = dlp
+    logp, lse, ent = api.token_logprob_fwd(z, every, entropy=True)
+    logp1, lse1, ent1 = api.token_logprob_fwd(tail, ids.to(torch.int32), entropy=True)
+    for p, q in ((logp, logp1), (lse, lse1), (ent, ent1)):
+        same_bits(p[-70:], q, "last rows")
+        assert bool((p[:-70] == p[0]).all())
+    dh = torch.zeros(M, device=DEV)
+    dh[-70:] = de
+    d1 = api.token_logprob_bwd(tail, ids, lse1, dlp, entropy=ent1, d_entropy=de)
+    d = api.token_logprob_bwd(z, every, lse, dl, entropy=ent, d_entropy=dh)
+    same_bits(d[-70:], d1, "last rows' gradient")
+    assert bool((d[:-70] == d[0]).all())
 
 
 # ------------------------------------------------------------ graphs, streams and refusals

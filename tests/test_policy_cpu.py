@@ -149,6 +149,8 @@ REFUSALS = [
     ("linear misaligned wq", lambda L: li(L, wq=FAKE + 4), SHAPE),
     ("linear misaligned y", lambda L: li(L, y=FAKE + 2), SHAPE),
     ("linear too many tiles", lambda L: li(L, m=2**31 - 1, n=2**31 - 1), SHAPE),
+    ("linear rows past one launch", lambda L: li(L, m=2**30, n=1), SHAPE),
+    ("linear columns past one launch", lambda L: li(L, m=1, n=2**31 - 1), SHAPE),
     ("logprob null shape", lambda L: lf(L, NO_LP), NULL),
     ("logprob vocab 0", lambda L: lf(L, lp_shape(vocab=0)), SHAPE),
     ("logprob rows", lambda L: lf(L, lp_shape(rows=-1)), SHAPE),
