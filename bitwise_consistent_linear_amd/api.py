@@ -653,102 +653,50 @@ def policy_abi_version() -> int:
     return policy_lib().gdn_policy_abi_version()
 
 
-def _code(dtype, name="out_dtype"):
-    f32, bf16 = _dtypes()[1]
-    if dtype is f32:
-        return GDN_DTYPE_F32
-    if dtype is bf16:
-        return GDN_DTYPE_BF16
-    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
-
-
-@lru_cache(maxsize=None)
-def _dtypes():
-    """(float32,), (float32, bfloat16), (int8,), (int32, int64), (bool, uint8)"""
-    t = _torch()
-    return ((t.float32,), (t.float32, t.bfloat16), (t.int8,), (t.int32, t.int64),
-            (t.bool, t.uint8))
-
-
-@lru_cache(maxsize=None)
-def _empty():
-    return _torch().empty
-
-
-@lru_cache(maxsize=None)
-def _stream_calls():
-    """(current device, raw current stream of a device)"""
-    torch = _torch()
-    return torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-
-
-# These calls take microseconds on the GPU, so their checks are one expression each; what is
-# wrong is found out only where something is.
-
 def _refuse(t, name, dtypes, shape, index):
+    """Raises for a tensor that is not a dense one of `shape` on GPU `index`."""
     _need(t, name, dtypes, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} is on {t.device}, expected GPU {index}")
 
 
-def _take(t, name, dtypes, shape, index):
-    """The pointer of a dense tensor of `shape` on GPU `index`."""
-    try:
-        if (t.dtype in dtypes and t.shape == shape and t.get_device() == index
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:  # no tensor
-        pass
-    _refuse(t, name, dtypes, shape, index)
-
-
-def _rows(t, name, dtypes):
-    """Row stride, device index of a GPU matrix whose rows are contiguous (stride 0 repeats a
-    row)."""
-    try:
-        index, dtype, shape, strides = t.get_device(), t.dtype, t.shape, t.stride()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch tensor") from None
-    if index < 0:
+def _refuse_rows(t, name, dtypes):
+    """Raises for a tensor that is not a GPU matrix whose rows are contiguous."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
-    if dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {dtype}, expected one of {dtypes}")
-    if len(shape) != 2:
-        raise ValueError(f"{name} must have 2 dimensions, got {tuple(shape)}")
-    if strides[1] != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must be contiguous inside a row, got strides {strides}")
-    return (strides[0] if shape[0] > 1 else shape[1]), index
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous inside a row, got strides {t.stride()}")
 
 
-def _place(t, name, dtype, shape, like, index):
-    """The caller's output, checked, or a new one."""
-    if t is None:
-        return _empty()(*shape, dtype=dtype, device=like.device)
-    _take(t, name, (dtype,), shape, index)
-    return t
+_policy_calls = None
 
 
-def _raw_stream(index):
-    """The current stream of GPU `index`, which has to be the current device: the library
-    launches there."""
-    device, stream = _stream_calls()
-    if device() != index:
-        raise ValueError(f"the tensors are on GPU {index}, the current device is {device()}")
-    return stream(index)
-
-
-def _workspace_ptr(t, need, like, index):
-    """(tensor to keep, pointer, bytes) of a uint8 workspace, the caller's or a new one of
-    need() bytes."""
-    torch = _torch()
-    if t is None:
-        n = need()
-        t = torch.empty(n, dtype=torch.uint8, device=like.device)
-        return t, t.data_ptr(), n
-    if _need(t, "workspace", (torch.uint8,), 1).get_device() != index:
-        raise ValueError(f"workspace is on {t.device}, expected GPU {index}")
-    return t, t.data_ptr(), t.numel()
+def _policy():
+    """The module that checks tensors, allocates outputs and enters libgdn_policy.so
+    (csrc/policy_binding.cpp): these calls take microseconds on the GPU, and so do as many
+    steps in Python. Raises if it has not been built."""
+    global _policy_calls
+    if _policy_calls is None:
+        torch = _torch()
+        policy_lib()
+        try:
+            from . import _policy_binding as calls
+        except ImportError as e:
+            raise RuntimeError("_policy_binding.so is missing or of another torch: build it "
+                               "with __graft_entry__.build()") from e
+        f32, bf16 = torch.float32, torch.bfloat16
+        calls.setup(torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _refuse,
+                    _refuse_rows, _need, GdnError,
+                    ((f32,), (f32, bf16), (torch.int8,), (torch.int32, torch.int64),
+                     (torch.bool, torch.uint8), (torch.int32,), (torch.uint8,), (bf16,)))
+        _policy_calls = calls
+    return _policy_calls
 
 
 def _elsewhere(stream, fn, *args, **kw):
@@ -758,9 +706,10 @@ def _elsewhere(stream, fn, *args, **kw):
 
 
 def _norm_kind(kind):
+    """Whether it is the layer norm."""
     if kind not in _NORM_KINDS:
         raise ValueError(f"kind must be 'layer' or 'rms', got {kind!r}")
-    return _NORM_KINDS[kind]
+    return _NORM_KINDS[kind] == GDN_NORM_LAYER
 
 
 def layer_norm_fwd(x, weight, bias=None, *, eps=1e-5, kind="layer", y=None, mean=None,
@@ -772,23 +721,7 @@ def layer_norm_fwd(x, weight, bias=None, *, eps=1e-5, kind="layer", y=None, mean
     if stream is not None:
         return _elsewhere(stream, layer_norm_fwd, x, weight, bias, eps=eps, kind=kind, y=y,
                           mean=mean, rstd=rstd)
-    f32, fl = _dtypes()[:2]
-    k = _norm_kind(kind)
-    stride, dev = _rows(x, "x", fl)
-    M, D = x.shape
-    w = _take(weight, "weight", fl, (D,), dev)
-    b = None if bias is None else _take(bias, "bias", (weight.dtype,), (D,), dev)
-    y = _place(y, "y", x.dtype, (M, D), x, dev)
-    if k == GDN_NORM_LAYER:
-        mean = _place(mean, "mean", f32[0], (M,), x, dev)
-    elif mean is not None:
-        raise ValueError("kind 'rms' has no mean")
-    rstd = _place(rstd, "rstd", f32[0], (M,), x, dev)
-    shape = GdnNormShape(M, D, k, _code(x.dtype), _code(weight.dtype))
-    _policy_check(policy_lib().gdn_layer_norm_fwd(
-        ctypes.byref(shape), x.data_ptr(), stride, w, b, eps, y.data_ptr(), _ptr(mean),
-        rstd.data_ptr(), _raw_stream(dev)))
-    return y, mean, rstd
+    return _policy().norm_fwd(x, weight, bias, eps, _norm_kind(kind), y, mean, rstd)
 
 
 def layer_norm_bwd_workspace_bytes(shape: GdnNormShape) -> int:
@@ -810,36 +743,11 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, kind="layer", bias=None, dx=Non
         return _elsewhere(stream, layer_norm_bwd, dy, x, weight, mean, rstd, kind=kind,
                           bias=bias, dx=dx, d_weight=d_weight, d_bias=d_bias,
                           workspace=workspace)
-    f32, fl = _dtypes()[:2]
-    k = _norm_kind(kind)
-    layer = k == GDN_NORM_LAYER
-    x_stride, dev = _rows(x, "x", fl)
-    dy_stride, dy_dev = _rows(dy, "dy", (x.dtype,))
-    if dy.shape != x.shape or dy_dev != dev:
-        raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} differ, in shape or GPU")
-    M, D = x.shape
-    w = _take(weight, "weight", fl, (D,), dev)
-    if layer:
-        _take(mean, "mean", f32, (M,), dev)
-    elif mean is not None:
-        raise ValueError("kind 'rms' has no mean")
-    rs = _take(rstd, "rstd", f32, (M,), dev)
-    dx = _place(dx, "dx", x.dtype, (M, D), x, dev)
-    d_weight = _place(d_weight, "d_weight", f32[0], (D,), x, dev)
+    layer = _norm_kind(kind)
     if bias is None:
         bias = layer or d_bias is not None
-    if bias:
-        d_bias = _place(d_bias, "d_bias", f32[0], (D,), x, dev)
-    elif d_bias is not None:
-        raise ValueError("d_bias is given but bias is False")
-    shape = GdnNormShape(M, D, k, _code(x.dtype), _code(weight.dtype))
-    ws, ws_ptr, ws_bytes = _workspace_ptr(
-        workspace, lambda: layer_norm_bwd_workspace_bytes(shape), x, dev)
-    _policy_check(policy_lib().gdn_layer_norm_bwd(
-        ctypes.byref(shape), dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, w, _ptr(mean),
-        rs, dx.data_ptr(), d_weight.data_ptr(), _ptr(d_bias), ws_ptr, ws_bytes,
-        _raw_stream(dev)))
-    return dx, d_weight, d_bias
+    return _policy().norm_bwd(dy, x, weight, mean, rstd, layer, bias, dx, d_weight, d_bias,
+                              workspace)
 
 
 def quantize_rows(x, *, xq=None, scale=None, stream=None):
@@ -849,15 +757,7 @@ def quantize_rows(x, *, xq=None, scale=None, stream=None):
     scale float32 [M])."""
     if stream is not None:
         return _elsewhere(stream, quantize_rows, x, xq=xq, scale=scale)
-    f32, fl, i8 = _dtypes()[:3]
-    stride, dev = _rows(x, "x", fl)
-    M, K = x.shape
-    xq = _place(xq, "xq", i8[0], (M, -(-K // I8_K_ALIGN) * I8_K_ALIGN), x, dev)
-    scale = _place(scale, "scale", f32[0], (M,), x, dev)
-    _policy_check(policy_lib().gdn_quantize_rows(
-        x.data_ptr(), M, K, stride, _code(x.dtype), xq.data_ptr(), scale.data_ptr(),
-        _raw_stream(dev)))
-    return xq, scale
+    return _policy().quantize_rows(x, xq, scale)
 
 
 def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, stream=None):
@@ -867,32 +767,12 @@ def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, stream=No
     if stream is not None:
         return _elsewhere(stream, linear_i8_fwd, xq, x_scale, wq, w_scale,
                           out_dtype=out_dtype, y=y)
-    f32, _, i8 = _dtypes()[:3]
-    _need(xq, "xq", i8, 2)
-    _need(wq, "wq", i8, 2)
-    M, K = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K:
-        raise ValueError(f"xq is {tuple(xq.shape)} but wq is {tuple(wq.shape)}")
-    dev = xq.get_device()
-    x_ptr, w_ptr = _take(xq, "xq", i8, (M, K), dev), _take(wq, "wq", i8, (N, K), dev)
-    xs = _take(x_scale, "x_scale", f32, (M,), dev)
-    ws = _take(w_scale, "w_scale", f32, (N,), dev)
+    torch = _torch()
     if out_dtype is None:
-        out_dtype = f32[0] if y is None else y.dtype
-    code = _code(out_dtype)
-    y = _place(y, "y", out_dtype, (M, N), xq, dev)
-    _policy_check(policy_lib().gdn_linear_i8_fwd(M, N, K, x_ptr, xs, w_ptr, ws, code,
-                                                 y.data_ptr(), _raw_stream(dev)))
-    return y
-
-
-def _logprob_args(logits, ids, scale):
-    _, fl, _, ints, _ = _dtypes()
-    stride, dev = _rows(logits, "logits", fl)
-    M, V = logits.shape
-    _take(ids, "ids", ints, (M,), dev)
-    return GdnLogprobShape(M, V, stride, _code(logits.dtype), ids.element_size(), scale), dev
+        out_dtype = torch.float32 if y is None else y.dtype
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+    return _policy().linear_i8(xq, x_scale, wq, w_scale, out_dtype is torch.bfloat16, y)
 
 
 def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=None,
@@ -904,16 +784,7 @@ def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=N
     if stream is not None:
         return _elsewhere(stream, token_logprob_fwd, logits, ids, scale=scale,
                           entropy=entropy, logp=logp, lse=lse)
-    f32 = _dtypes()[0][0]
-    shape, dev = _logprob_args(logits, ids, scale)
-    rows = (shape.rows,)
-    logp = _place(logp, "logp", f32, rows, logits, dev)
-    lse = _place(lse, "lse", f32, rows, logits, dev)
-    ent = _place(None, "entropy", f32, rows, logits, dev) if entropy else None
-    _policy_check(policy_lib().gdn_token_logprob_fwd(
-        ctypes.byref(shape), logits.data_ptr(), ids.data_ptr(), logp.data_ptr(),
-        lse.data_ptr(), _ptr(ent), _raw_stream(dev)))
-    return logp, lse, ent
+    return _policy().logprob_fwd(logits, ids, scale, entropy, logp, lse)
 
 
 def token_logprob_bwd(logits, ids, lse, d_logp, *, scale=1.0, entropy=None, d_entropy=None,
@@ -924,46 +795,13 @@ def token_logprob_bwd(logits, ids, lse, d_logp, *, scale=1.0, entropy=None, d_en
     if stream is not None:
         return _elsewhere(stream, token_logprob_bwd, logits, ids, lse, d_logp, scale=scale,
                           entropy=entropy, d_entropy=d_entropy, d_logits=d_logits)
-    f32 = _dtypes()[0]
-    shape, dev = _logprob_args(logits, ids, scale)
-    rows = (shape.rows,)
-    lse_ptr = _take(lse, "lse", f32, rows, dev)
-    dlp = _take(d_logp, "d_logp", f32, rows, dev)
-    ent = d_ent = None
-    if d_entropy is not None:
-        if entropy is None:
-            raise ValueError("d_entropy needs the entropy that token_logprob_fwd returned")
-        ent = _take(entropy, "entropy", f32, rows, dev)
-        d_ent = _take(d_entropy, "d_entropy", f32, rows, dev)
-    d_logits = _place(d_logits, "d_logits", logits.dtype, logits.shape, logits, dev)
-    _policy_check(policy_lib().gdn_token_logprob_bwd(
-        ctypes.byref(shape), logits.data_ptr(), ids.data_ptr(), lse_ptr, dlp, ent, d_ent,
-        d_logits.data_ptr(), _raw_stream(dev)))
-    return d_logits
+    return _policy().logprob_bwd(logits, ids, lse, d_logp, scale, entropy, d_entropy, d_logits)
 
 
-def _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens, clip_low,
-                 clip_high, dual_clip, kl_coef, entropy_coef, reduction):
-    """(GdnPolicyShape, device index, pointers up to cu_seqlens) of a policy loss call."""
-    f32, _, _, ints, flags = _dtypes()
+def _reduction(reduction):
     if reduction not in _REDUCTIONS:
         raise ValueError(f"reduction must be 'token' or 'sequence', got {reduction!r}")
-    _need(logp, "logp", f32, 1)
-    dev, tokens = logp.get_device(), logp.shape
-    N = 1
-    if cu_seqlens is not None:
-        N = cu_seqlens.shape[0] - 1
-    ptrs = (logp.data_ptr(), _take(old_logp, "old_logp", f32, tokens, dev),
-            _take(advantages, "advantages", f32, tokens, dev),
-            None if ref_logp is None else _take(ref_logp, "ref_logp", f32, tokens, dev),
-            None if entropy is None else _take(entropy, "entropy", f32, tokens, dev),
-            None if mask is None else _take(mask, "mask", flags, tokens, dev),
-            None if cu_seqlens is None else _take(cu_seqlens, "cu_seqlens", ints[:1], (N + 1,),
-                                                  dev))
-    return GdnPolicyShape(tokens[0], N, _REDUCTIONS[reduction], 0, clip_low, clip_high,
-                          0.0 if dual_clip is None else dual_clip,
-                          0.0 if ref_logp is None else kl_coef,
-                          0.0 if entropy is None else entropy_coef), dev, ptrs
+    return _REDUCTIONS[reduction]
 
 
 def policy_loss_workspace_bytes(shape: GdnPolicyShape) -> int:
@@ -989,18 +827,9 @@ def policy_loss_fwd(logp, old_logp, advantages, *, ref_logp=None, entropy=None, 
                           dual_clip=dual_clip, kl_coef=kl_coef, entropy_coef=entropy_coef,
                           reduction=reduction, stats=stats, weight=weight,
                           workspace=workspace)
-    f32 = _dtypes()[0][0]
-    shape, dev, ptrs = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask,
-                                    cu_seqlens, clip_low, clip_high, dual_clip, kl_coef,
-                                    entropy_coef, reduction)
-    stats = _place(stats, "stats", f32, (5,), logp, dev)
-    weight = _place(weight, "weight", f32, (shape.seqs,), logp, dev)
-    ws, ws_ptr, ws_bytes = _workspace_ptr(
-        workspace, lambda: policy_loss_workspace_bytes(shape), logp, dev)
-    _policy_check(policy_lib().gdn_policy_loss_fwd(
-        ctypes.byref(shape), *ptrs, stats.data_ptr(), weight.data_ptr(), ws_ptr, ws_bytes,
-        _raw_stream(dev)))
-    return stats, weight
+    return _policy().policy_fwd(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
+                                _reduction(reduction), clip_low, clip_high, dual_clip, kl_coef,
+                                entropy_coef, stats, weight, workspace)
 
 
 def policy_loss_bwd(logp, old_logp, advantages, weight, *, ref_logp=None, entropy=None,
@@ -1017,17 +846,6 @@ def policy_loss_bwd(logp, old_logp, advantages, weight, *, ref_logp=None, entrop
                           dual_clip=dual_clip, kl_coef=kl_coef, entropy_coef=entropy_coef,
                           reduction=reduction, d_loss=d_loss, d_logp=d_logp,
                           d_entropy=d_entropy)
-    f32 = _dtypes()[0]
-    shape, dev, ptrs = _policy_args(logp, old_logp, advantages, ref_logp, entropy, mask,
-                                    cu_seqlens, clip_low, clip_high, dual_clip, kl_coef,
-                                    entropy_coef, reduction)
-    w = _take(weight, "weight", f32, (shape.seqs,), dev)
-    d_logp = _place(d_logp, "d_logp", f32[0], logp.shape, logp, dev)
-    if entropy is not None:
-        d_entropy = _place(d_entropy, "d_entropy", f32[0], logp.shape, logp, dev)
-    elif d_entropy is not None:
-        raise ValueError("d_entropy is given without an entropy")
-    _policy_check(policy_lib().gdn_policy_loss_bwd(
-        ctypes.byref(shape), *ptrs[:4], *ptrs[5:], w, d_loss, d_logp.data_ptr(),
-        _ptr(d_entropy), _raw_stream(dev)))
-    return d_logp, d_entropy
+    return _policy().policy_bwd(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
+                                _reduction(reduction), clip_low, clip_high, dual_clip, kl_coef,
+                                entropy_coef, weight, d_loss, d_logp, d_entropy)

@@ -39,6 +39,7 @@ FLAGS = [
 
 
 POLICY_LIB = os.path.join(PKG, "libgdn_policy.so")
+POLICY_BINDING = os.path.join(PKG, "_policy_binding.so")
 POLICY_SOURCES = ["norm.hip", "linear_i8.hip", "logprob.hip", "policy_loss.hip", "policy_api.cpp"]
 
 
@@ -87,7 +88,9 @@ def build_policy(verbose: bool = False) -> str:
     """Build bitwise_consistent_linear_amd/libgdn_policy.so, the policy-head operators, with
     the same flags; return its path. A library of its own: libgdn_cpr.so holds exactly the
     contract's entry points and only its binary32 instructions."""
-    return _build(POLICY_SOURCES, POLICY_LIB, verbose)
+    lib = _build(POLICY_SOURCES, POLICY_LIB, verbose)
+    build_policy_binding(verbose)
+    return lib
 
 
 PROBE_LIB = os.path.join(PKG, "libgdn_probe.so")
@@ -109,6 +112,34 @@ def build_probe(verbose: bool = False) -> str:
 
 
 KERNEL_SOURCES = [s for s in SOURCES if s.endswith(".hip")]
+
+
+def build_policy_binding(verbose: bool = False) -> str:
+    """Build _policy_binding.so, the policy head's Python calls, against the installed torch;
+    return its path. Host code only. libgdn_policy.so is found beside it."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.join(os.path.dirname(torch.__file__))
+    abi = int(torch.compiled_with_cxx11_abi())
+    tmp = POLICY_BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE,
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "policy_binding.cpp"), "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-L", PKG, "-l:" + os.path.basename(POLICY_LIB), "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("failed to build _policy_binding.so")
+    os.replace(tmp, POLICY_BINDING)
+    return POLICY_BINDING
 
 
 def device_asm(out_path: str, sources=None) -> str:

@@ -243,6 +243,29 @@ def test_library_missing_is_an_error(monkeypatch, tmp_path):
         api.policy_lib()
 
 
+def test_binding_missing_is_an_error(monkeypatch):
+    import sys
+
+    import bitwise_consistent_linear_amd as package
+    monkeypatch.setattr(api, "_policy_calls", None)
+    monkeypatch.delattr(package, "_policy_binding", raising=False)
+    monkeypatch.setitem(sys.modules, package.__name__ + "._policy_binding", None)
+    with pytest.raises(RuntimeError, match="_policy_binding"):
+        api.quantize_rows(torch.zeros(4, 8))
+
+
+def test_binding_refuses_wrong_calls():
+    """The module's own checks: the number of arguments, and values that are no numbers."""
+    calls = api._policy()
+    with pytest.raises(TypeError, match="number of arguments"):
+        calls.quantize_rows(torch.zeros(4, 8))
+    with pytest.raises(TypeError, match="setup takes"):
+        calls.setup(1, 2)
+    for bad in (torch.zeros(4, 8), None, 3, torch.zeros(4, 8, dtype=torch.bfloat16).to_sparse()):
+        with pytest.raises((TypeError, ValueError)):
+            api.layer_norm_fwd(bad, torch.ones(8))
+
+
 @pytest.fixture(scope="module")
 def asm(tmp_path_factory):
     path = str(tmp_path_factory.mktemp("isa") / "policy.s")
