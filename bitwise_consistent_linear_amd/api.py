@@ -630,7 +630,8 @@ def policy_lib():
             "gdn_layer_norm_bwd": [NS, P, I64, P, I64, P, P, P, P, P, P, P, SZ, P],
             "gdn_quantize_rows": [P, I64, I64, I64, I32, P, P, P],
             "gdn_linear_i8_fwd": [I64, I64, I64, P, P, P, P, I32, P, P],
-            "gdn_token_logprob_fwd": [LS, P, P, P, P, P, P],
+            "gdn_token_logprob_fwd_workspace": [LS, SZP],
+            "gdn_token_logprob_fwd": [LS, P, P, P, P, P, P, SZ, P],
             "gdn_token_logprob_bwd": [LS, P, P, P, P, P, P, P, P],
             "gdn_policy_loss_workspace": [PS, SZP],
             "gdn_policy_loss_fwd": [PS, P, P, P, P, P, P, P, P, P, P, SZ, P],
@@ -775,16 +776,26 @@ def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, stream=No
     return _policy().linear_i8(xq, x_scale, wq, w_scale, out_dtype is torch.bfloat16, y)
 
 
+def token_logprob_fwd_workspace_bytes(shape: GdnLogprobShape) -> int:
+    """gdn_token_logprob_fwd_workspace: device bytes the log-probabilities need (often 0)."""
+    n = ctypes.c_size_t(0)
+    _policy_check(policy_lib().gdn_token_logprob_fwd_workspace(ctypes.byref(shape),
+                                                               ctypes.byref(n)))
+    return n.value
+
+
 def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=None,
-                      stream=None):
+                      workspace=None, stream=None):
     """gdn_token_logprob_fwd: log-probability of token ids [M] (int32 or int64) under the
     softmax of scale * logits [M, V] (float32 or bfloat16; rows may have a stride), the
     log-sum-exp, and with entropy=True the entropy. Rows whose id is outside [0, V) are not
-    scored: zeros. Returns (logp [M], lse [M], entropy [M] or None), float32."""
+    scored: zeros. ``workspace`` is a uint8 GPU tensor of at least
+    token_logprob_fwd_workspace_bytes() bytes (allocated here when omitted).
+    Returns (logp [M], lse [M], entropy [M] or None), float32."""
     if stream is not None:
         return _elsewhere(stream, token_logprob_fwd, logits, ids, scale=scale,
-                          entropy=entropy, logp=logp, lse=lse)
-    return _policy().logprob_fwd(logits, ids, scale, entropy, logp, lse)
+                          entropy=entropy, logp=logp, lse=lse, workspace=workspace)
+    return _policy().logprob_fwd(logits, ids, scale, entropy, logp, lse, workspace)
 
 
 def token_logprob_bwd(logits, ids, lse, d_logp, *, scale=1.0, entropy=None, d_entropy=None,

@@ -1,12 +1,14 @@
 // Log-probability of the chosen token of each row of logits, and its gradient, on gfx950.
 //
-// Forward: bound by the one read of the logits. A workgroup takes a row; each thread keeps a
-// running maximum m of its logits and, relative to it, the sums s of the exponentials and t
-// of the exponentials times the differences, the next tile's loads in flight under this one's
-// arithmetic; the threads' triples are then merged over lanes and waves in a fixed order. lse = scale m + log s, logp = scale (v[id] - m) - log s,
-// entropy = log s - scale t / s: differences from the maximum keep what differences of large
-// logits would lose. The order depends on the vocabulary alone, so a row has the same bits
-// in any batch.
+// Forward: bound by the one read of the logits (8192 x 65536 bf16 with entropies 168 us, 6.0
+// TB/s). A workgroup takes a row; each thread keeps a running maximum m of its logits and,
+// relative to it, the sums s of the exponentials and t of the exponentials times the
+// differences, the next tile's loads in flight under this one's arithmetic; the threads' triples
+// are then merged over lanes and waves in a fixed order. lse = scale m + log s, logp =
+// scale (v[id] - m) - log s, entropy = log s - scale t / s: differences from the maximum keep
+// what differences of large logits would lose. A few rows of a long vocabulary are split over
+// workgroups at fixed places where the sums begin anew in either way, so the order depends on
+// the vocabulary alone and a row has the same bits in any batch.
 //
 // Backward: elementwise in the logits, bound by reading them and writing the gradient: 8192 x
 // 65536 bf16 with the entropy's term 348 us (6.0 TB/s), 1021 x 50021 binary32 74 us (5.3 TB/s).
@@ -55,48 +57,34 @@ __device__ __forceinline__ Softmax over_lanes(Softmax a, float c) {
   return a;
 }
 
-// Eight logits of a row at [col, col + 8), -infinity past its end.
-template <bool B16>
-__device__ __forceinline__ void load_logits(Vec8<B16> &v, const void *base, int64_t off,
-                                            int64_t col, int64_t vocab) {
-  if (col + 8 <= vocab) {
-    v.load(base, off + col);
-  } else {
-    const int n = col < vocab ? (int)(vocab - col) : 0;
-    v.load_part(base, off + col, n, kNegInf);
-  }
+// Two sets of logits together.
+__device__ __forceinline__ void merge(Softmax &a, Softmax b, float c) {
+  const float top = fmaxf(a.m, b.m);
+  rebase(a, top, c);
+  rebase(b, top, c);
+  a.s += b.s;
+  a.t += b.t;
 }
 
+// A thread's 32 logits of a tile: four runs of eight, a tile's runs `threads` apart,
+// -infinity past the row's end.
 constexpr int kFwdVecs = 4;
-
-template <bool B16, bool ENT>
-__global__ __launch_bounds__(512) void logprob_fwd_kernel(const LogprobArgs p) {
-  __shared__ Softmax part[8];
-  const int64_t row = blockIdx.x, V = p.vocab;
-  const int threads = blockDim.x, lane = threadIdx.x % 64, waves = threads / 64;
-  const int64_t id = id_of(p, row);
-  if (id < 0 || id >= V) {
-    if (threadIdx.x == 0) {
-      p.logp[row] = p.lse[row] = 0.0f;
-      if (ENT) p.entropy[row] = 0.0f;
-    }
-    return;
-  }
-  const int64_t off = row * p.stride;
-  const float c = p.scale_log2e;
-  const float chosen = B16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[off + id])
-                           : static_cast<const float *>(p.logits)[off + id];
-  const int64_t tile = (int64_t)threads * 8 * kFwdVecs;
-  auto load = [&](Vec8<B16> (&x)[kFwdVecs], int64_t c0) {
+template <bool B16>
+struct Tile {
+  Vec8<B16> x[kFwdVecs];
+  __device__ __forceinline__ void load(const LogprobArgs &p, int64_t off, int64_t c0) {
 #pragma unroll
-    for (int j = 0; j < kFwdVecs; ++j)
-      load_logits(x[j], p.logits, off, c0 + 8 * (int64_t)(j * threads + threadIdx.x), V);
-  };
-  Softmax a{kLowest, 0.0f, 0.0f};
-  Vec8<B16> x[kFwdVecs], next[kFwdVecs];
-  load(x, 0);
-  for (int64_t c0 = 0; c0 < V; c0 += tile) {
-    if (c0 + tile < V) load(next, c0 + tile);
+    for (int j = 0; j < kFwdVecs; ++j) {
+      const int64_t col = c0 + 8 * (int64_t)(j * (int)blockDim.x + (int)threadIdx.x);
+      if (col + 8 <= p.vocab)
+        x[j].load(p.logits, off + col);
+      else
+        x[j].load_part(p.logits, off + col, col < p.vocab ? (int)(p.vocab - col) : 0, kNegInf);
+    }
+  }
+  // the thread's logits into a
+  template <bool ENT>
+  __device__ __forceinline__ void add_to(Softmax &a, float c) const {
     float top = a.m;
 #pragma unroll
     for (int j = 0; j < kFwdVecs; ++j)
@@ -111,34 +99,126 @@ __global__ __launch_bounds__(512) void logprob_fwd_kernel(const LogprobArgs p) {
         a.s += k;
         if (ENT) a.t = fmaf(k, fmaxf(d, kFar), a.t);
       }
-#pragma unroll
-    for (int j = 0; j < kFwdVecs; ++j) x[j] = next[j];
   }
+};
+
+// Tiles that a thread adds up from nothing before it merges the sum into its row's: 65536
+// values of a workgroup of 512 threads. Rows of more can be split there with the same bits.
+constexpr int kGroupTiles = 4, kMostFwdThreads = 512;
+constexpr int64_t kGroupValues = (int64_t)kGroupTiles * kMostFwdThreads * 8 * kFwdVecs;
+
+// A thread's logits of a row from `from` to `end`, groups of tiles in turn.
+template <bool B16, bool ENT>
+__device__ __forceinline__ Softmax thread_sums(const LogprobArgs &p, int64_t off, int64_t from,
+                                               int64_t end) {
+  const int64_t tile = (int64_t)blockDim.x * 8 * kFwdVecs;
+  const float c = p.scale_log2e;
+  Softmax a{kLowest, 0.0f, 0.0f}, g = a;
+  Tile<B16> x, next;
+  x.load(p, off, from);
+  int tiles = 0;
+  for (int64_t c0 = from; c0 < end; c0 += tile) {
+    if (c0 + tile < end) next.load(p, off, c0 + tile);
+    x.template add_to<ENT>(g, c);
+    if (++tiles == kGroupTiles) {
+      merge(a, g, c);
+      g = Softmax{kLowest, 0.0f, 0.0f};
+      tiles = 0;
+    }
+    x = next;
+  }
+  if (tiles > 0) merge(a, g, c);
+  return a;
+}
+
+__device__ __forceinline__ bool scored(const LogprobArgs &p, int64_t id) {
+  return id >= 0 && id < p.vocab;
+}
+
+__device__ __forceinline__ float logit_of(const LogprobArgs &p, int64_t at) {
+  return p.bf16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[at])
+                : static_cast<const float *>(p.logits)[at];
+}
+
+// The outputs of a row from all its logits and the chosen one; none: it is not scored.
+template <bool ENT>
+__device__ __forceinline__ void put_row(const LogprobArgs &p, int64_t row, bool none, Softmax a,
+                                        float chosen) {
+  const float ls = logf(a.s);
+  const bool empty = a.s == 0.0f;  // every logit is -inf
+  p.lse[row] = none ? 0.0f : empty ? kNegInf : fmaf(a.m, p.scale, ls);
+  p.logp[row] = none ? 0.0f : empty ? kNegInf : fmaf(chosen - a.m, p.scale, -ls);
+  if (ENT) p.entropy[row] = none || empty ? 0.0f : fmaf(-a.t / a.s, p.scale, ls);
+}
+
+// The threads' sums of a row together and its outputs: lanes, then waves.
+template <bool ENT>
+__device__ __forceinline__ void finish_row(const LogprobArgs &p, int64_t row, Softmax a,
+                                           float chosen) {
+  __shared__ Softmax part[8];
+  const int lane = threadIdx.x % 64, waves = (int)blockDim.x / 64;
+  const float c = p.scale_log2e;
   a = over_lanes(a, c);
   if (waves > 1) {
     if (lane == 0) part[threadIdx.x / 64] = a;
     __syncthreads();
     if (threadIdx.x >= 64) return;
-    a = lane < waves ? part[lane] : Softmax{kLowest, 0.0f, 0.0f};
-    a = over_lanes(a, c);
+    a = over_lanes(lane < waves ? part[lane] : Softmax{kLowest, 0.0f, 0.0f}, c);
   }
-  if (threadIdx.x == 0) {
-    const float ls = logf(a.s);
-    const bool none = a.s == 0.0f;  // every logit is -inf
-    p.lse[row] = none ? kNegInf : fmaf(a.m, p.scale, ls);
-    p.logp[row] = none ? kNegInf : fmaf(chosen - a.m, p.scale, -ls);
-    if (ENT) p.entropy[row] = none ? 0.0f : fmaf(-a.t / a.s, p.scale, ls);
+  if (threadIdx.x == 0) put_row<ENT>(p, row, false, a, chosen);
+}
+
+// A row by a workgroup.
+template <bool B16, bool ENT>
+__global__ __launch_bounds__(kMostFwdThreads) void logprob_fwd_kernel(const LogprobArgs p) {
+  const int64_t row = blockIdx.x, id = id_of(p, row);
+  if (!scored(p, id)) {
+    if (threadIdx.x == 0) put_row<ENT>(p, row, true, Softmax{0.0f, 0.0f, 0.0f}, 0.0f);
+    return;
   }
+  const int64_t off = row * p.stride;
+  const float chosen = logit_of(p, off + id);
+  finish_row<ENT>(p, row, thread_sums<B16, ENT>(p, off, 0, p.vocab), chosen);
+}
+
+// A group of tiles of a row by a workgroup, its threads' sums put down for the next kernel:
+// 6 KiB for the group's 128 or 256.
+template <bool B16, bool ENT>
+__global__ __launch_bounds__(kMostFwdThreads) void logprob_groups_kernel(const LogprobArgs p) {
+  const int64_t row = blockIdx.x / p.groups, from = blockIdx.x % p.groups * kGroupValues;
+  if (!scored(p, id_of(p, row))) return;
+  const int64_t end = p.vocab - from < kGroupValues ? p.vocab : from + kGroupValues;
+  const Softmax a = thread_sums<B16, ENT>(p, row * p.stride, from, end);
+  float *part = p.parts + (int64_t)blockIdx.x * 3 * kMostFwdThreads + threadIdx.x;
+  part[0] = a.m;
+  part[kMostFwdThreads] = a.s;
+  if (ENT) part[2 * kMostFwdThreads] = a.t;
+}
+
+// The groups of a row together, each thread's in turn as the kernel of a whole row adds them:
+// the same bits.
+template <bool ENT>
+__global__ __launch_bounds__(kMostFwdThreads) void logprob_join_kernel(const LogprobArgs p) {
+  const int64_t row = blockIdx.x, id = id_of(p, row);
+  if (!scored(p, id)) {
+    if (threadIdx.x == 0) put_row<ENT>(p, row, true, Softmax{0.0f, 0.0f, 0.0f}, 0.0f);
+    return;
+  }
+  const float c = p.scale_log2e, chosen = logit_of(p, row * p.stride + id);
+  const float *part = p.parts + row * p.groups * 3 * kMostFwdThreads + threadIdx.x;
+  Softmax a{kLowest, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int64_t g = 0; g < p.groups; ++g, part += 3 * kMostFwdThreads)
+    merge(a, Softmax{part[0], part[kMostFwdThreads], ENT ? part[2 * kMostFwdThreads] : 0.0f}, c);
+  finish_row<ENT>(p, row, a, chosen);
 }
 
 // Threads of a row, by the vocabulary alone: one tile of 32 values a thread up to 8192 values
 // and 512 threads from there. 8192 rows of 65536 bf16 values take 179 us at 512 threads (6.0
-// TB/s), 191 at 256 and 221 at 1024; of 2048 values 11.0 us at 64 threads, 44 at 512. A row
-// by itself is bound by what one compute unit can fetch: 131072 binary32 values take 12 us.
+// TB/s), 191 at 256 and 221 at 1024; of 2048 values 11.0 us at 64 threads, 44 at 512.
 int fwd_threads(int64_t vocab) {
-  return vocab <= 2048 ? 64 : vocab <= 4096 ? 128 : vocab <= 8192 ? 256 : 512;
+  return vocab <= 2048 ? 64 : vocab <= 4096 ? 128 : vocab <= 8192 ? 256 : kMostFwdThreads;
 }
-
 // Runs of eight values a thread: 32 bytes of either type (4096 x 65536 binary32 takes 344 us
 // with one run and 372 with two, 8192 x 65536 bf16 355 with two and 402 with one).
 constexpr int kBwdThreads = 256;
@@ -206,6 +286,7 @@ hipError_t run(const void *fn, const LogprobArgs &a, int64_t per, int threads,
     args.d_logp = reinterpret_cast<const float *>(past(a.d_logp, 4));
     args.d_entropy = reinterpret_cast<const float *>(past(a.d_entropy, 4));
     args.d_logits = const_cast<char *>(past(a.d_logits, a.vocab * bytes));
+    args.parts = a.parts ? a.parts + r * a.groups * 3 * kMostFwdThreads : nullptr;
     void *kargs[] = {&args};
     const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(args.rows * per)), dim3(threads),
                                          kargs, 0, stream);
@@ -221,12 +302,39 @@ int64_t bwd_spans(const LogprobArgs &a) {
 
 }  // namespace
 
+// Groups that a row is split into, 0 where a workgroup takes it whole. A row by itself is bound
+// by the arithmetic of its compute unit (1.2 us for 16384 values of either type), so a few long
+// rows leave the others idle; the second kernel costs 3 us. 8 rows in the two ways, whole and
+// split: of 131072 binary32 values 10.1 and 9.2 us, of 262144 21.6 and 11.2, of 300001 25.7
+// and 11.4; 64 rows of 262144 25.0 and 16.8, 128 rows 26.7 and 26.2, 256 rows 41 and 45.
+int64_t split_groups(const LogprobArgs &a) {
+  const bool split = a.rows <= 64 && a.vocab > kGroupValues / 2 * 3;
+  return split ? (a.vocab + kGroupValues - 1) / kGroupValues : 0;
+}
+
+int64_t logprob_parts_bytes(const LogprobArgs &a) {
+  return a.rows * split_groups(a) * 3 * kMostFwdThreads * (int64_t)sizeof(float);
+}
+
 hipError_t launch_logprob_fwd(const LogprobArgs &a, hipStream_t stream) {
+  LogprobArgs args = a;
+  args.groups = split_groups(a);
+  if (args.groups > 0) {
+    const void *fn = a.bf16 ? (a.entropy ? (const void *)logprob_groups_kernel<true, true>
+                                         : (const void *)logprob_groups_kernel<true, false>)
+                            : (a.entropy ? (const void *)logprob_groups_kernel<false, true>
+                                         : (const void *)logprob_groups_kernel<false, false>);
+    const hipError_t e = run(fn, args, args.groups, kMostFwdThreads, stream);
+    if (e != hipSuccess) return e;
+    return run(a.entropy ? (const void *)logprob_join_kernel<true>
+                         : (const void *)logprob_join_kernel<false>,
+               args, 1, kMostFwdThreads, stream);
+  }
   const void *fn = a.bf16 ? (a.entropy ? (const void *)logprob_fwd_kernel<true, true>
                                        : (const void *)logprob_fwd_kernel<true, false>)
                           : (a.entropy ? (const void *)logprob_fwd_kernel<false, true>
                                        : (const void *)logprob_fwd_kernel<false, false>);
-  return run(fn, a, 1, fwd_threads(a.vocab), stream);
+  return run(fn, args, 1, fwd_threads(a.vocab), stream);
 }
 
 int64_t logprob_bwd_grid(const LogprobArgs &a) { return a.rows * bwd_spans(a); }

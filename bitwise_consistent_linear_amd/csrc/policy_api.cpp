@@ -304,9 +304,21 @@ GDN_EXPORT gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, c
   return gdn::launched(fn, gdn::launch_linear_i8(a, static_cast<hipStream_t>(stream)));
 }
 
+GDN_EXPORT gdn_status_t gdn_token_logprob_fwd_workspace(const gdn_logprob_shape_t *shape,
+                                                        size_t *bytes) {
+  const char *fn = "gdn_token_logprob_fwd_workspace";
+  if (!bytes) return gdn::no(GDN_E_NULL, fn, "bytes is NULL");
+  gdn::LogprobArgs a;
+  gdn_status_t st = gdn::logprob_shape(fn, shape, a);
+  if (st != GDN_OK) return st;
+  *bytes = (size_t)gdn::logprob_parts_bytes(a);
+  return gdn::ok();
+}
+
 GDN_EXPORT gdn_status_t gdn_token_logprob_fwd(const gdn_logprob_shape_t *shape, const void *logits,
                                               const void *ids, float *logp, float *lse,
-                                              float *entropy, void *stream) {
+                                              float *entropy, void *workspace,
+                                              size_t workspace_bytes, void *stream) {
   const char *fn = "gdn_token_logprob_fwd";
   gdn::LogprobArgs a;
   gdn_status_t st = gdn::logprob_shape(fn, shape, a);
@@ -317,6 +329,13 @@ GDN_EXPORT gdn_status_t gdn_token_logprob_fwd(const gdn_logprob_shape_t *shape, 
   if (!gdn::aligned(logits, gdn::bytes_of(shape->logits_dtype)) ||
       !gdn::aligned(ids, shape->id_bytes) || gdn::any_misaligned({logp, lse, entropy}, 4))
     return gdn::no(GDN_E_SHAPE, fn, "a buffer is not aligned to its element");
+  const int64_t need = gdn::logprob_parts_bytes(a);
+  if (need > 0 && !workspace) return gdn::no(GDN_E_NULL, fn, "workspace is required");
+  if (need > 0 && !gdn::aligned(workspace, 4))
+    return gdn::no(GDN_E_SHAPE, fn, "workspace must be 4-byte aligned");
+  if (workspace_bytes < (size_t)need)
+    return gdn::no(GDN_E_SHAPE, fn, "workspace smaller than gdn_token_logprob_fwd_workspace reports");
+  a.parts = static_cast<float *>(workspace);
   a.logits = logits;
   a.ids = ids;
   a.logp = logp;

@@ -170,6 +170,7 @@ Workspace workspace(PyObject *o, int dev, Size size) {
   }
   size_t bytes = 0;
   check(size(&bytes));
+  if (bytes == 0) return {at::Tensor(), nullptr, 0};
   at::Tensor t = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(
                                                  at::kCUDA, (at::DeviceIndex)dev));
   void *p = t.data_ptr();
@@ -306,14 +307,17 @@ Logits logits_of(PyObject *logits, PyObject *ids, PyObject *scale) {
                       (int32_t)THPVariable_Unpack(ids).element_size(), number(scale)}};
 }
 
-// logprob_fwd(logits, ids, scale, entropy, logp, lse)
+// logprob_fwd(logits, ids, scale, entropy, logp, lse, workspace)
 PyObject *logprob_fwd(PyObject *const *a) {
   const Logits g = logits_of(a[0], a[1], a[2]);
   const int64_t M = g.shape.rows;
   Out none, logp(a[4], "logp", at::kFloat, {M}, g.dev), lse(a[5], "lse", at::kFloat, {M}, g.dev);
+  const Workspace ws = workspace(
+      a[6], g.dev, [&](size_t *n) { return gdn_token_logprob_fwd_workspace(&g.shape, n); });
   auto call = [&](Out &ent) {
     check(gdn_token_logprob_fwd(&g.shape, g.z.t.data_ptr(), g.ids, logp.get<float>(),
-                                lse.get<float>(), ent.get<float>(), stream_of(g.dev)));
+                                lse.get<float>(), ent.get<float>(), ws.ptr, ws.bytes,
+                                stream_of(g.dev)));
     return tuple(logp, lse, ent);
   };
   if (!flag(a[3])) return call(none);
@@ -461,7 +465,7 @@ PyMethodDef g_methods[] = {
     method<norm_bwd, 11>("norm_bwd"),
     method<quantize_rows, 3>("quantize_rows"),
     method<linear_i8, 6>("linear_i8"),
-    method<logprob_fwd, 6>("logprob_fwd"),
+    method<logprob_fwd, 7>("logprob_fwd"),
     method<logprob_bwd, 8>("logprob_bwd"),
     method<policy_fwd, kPolicyArgs + 3>("policy_fwd"),
     method<policy_bwd, kPolicyArgs + 4>("policy_bwd"),

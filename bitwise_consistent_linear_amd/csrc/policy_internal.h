@@ -54,7 +54,10 @@ struct LogprobArgs {
   float *logp, *lse, *entropy;
   const float *d_logp, *d_entropy;
   void *d_logits;
+  float *parts;   // forward of few long rows: the threads' sums, [rows][groups][3][threads]
+  int64_t groups;  // of a row; set by the launcher
 };
+int64_t logprob_parts_bytes(const LogprobArgs &args);  // 0: a row is one workgroup's
 hipError_t launch_logprob_fwd(const LogprobArgs &args, hipStream_t stream);
 int64_t logprob_bwd_grid(const LogprobArgs &args);
 hipError_t launch_logprob_bwd(const LogprobArgs &args, hipStream_t stream);

@@ -130,19 +130,25 @@ typedef struct gdn_logprob_shape {
   double scale; /* logits are multiplied by it: the inverse of the sampling temperature */
 } gdn_logprob_shape_t;
 
+/* Bytes of device workspace that gdn_token_logprob_fwd needs, into *bytes (host): 0 but for a
+ * few rows of a long vocabulary, which are split over several workgroups. Host only. */
+gdn_status_t gdn_token_logprob_fwd_workspace(const gdn_logprob_shape_t *shape, size_t *bytes);
+
 /* For each row, with z = scale * logits, lse = log(sum(exp(z))), p = exp(z - lse):
  *   logp = z[id] - lse,  entropy = -sum(p * (z - lse)) = lse - sum(p * z)
  * in one pass over the logits (running maximum and sums in binary32).
  *   ids [rows]     : a row whose id is outside [0, vocab) is not scored: its logits are not
  *                    read and its outputs are 0
  *   logp, lse float [rows]; entropy float [rows] or NULL
+ *   workspace      : device, 4-byte aligned, gdn_token_logprob_fwd_workspace() bytes (NULL
+ *                    where that is 0); its contents on entry do not matter
  * A logit of -infinity has p = 0 and adds nothing to the entropy; a scored row of nothing but
  * -infinity has lse and logp -infinity and entropy 0; a row with NaN or +infinity gives NaN.
  * Errors: GDN_E_NULL, GDN_E_SHAPE (sizes, stride, scale, alignment), GDN_E_UNSUPPORTED
  * (dtype, id_bytes), GDN_E_DEVICE. rows == 0 does nothing. */
 gdn_status_t gdn_token_logprob_fwd(const gdn_logprob_shape_t *shape, const void *logits,
                                    const void *ids, float *logp, float *lse, float *entropy,
-                                   void *stream);
+                                   void *workspace, size_t workspace_bytes, void *stream);
 
 /* Gradient of gdn_token_logprob_fwd's outputs with respect to the logits:
  *   d_logits[c] = scale * (d_logp * ([c == id] - p[c])

@@ -374,6 +374,40 @@ def test_logprob_strides_and_rows_alone():
             same_bits(p, q[lo:hi], f"rows {lo}:{hi}")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [98304, 98305, 131072, 196609, 262147])
+def test_logprob_few_long_rows(V, dt):
+    """Few rows of a long vocabulary are split over workgroups: against the 64-bit form, with
+    whole parts masked, and the same bits as in a batch whose rows are not split."""
+    inf = float("inf")
+    z, ids, _, _ = lp_inputs(70, V, DTYPES[dt], V)
+    z[3, :65536] = -inf
+    z[4, 65536:] = -inf
+    z[5, :] = -inf
+    z[6, 1:] = torch.finfo(z.dtype).min
+    z[7, V - 1] = inf
+    z[8, 0] = float("nan")
+    ids[3], ids[4], ids[9] = V - 1, 0, V - 1
+    zd, idd = z.to(DEV), ids.to(DEV)
+    full = api.token_logprob_fwd(zd, idd, scale=0.8, entropy=True)
+    part = api.token_logprob_fwd(zd[:64], idd[:64], scale=0.8, entropy=True)
+    for p, q in zip(part, full):
+        same_bits(p.nan_to_num(7.0), q[:64].nan_to_num(7.0), "64 rows of 70")
+    one = api.token_logprob_fwd(zd[9:10], idd[9:10], scale=0.8)
+    same_bits(one[0], full[0][9:10], "a row alone, without the entropy")
+    own = torch.empty(api.token_logprob_fwd_workspace_bytes(api.GdnLogprobShape(
+        1, V, V, int(dt == "bf16"), 8, 0.8)), dtype=torch.uint8, device=DEV)
+    assert own.numel() == (0 if V == 98304 else 1024 * 6 * (-(-V // 65536)))
+    same_bits(api.token_logprob_fwd(zd[9:10], idd[9:10], scale=0.8, workspace=own)[1], one[1],
+              "the caller's workspace")
+    ok = [0, 1, 2, 3, 4, 5, 9, 63]
+    for got, (want, bound), name in zip(part, R.logprob_bounds(z[ok], ids[ok], 0.8),
+                                        ("logp", "lse", "entropy")):
+        R.check(got[ok], want, bound, name)
+    for v in part[:2]:
+        assert bool(v[7].isnan()) and bool(v[8].isnan())
+
+
 def test_logprob_gradient_against_differences():
     """The kernel's gradient against central differences of the 64-bit log-probability: off by
     the gradient's own bound and by the difference's step (h^2 / 6 times a third derivative of

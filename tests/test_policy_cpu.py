@@ -29,7 +29,7 @@ def L():
 def test_exports_every_declared_function(L):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"\b(gdn_[a-z0-9_]+)\s*\(", text))
-    assert len(names) == 12, names
+    assert len(names) == 13, names
     out = subprocess.run(["nm", "-D", "--defined-only", api.POLICY_LIB_PATH],
                          capture_output=True, text=True, check=True).stdout
     assert set(re.findall(r"\s[TW]\s+(gdn_\w+)$", out, flags=re.M)) == names
@@ -66,9 +66,9 @@ def lp_shape(rows=4, vocab=64, stride=64, dt=F32, idb=8, scale=1.0):
     return ctypes.byref(api.GdnLogprobShape(rows, vocab, stride, dt, idb, scale))
 
 
-def lf(L, sh=None, logits=FAKE, ids=FAKE, logp=FAKE, lse=FAKE, ent=FAKE):
+def lf(L, sh=None, logits=FAKE, ids=FAKE, logp=FAKE, lse=FAKE, ent=FAKE, ws=None, n=0):
     return L.gdn_token_logprob_fwd(lp_shape() if sh is None else sh, logits, ids, logp, lse,
-                                   ent, None)
+                                   ent, ws, n, None)
 
 
 def lb(L, sh=None, logits=FAKE, ids=FAKE, lse=FAKE, dlp=FAKE, ent=FAKE, de=FAKE, out=2 * FAKE):
@@ -99,6 +99,7 @@ NAN, INF = float("nan"), float("inf")
 NO_NORM = ctypes.POINTER(api.GdnNormShape)()
 NO_LP = ctypes.POINTER(api.GdnLogprobShape)()
 NO_PO = ctypes.POINTER(api.GdnPolicyShape)()
+LONG = lp_shape(rows=1, vocab=1 << 20, stride=1 << 20)  # split over workgroups
 REFUSALS = [
     ("norm null shape", lambda L: nf(L, NO_NORM), NULL),
     ("norm negative rows", lambda L: nf(L, norm_shape(rows=-1)), SHAPE),
@@ -164,6 +165,10 @@ REFUSALS = [
     ("logprob null lse", lambda L: lf(L, lse=None), NULL),
     ("logprob misaligned ids", lambda L: lf(L, ids=FAKE + 4), SHAPE),
     ("logprob misaligned logits", lambda L: lf(L, logits=FAKE + 2), SHAPE),
+    ("logprob no workspace", lambda L: lf(L, LONG), NULL),
+    ("logprob short workspace", lambda L: lf(L, LONG, ws=FAKE, n=8), SHAPE),
+    ("logprob misaligned workspace", lambda L: lf(L, LONG, ws=FAKE + 2, n=1 << 30), SHAPE),
+    ("logprob workspace null", lambda L: L.gdn_token_logprob_fwd_workspace(lp_shape(), None), NULL),
     ("logprob bwd entropy alone", lambda L: lb(L, de=None), NULL),
     ("logprob bwd d_entropy alone", lambda L: lb(L, ent=None), NULL),
     ("logprob bwd null d_logits", lambda L: lb(L, out=None), NULL),
@@ -216,6 +221,9 @@ def test_workspaces_grow_with_the_sizes():
     big = api.layer_norm_bwd_workspace_bytes(api.GdnNormShape(4096, 100, 0, F32, F32))
     assert small >= 2 * 100 * 4 and big > small and small % 256 == big % 256 == 0
     a = api.policy_loss_workspace_bytes(api.GdnPolicyShape(100, 3, 0, 0, 0.2, 0.2, 0, 0, 0))
+    c = lambda rows, vocab: api.token_logprob_fwd_workspace_bytes(  # noqa: E731
+        api.GdnLogprobShape(rows, vocab, vocab, F32, 8, 1.0))
+    assert c(1, 1000) == c(100000, 1 << 20) == 0 < c(1, 1 << 20) < c(2, 1 << 20) < c(2, 1 << 21)
     b = api.policy_loss_workspace_bytes(api.GdnPolicyShape(10**6, 300, 0, 0, 0.2, 0.2, 0, 0, 0))
     assert b > a > 0 and a % 256 == b % 256 == 0
 
