@@ -97,6 +97,8 @@ __global__ __launch_bounds__(1024) void quantize_kernel(const QuantizeArgs p) {
     } else {
       load(x, row);
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) settle_row(x[j], 8 * (j * T + t), p.k);
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) top = max(top, abs_top(x[j]));

@@ -66,21 +66,26 @@ __device__ __forceinline__ void merge(Softmax &a, Softmax b, float c) {
   a.t += b.t;
 }
 
-// A thread's 32 logits of a tile: four runs of eight, a tile's runs `threads` apart,
-// -infinity past the row's end.
+// A thread's 32 logits of a tile: four runs of eight, `threads` runs apart, -infinity past the
+// row's end.
 constexpr int kFwdVecs = 4;
 template <bool B16>
 struct Tile {
   Vec8<B16> x[kFwdVecs];
+  __device__ __forceinline__ static int64_t col(int64_t c0, int j) {
+    return c0 + 8 * (int64_t)(j * (int)blockDim.x + (int)threadIdx.x);
+  }
   __device__ __forceinline__ void load(const LogprobArgs &p, int64_t off, int64_t c0) {
 #pragma unroll
-    for (int j = 0; j < kFwdVecs; ++j) {
-      const int64_t col = c0 + 8 * (int64_t)(j * (int)blockDim.x + (int)threadIdx.x);
-      if (col + 8 <= p.vocab)
-        x[j].load(p.logits, off + col);
-      else
-        x[j].load_part(p.logits, off + col, col < p.vocab ? (int)(p.vocab - col) : 0, kNegInf);
-    }
+    for (int j = 0; j < kFwdVecs; ++j) x[j].load(p.logits, off + col(c0, j));
+  }
+  // the row's last tile, not a whole one
+  __device__ __forceinline__ void load_last(const LogprobArgs &p, int64_t off, int64_t c0) {
+#pragma unroll
+    for (int j = 0; j < kFwdVecs; ++j)
+      load_row(x[j], p.logits, off, col(c0, j), p.vocab, kNegInf);
+#pragma unroll
+    for (int j = 0; j < kFwdVecs; ++j) settle_row(x[j], col(c0, j), p.vocab, kNegInf);
   }
   // the thread's logits into a
   template <bool ENT>
@@ -115,17 +120,25 @@ __device__ __forceinline__ Softmax thread_sums(const LogprobArgs &p, int64_t off
   const float c = p.scale_log2e;
   Softmax a{kLowest, 0.0f, 0.0f}, g = a;
   Tile<B16> x, next;
-  x.load(p, off, from);
   int tiles = 0;
-  for (int64_t c0 = from; c0 < end; c0 += tile) {
-    if (c0 + tile < end) next.load(p, off, c0 + tile);
+  auto add = [&]() {
     x.template add_to<ENT>(g, c);
     if (++tiles == kGroupTiles) {
       merge(a, g, c);
       g = Softmax{kLowest, 0.0f, 0.0f};
       tiles = 0;
     }
+  };
+  int64_t c0 = from;
+  if (c0 + tile <= end) x.load(p, off, c0);
+  for (; c0 + tile <= end; c0 += tile) {
+    if (c0 + 2 * tile <= end) next.load(p, off, c0 + tile);
+    add();
     x = next;
+  }
+  if (c0 < end) {
+    x.load_last(p, off, c0);
+    add();
   }
   if (tiles > 0) merge(a, g, c);
   return a;
@@ -213,11 +226,15 @@ __global__ __launch_bounds__(kMostFwdThreads) void logprob_join_kernel(const Log
   finish_row<ENT>(p, row, a, chosen);
 }
 
-// Threads of a row, by the vocabulary alone: one tile of 32 values a thread up to 8192 values
-// and 512 threads from there. 8192 rows of 65536 bf16 values take 179 us at 512 threads (6.0
-// TB/s), 191 at 256 and 221 at 1024; of 2048 values 11.0 us at 64 threads, 44 at 512.
+// Threads of a row, by the vocabulary alone: as many tiles of 32 values a thread as 512 threads
+// would need, spread evenly, and 512 threads beyond a group. 8192 rows of 65536 bf16 values take
+// 169 us at 512 threads (6.0 TB/s), 191 at 256 and 221 at 1024; 4096 rows of 20000 29 us in two
+// tiles of 320 threads, 40 in one of 512 and a rest; of 2048 values 11.0 us at 64, 44 at 512.
 int fwd_threads(int64_t vocab) {
-  return vocab <= 2048 ? 64 : vocab <= 4096 ? 128 : vocab <= 8192 ? 256 : kMostFwdThreads;
+  constexpr int64_t kMost = kMostFwdThreads * 8 * kFwdVecs;
+  if (vocab > kGroupValues) return kMostFwdThreads;
+  const int64_t tiles = (vocab + kMost - 1) / kMost, each = (vocab + tiles - 1) / tiles;
+  return (int)((each + 64 * 8 * kFwdVecs - 1) / (64 * 8 * kFwdVecs)) * 64;
 }
 // Runs of eight values a thread: 32 bytes of either type (4096 x 65536 binary32 takes 344 us
 // with one run and 372 with two, 8192 x 65536 bf16 355 with two and 402 with one).
@@ -250,6 +267,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobA
 #pragma unroll
     for (int e = 0; e < 8; ++e) d[e] = 0.0f;
     if (use) {
+      settle_row(x[j], c, V);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float z = fmaf(x[j].get(e), scale, -lse), q = exp_of(z);

@@ -48,6 +48,11 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(const NormArgs p) {
     else
       b[j].zero();
   }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    settle_row(w[j], 8 * (j * T + t), D);
+    if (p.bias) settle_row(b[j], 8 * (j * T + t), D);
+  }
   // rows past the end repeat the last one, unwritten
   auto load = [&](Vec8<XB> (&x)[NV], int64_t row) {
     if (row >= p.rows) row = p.rows - 1;
@@ -60,6 +65,8 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(const NormArgs p) {
   for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step) {
     const int64_t row = r0 + g;
     if (r0 + step < p.rows) load(next, row + step);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) settle_row(x[j], 8 * (j * T + t), D);
     float mean[1] = {0.0f};
     if (layer) {
 #pragma unroll
@@ -122,6 +129,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) load_row(w[j], p.weight, 0, 8 * (j * T + t), D);
   };
+  auto settle_weight = [&]() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) settle_row(w[j], 8 * (j * T + t), D);
+  };
   if (kAhead) load_weight();
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -145,6 +156,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
   };
   Row cur, next;
   if (kAhead && p.rows > 0) load(cur, (int64_t)blockIdx.x * groups + g);
+  if (kAhead) settle_weight();
   int par = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += step, par ^= 1) {
     const int64_t row = r0 + g;
@@ -153,6 +165,12 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
     } else {
       load(cur, row);
       load_weight();
+      settle_weight();
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      settle_row(cur.x[j], 8 * (j * T + t), D);
+      settle_row(cur.dy[j], 8 * (j * T + t), D);
     }
     float c[2] = {0.0f, 0.0f};  // sums of g xh and of g; dy is 0 past the row's end
     float xh[NV][8], gw[NV][8];

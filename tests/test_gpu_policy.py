@@ -159,6 +159,45 @@ def test_norm_rows_do_not_depend_on_the_batch(M, D):
             same_bits(p, q[lo:hi], f"rows {lo}:{hi}")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 513, 1038, 8195])
+def test_rows_of_every_ending(D, dt):
+    """A row's last values, 1 to 8 of a run of eight, through every kernel that reads rows: next
+    to NaN on both sides, which must stay outside."""
+    dt, M = DTYPES[dt], 5
+    x, w, b, dy = norm_inputs(M, D, dt, dt, 80 + D)
+
+    def guarded(t):
+        wide = torch.full((t.shape[0] * t.shape[1] + 32,), float("nan"), dtype=dt, device=DEV)
+        inner = wide[16:-16].view(t.shape)
+        inner.copy_(t)
+        return inner
+
+    xd, dyd = guarded(x), guarded(dy)
+    y, mean, rstd = api.layer_norm_fwd(xd, guarded(w[None])[0], guarded(b[None])[0])
+    (wy, ey), _, _ = R.norm_fwd_bounds(x, w, b, 1e-5, "layer", dt)
+    R.check(y, wy, ey, "y")
+    dx, dw, db = api.layer_norm_bwd(dyd, xd, w.to(DEV), mean, rstd)
+    (wx, ex), (ww, ew), (wb, eb) = R.norm_bwd_bounds(dy, x, w, mean.cpu(), rstd.cpu(), "layer", dt)
+    R.check(dx, wx, ex, "dx")
+    R.check(dw, ww, ew, "d_weight")
+    R.check(db, wb, eb, "d_bias")
+    q, s = api.quantize_rows(xd)
+    wq, ws = R.quantize(x, -(-D // 128) * 128)
+    assert torch.equal(q.cpu().to(torch.int64), wq)
+    same_bits(s.cpu(), ws, "scale")
+    ids = torch.tensor([0, D - 1, D // 2, -1, D - 1])
+    logp, lse, ent = api.token_logprob_fwd(xd, ids.to(DEV), scale=0.8, entropy=True)
+    for got, (want, bound), name in zip((logp, lse, ent), R.logprob_bounds(x, ids, 0.8),
+                                        ("logp", "lse", "entropy")):
+        R.check(got, want, bound, name)
+    dlp = torch.ones(M)
+    d = api.token_logprob_bwd(xd, ids.to(DEV), lse, dlp.to(DEV), scale=0.8, entropy=ent,
+                              d_entropy=dlp.to(DEV))
+    want, bound = R.logprob_bwd_bounds(x, ids, lse.cpu(), dlp, 0.8, ent.cpu(), dlp, dt)
+    R.check(d, want, bound, "d_logits")
+
+
 # --------------------------------------------------------------------------- 8-bit product
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
