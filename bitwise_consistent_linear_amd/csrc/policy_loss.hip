@@ -131,6 +131,65 @@ struct Starts {
   }
 };
 
+// Which of the sequences whose starts are held (lanes from `from` to `to` of the window) each of
+// a chunk's tokens belongs to, found for all of them at once: every sequence with tokens marks the
+// place of its start, and a token's sequence is the one marked last at or before it. One wave's
+// LDS, no barrier: its accesses to LDS are in order.
+struct Marks {
+  uint8_t at[kChunk];
+};
+__device__ __forceinline__ void lds_in_order() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+// own: this lane's sequence has a start at token c0 + place inside the chunk, and tokens. Gives in
+// seq[j] the lane of the sequence of token c0 + 64 j + lane, -1 for a token before all of them.
+__device__ __forceinline__ void find_sequences(Marks &m, bool own, int place, int (&seq)[kPer]) {
+  const int lane = threadIdx.x % 64;
+  lds_in_order();  // earlier reads are done
+  reinterpret_cast<uint32_t *>(m.at)[lane] = 0;
+  lds_in_order();
+  if (own) m.at[place] = (uint8_t)(lane + 1);
+  lds_in_order();
+  uint8_t mark[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) mark[j] = m.at[64 * j + lane];
+  int before = -1;  // the place marked last in the runs of 64 so far
+  const uint64_t below = (~0ull) >> (63 - lane);
+  int place_of[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint64_t all = __ballot(mark[j] != 0), mine = all & below;
+    place_of[j] = mine ? 64 * j + 63 - __builtin_clzll(mine) : before;
+    if (all) before = 64 * j + 63 - __builtin_clzll(all);
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    seq[j] = place_of[j] < 0 ? -1 : (int)m.at[place_of[j]] - 1;
+}
+
+// The value that lane `from` holds (any lane where from < 0).
+__device__ __forceinline__ double of_lane(double v, int from) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (from & 63), (int)(uint32_t)b);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (from & 63), (int)(uint32_t)(b >> 32));
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ int of_lane(int v, int from) {
+  return __builtin_amdgcn_ds_bpermute(4 * (from & 63), v);
+}
+
+// Bits [a, b) of a chunk's 256 flags set.
+__device__ __forceinline__ int count_bits(const uint64_t (&f)[kPer], int a, int b) {
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int lo = max(a - 64 * j, 0), hi = min(b - 64 * j, 64);
+    if (lo < hi) n += __popcll((f[j] >> lo) << (64 - (hi - lo)));
+  }
+  return n;
+}
+
 // v plus its neighbour's by a DPP move, 0 where there is none.
 template <int Ctrl, int Rows>
 __device__ __forceinline__ double plus_moved(double v) {
@@ -156,6 +215,7 @@ __device__ __forceinline__ double wave_total(double v) {
 }
 
 __global__ __launch_bounds__(256) void policy_tokens_kernel(const PolicyArgs p) {
+  __shared__ __align__(4) Marks marks[4];
   const int64_t block = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lane = threadIdx.x % 64;
   const int64_t t0 = block * p.span;
@@ -186,6 +246,13 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(const PolicyArgs p) 
     }
     cut = count = 0;
   };
+  // Sequences that lie inside a chunk are taken together, each token with its weight but for a
+  // factor of the whole batch: 1, or 1 / (its sequence's scored tokens). Their counts are exact
+  // from the tokens' flags. The sum stands in the slot of the last of them, over that weight.
+  double inner[3] = {0.0, 0.0, 0.0}, last_over = 0.0;
+  int64_t last = -1;
+  int last_lane = 0;
+  Marks &mark = marks[threadIdx.x / 64];
   for (int64_t c0 = t0; c0 < end; c0 += kChunk) {
     const int64_t c1 = c0 + kChunk < end ? c0 + kChunk : end;
     if (c0 > t0) load(c0);
@@ -194,6 +261,53 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(const PolicyArgs p) 
     for (int j = 0; j < kPer; ++j) o[j] = token_terms(p, in[j]);
     // the sequences that meet [c0, c1), those that end in it put down
     while (s < c1) {
+      if (s >= c0 && e <= c1) {
+        const int base = (int)(n - starts.first), from = starts.held - (int)c0;
+        const int to = of_lane(starts.held, lane + 1) - (int)c0, size = (int)(c1 - c0);
+        const bool inside = lane >= base && lane < 63 && starts.first + lane < p.seqs &&
+                            from >= 0 && to <= size;
+        const uint64_t rest = ~__ballot(inside) >> base;  // bit 63 is never inside: not 0
+        const int more = __builtin_ctzll(rest), run = more > 0 ? more : 1;
+        const bool own = inside && lane < base + run && to > from;
+        uint64_t used[kPer], cuts[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          used[j] = __ballot(in[j].use);
+          cuts[j] = __ballot(in[j].use && !o[j].moves);
+        }
+        const int c = own ? count_bits(used, from, to) : 0;
+        const double w = c > 0 ? (p.by_sequence ? 1.0 / (double)c : 1.0) : 0.0;
+        int seq[kPer];
+        find_sequences(mark, own, from, seq);
+        const int run_end = __builtin_amdgcn_readlane(starts.held, base + run) - (int)c0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const double wt = of_lane(w, seq[j]);
+          if (in[j].use && seq[j] >= 0 && 64 * j + lane < run_end) {
+            inner[0] += wt * o[j].pg;
+            inner[1] += wt * o[j].kl;
+            inner[2] += wt * (double)in[j].entropy;
+          }
+        }
+        if (own) {
+          double *out = p.partials + (block + starts.first + lane) * kSums;
+          out[0] = out[1] = out[2] = 0.0;
+          out[3] = (double)count_bits(cuts, from, to);
+          out[4] = (double)c;
+        }
+        if (const uint64_t any = __ballot(c > 0)) {
+          last_lane = 63 - __builtin_clzll(any);
+          last = starts.first + last_lane;
+          last_over = p.by_sequence ? (double)__builtin_amdgcn_readlane(c, last_lane) : 1.0;
+        }
+        n += run;
+        if (n >= p.seqs) {
+          s = e = p.tokens;
+          break;
+        }
+        starts.span(p, n, s, e);
+        continue;
+      }
       if (e > s && e > c0) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -218,6 +332,14 @@ __global__ __launch_bounds__(256) void policy_tokens_kernel(const PolicyArgs p) 
     }
   }
   if (s < end && e > end) flush();
+  if (last >= 0) {
+    double *out = p.partials + (block + last) * kSums;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const double v = of_lane(wave_total(inner[k]), 63) * last_over;
+      if (lane == last_lane) out[k] = v;  // the lane that wrote 0 there
+    }
+  }
 }
 
 // Sums over a workgroup of 1024 threads, in every thread, waves in order.
@@ -332,6 +454,7 @@ __global__ __launch_bounds__(1024) void policy_finish_kernel(const PolicyArgs p)
 }
 
 __global__ __launch_bounds__(256) void policy_grad_kernel(const PolicyArgs p) {
+  __shared__ __align__(4) Marks marks[4];
   const int64_t block = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lane = threadIdx.x % 64;
   const int64_t t0 = block * kChunk;
@@ -341,23 +464,25 @@ __global__ __launch_bounds__(256) void policy_grad_kernel(const PolicyArgs p) {
 #pragma unroll
   for (int j = 0; j < kPer; ++j) in[j] = load_token(p, t0 + 64 * j + lane, end, false);
   Starts starts;
-  int64_t n = starts.seek(p, t0), held = -1;
-  float weight = 0.0f, w[kPer] = {};  // weight: of sequence first + lane
-  for (; n < p.seqs; ++n) {
-    int64_t s, e;
-    starts.span(p, n, s, e);
-    if (s >= end) break;
-    if (starts.first != held) {
-      held = starts.first;
-      weight = held + lane < p.seqs ? p.weight[held + lane] : 0.0f;
-    }
-    const float wn = __int_as_float(__builtin_amdgcn_readlane(
-        __float_as_int(weight), __builtin_amdgcn_readfirstlane((int)(n - starts.first))));
+  int64_t n = starts.seek(p, t0);
+  float w[kPer] = {};
+  const int size = (int)(end - t0);
+  while (n < p.seqs) {  // 63 sequences at a time
+    if (n - starts.first >= 63) starts.load(p, n);
+    const int64_t mine = starts.first + lane;
+    const bool held = lane >= (int)(n - starts.first) && lane < 63 && mine < p.seqs;
+    const float weight = held ? p.weight[mine] : 0.0f;
+    const int from = max(starts.held - (int)t0, 0), to = of_lane(starts.held, lane + 1) - (int)t0;
+    int seq[kPer];
+    find_sequences(marks[threadIdx.x / 64], held && from < size && to > from, from, seq);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int64_t t = t0 + 64 * j + lane;
-      if (t >= s && t < e) w[j] = wn;
+      const int stop = of_lane(to, seq[j]);
+      const float wt = __int_as_float(of_lane(__float_as_int(weight), seq[j]));
+      if (seq[j] >= 0 && 64 * j + lane < stop) w[j] = wt;
     }
+    n = starts.first + 63;
+    if (starts.at(n) >= end) break;
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {

@@ -476,7 +476,13 @@ def cut(lengths):
 POLICY_CASES = [("many", [37] * 513 + [0, 2, 70000] + [5] * 700), ("one", [1]), ("none scored", [5, 3]), ("tiny", [0, 1, 0, 0, 2, 1]),
                 ("block edges", [256, 256, 255, 1, 257, 0, 513]), ("many short", [1] * 700),
                 ("many empty", [0] * 300 + [40] + [0] * 300 + [1, 0]), ("long", [5000, 1, 9000]),
-                ("mixed", [0, 3, 1000, 17, 2, 2, 2, 2500, 0])]
+                ("mixed", [0, 3, 1000, 17, 2, 2, 2, 2500, 0]),
+                # sequences inside 256 tokens, over their borders, and 62 to 65 of them at once
+                ("ragged", [int(v) for v in np.random.default_rng(1).geometric(0.03, 200) - 1]),
+                ("short and long", [int(v) for v in np.random.default_rng(2).choice(
+                    [0, 1, 7, 60, 200, 255, 256, 257, 600], 90)]),
+                ("63 in a chunk", [4] * 62 + [8] + [4] * 63 + [4] * 64 + [1] * 256 + [2] * 65),
+                ("chunk of empty ones", [250] + [0] * 200 + [3] + [0] * 70 + [9])]
 
 
 def policy_inputs(name, lengths, seed):
