@@ -121,7 +121,7 @@ def build_policy_binding(verbose: bool = False) -> str:
 
     import torch
 
-    base = os.path.join(os.path.dirname(torch.__file__))
+    base = os.path.dirname(torch.__file__)
     abi = int(torch.compiled_with_cxx11_abi())
     tmp = POLICY_BINDING + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
@@ -130,7 +130,8 @@ def build_policy_binding(verbose: bool = False) -> str:
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "policy_binding.cpp"), "-o", tmp,
-           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_hip", "-ltorch_cpu",
+           "-ltorch", "-lc10",
            "-L", PKG, "-l:" + os.path.basename(POLICY_LIB), "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -2,7 +2,7 @@
 //
 // The calls take a few microseconds on the GPU, and a training or decode step is a row of them:
 // through ctypes, with every argument checked in Python, the layer norm of 256 rows cost 8.9 us
-// of host time where its kernel runs 4.5 and a launch costs 2.5. Here a call checks its tensors,
+// of host time where its kernel runs 4.5 and a launch costs 2.5; it costs 5.5. A call checks its tensors,
 // allocates what it returns with torch (on the current stream) and enters the C ABI without
 // a Python object in between. A check that fails hands the tensor to the Python function that
 // names what is wrong; nothing has been allocated or launched by then but the outputs before it.
@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 
 #include "gdn_policy.h"
 
@@ -97,6 +98,31 @@ void *take_if(PyObject *o, const char *name, Types types, at::IntArrayRef shape,
   return given(o) ? take(o, name, types, shape, dev) : nullptr;
 }
 
+// The current stream of GPU `dev`, which has to be the current device: the library launches there.
+void *stream_of(int dev) {
+  PyObject *r = PyObject_CallNoArgs(g_device);
+  const long current = r ? PyLong_AsLong(r) : -1;
+  Py_XDECREF(r);
+  if (PyErr_Occurred()) throw Refused{};
+  if (current != dev)
+    value_error("the tensors are on GPU " + std::to_string(dev) + ", the current device is " +
+                std::to_string(current));
+  PyObject *index = PyLong_FromLong(dev);
+  r = index ? PyObject_CallOneArg(g_stream, index) : nullptr;
+  Py_XDECREF(index);
+  void *s = r ? PyLong_AsVoidPtr(r) : nullptr;
+  Py_XDECREF(r);
+  if (PyErr_Occurred()) throw Refused{};
+  return s;
+}
+
+// A new dense tensor on GPU `dev`: at::empty without its way through the dispatcher (three of
+// them and a launch take 5.5 us of host time against 6.1).
+at::Tensor fresh(at::ScalarType type, at::IntArrayRef shape, int dev) {
+  return at::Tensor(at::detail::empty_cuda(
+      shape, type, c10::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
+}
+
 // An output: the caller's, checked, or a new one. Owns a reference until it is handed out.
 class Out {
  public:
@@ -107,8 +133,7 @@ class Out {
       Py_INCREF(o);
       obj_ = o;
     } else {
-      at::Tensor t = at::empty(
-          shape, at::TensorOptions().dtype(type).device(at::kCUDA, (at::DeviceIndex)dev));
+      at::Tensor t = fresh(type, shape, dev);
       ptr_ = t.data_ptr();
       obj_ = THPVariable_Wrap(std::move(t));
       if (!obj_) throw Refused{};
@@ -146,9 +171,6 @@ struct Workspace {
   void *ptr;
   size_t bytes;
 };
-template <class Size>
-Workspace workspace(PyObject *o, int dev, Size size);
-
 void check(gdn_status_t st) {
   if (st == GDN_OK) return;
   PyObject *e = PyObject_CallFunction(g_error, "is", (int)st, gdn_policy_last_error());
@@ -171,28 +193,9 @@ Workspace workspace(PyObject *o, int dev, Size size) {
   size_t bytes = 0;
   check(size(&bytes));
   if (bytes == 0) return {at::Tensor(), nullptr, 0};
-  at::Tensor t = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(
-                                                 at::kCUDA, (at::DeviceIndex)dev));
+  at::Tensor t = fresh(at::kByte, {(int64_t)bytes}, dev);
   void *p = t.data_ptr();
   return {std::move(t), p, bytes};
-}
-
-// The current stream of GPU `dev`, which has to be the current device: the library launches there.
-void *stream_of(int dev) {
-  PyObject *r = PyObject_CallNoArgs(g_device);
-  const long current = r ? PyLong_AsLong(r) : -1;
-  Py_XDECREF(r);
-  if (PyErr_Occurred()) throw Refused{};
-  if (current != dev)
-    value_error("the tensors are on GPU " + std::to_string(dev) + ", the current device is " +
-                std::to_string(current));
-  PyObject *index = PyLong_FromLong(dev);
-  r = index ? PyObject_CallOneArg(g_stream, index) : nullptr;
-  Py_XDECREF(index);
-  void *s = r ? PyLong_AsVoidPtr(r) : nullptr;
-  Py_XDECREF(r);
-  if (PyErr_Occurred()) throw Refused{};
-  return s;
 }
 
 double number(PyObject *o) {
@@ -211,6 +214,7 @@ PyObject *norm_fwd(PyObject *const *a) {
   const Rows x = rows(a[0], "x", kFloat);
   const int64_t M = x.t.size(0), D = x.t.size(1);
   const int dev = x.t.get_device();
+  void *const stream = stream_of(dev);
   const bool layer = flag(a[4]);
   const double eps = number(a[3]);
   void *w = take(a[1], "weight", kFloat, {D}, dev);
@@ -222,7 +226,7 @@ PyObject *norm_fwd(PyObject *const *a) {
                                   layer ? GDN_NORM_LAYER : GDN_NORM_RMS, code(xt), code(wt)};
   auto call = [&](Out &mean) {
     check(gdn_layer_norm_fwd(&shape, x.t.data_ptr(), x.stride, w, b, eps, y.get(),
-                             mean.get<float>(), rstd.get<float>(), stream_of(dev)));
+                             mean.get<float>(), rstd.get<float>(), stream));
     return tuple(y, mean, rstd);
   };
   if (!layer) return call(none);
@@ -239,6 +243,7 @@ PyObject *norm_bwd(PyObject *const *a) {
   const int dev = x.t.get_device();
   if (dy.t.sizes() != x.t.sizes() || dy.t.get_device() != dev)
     value_error("dy and x differ, in shape or GPU");
+  void *const stream = stream_of(dev);
   const bool layer = flag(a[5]), bias = flag(a[6]);
   void *w = take(a[2], "weight", kFloat, {D}, dev);
   const at::ScalarType wt = THPVariable_Unpack(a[2]).scalar_type();
@@ -254,7 +259,7 @@ PyObject *norm_bwd(PyObject *const *a) {
         a[10], dev, [&](size_t *n) { return gdn_layer_norm_bwd_workspace(&shape, n); });
     check(gdn_layer_norm_bwd(&shape, dy.t.data_ptr(), dy.stride, x.t.data_ptr(), x.stride, w,
                              mean, rstd, dx.get(), dw.get<float>(), db.get<float>(), ws.ptr,
-                             ws.bytes, stream_of(dev)));
+                             ws.bytes, stream));
     return tuple(dx, dw, db);
   };
   if (!bias) return call(none);
@@ -267,10 +272,11 @@ PyObject *quantize_rows(PyObject *const *a) {
   const Rows x = rows(a[0], "x", kFloat);
   const int64_t M = x.t.size(0), K = x.t.size(1);
   const int dev = x.t.get_device();
+  void *const stream = stream_of(dev);
   const int64_t padded = (K + GDN_I8_K_ALIGN - 1) / GDN_I8_K_ALIGN * GDN_I8_K_ALIGN;
   Out xq(a[1], "xq", at::kChar, {M, padded}, dev), scale(a[2], "scale", at::kFloat, {M}, dev);
   check(gdn_quantize_rows(x.t.data_ptr(), M, K, x.stride, code(x.t.scalar_type()),
-                          xq.get<int8_t>(), scale.get<float>(), stream_of(dev)));
+                          xq.get<int8_t>(), scale.get<float>(), stream));
   return tuple(xq, scale);
 }
 
@@ -279,6 +285,7 @@ PyObject *linear_i8(PyObject *const *a) {
   const at::Tensor &xq = need(a[0], "xq", kI8, 2), &wq = need(a[2], "wq", kI8, 2);
   const int64_t M = xq.size(0), K = xq.size(1), N = wq.size(0);
   const int dev = xq.get_device();
+  void *const stream = stream_of(dev);
   if (wq.size(1) != K)
     value_error("xq has rows of " + std::to_string(K) + " values but wq is " +
                 std::to_string(N) + " x " + std::to_string(wq.size(1)));
@@ -288,7 +295,7 @@ PyObject *linear_i8(PyObject *const *a) {
   Out y(a[5], "y", yt, {M, N}, dev);
   check(gdn_linear_i8_fwd(M, N, K, static_cast<const int8_t *>(xq.data_ptr()),
                           static_cast<const float *>(xs), static_cast<const int8_t *>(wq.data_ptr()),
-                          static_cast<const float *>(ws), code(yt), y.get(), stream_of(dev)));
+                          static_cast<const float *>(ws), code(yt), y.get(), stream));
   return y.release();
 }
 
@@ -310,6 +317,7 @@ Logits logits_of(PyObject *logits, PyObject *ids, PyObject *scale) {
 // logprob_fwd(logits, ids, scale, entropy, logp, lse, workspace)
 PyObject *logprob_fwd(PyObject *const *a) {
   const Logits g = logits_of(a[0], a[1], a[2]);
+  void *const stream = stream_of(g.dev);
   const int64_t M = g.shape.rows;
   Out none, logp(a[4], "logp", at::kFloat, {M}, g.dev), lse(a[5], "lse", at::kFloat, {M}, g.dev);
   const Workspace ws = workspace(
@@ -317,7 +325,7 @@ PyObject *logprob_fwd(PyObject *const *a) {
   auto call = [&](Out &ent) {
     check(gdn_token_logprob_fwd(&g.shape, g.z.t.data_ptr(), g.ids, logp.get<float>(),
                                 lse.get<float>(), ent.get<float>(), ws.ptr, ws.bytes,
-                                stream_of(g.dev)));
+                                stream));
     return tuple(logp, lse, ent);
   };
   if (!flag(a[3])) return call(none);
@@ -328,6 +336,7 @@ PyObject *logprob_fwd(PyObject *const *a) {
 // logprob_bwd(logits, ids, lse, d_logp, scale, entropy, d_entropy, d_logits)
 PyObject *logprob_bwd(PyObject *const *a) {
   const Logits g = logits_of(a[0], a[1], a[4]);
+  void *const stream = stream_of(g.dev);
   const int64_t M = g.shape.rows;
   auto row = [&](PyObject *o, const char *name) {
     return static_cast<const float *>(take(o, name, kF32, {M}, g.dev));
@@ -341,7 +350,7 @@ PyObject *logprob_bwd(PyObject *const *a) {
   }
   Out d(a[7], "d_logits", g.z.t.scalar_type(), g.z.t.sizes(), g.dev);
   check(gdn_token_logprob_bwd(&g.shape, g.z.t.data_ptr(), g.ids, lse, d_logp, ent, d_ent, d.get(),
-                              stream_of(g.dev)));
+                              stream));
   return d.release();
 }
 
@@ -388,13 +397,14 @@ Policy policy_of(PyObject *const *a) {
 // policy_fwd(..., stats, weight, workspace)
 PyObject *policy_fwd(PyObject *const *a) {
   const Policy p = policy_of(a);
+  void *const stream = stream_of(p.dev);
   a += kPolicyArgs;
   Out stats(a[0], "stats", at::kFloat, {5}, p.dev), weight(a[1], "weight", at::kFloat, {p.N}, p.dev);
   const Workspace ws = workspace(
       a[2], p.dev, [&](size_t *n) { return gdn_policy_loss_workspace(&p.shape, n); });
   check(gdn_policy_loss_fwd(&p.shape, p.logp, p.old, p.adv, p.ref, p.ent, p.mask, p.cu,
                             stats.get<float>(), weight.get<float>(), ws.ptr, ws.bytes,
-                            stream_of(p.dev)));
+                            stream));
   return tuple(stats, weight);
 }
 
@@ -402,6 +412,7 @@ PyObject *policy_fwd(PyObject *const *a) {
 PyObject *policy_bwd(PyObject *const *a) {
   const Policy p = policy_of(a);
   const bool entropy = given(a[4]);
+  void *const stream = stream_of(p.dev);
   a += kPolicyArgs;
   const float *w = static_cast<const float *>(take(a[0], "weight", kF32, {p.N}, p.dev));
   const double d_loss = number(a[1]);
@@ -409,7 +420,7 @@ PyObject *policy_bwd(PyObject *const *a) {
   Out none, dl(a[2], "d_logp", at::kFloat, {p.T}, p.dev);
   auto call = [&](Out &de) {
     check(gdn_policy_loss_bwd(&p.shape, p.logp, p.old, p.adv, p.ref, p.mask, p.cu, w, d_loss,
-                              dl.get<float>(), de.get<float>(), stream_of(p.dev)));
+                              dl.get<float>(), de.get<float>(), stream));
     return tuple(dl, de);
   };
   if (!entropy) return call(none);
