@@ -70,11 +70,13 @@ __device__ __forceinline__ uint32_t max_rotated(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 | N, 0xF, 0xF, true));
 }
 
-constexpr int kQuantizeGrid = 2048;  // workgroups; more rows are walked over
+// Workgroups; more rows are walked over. Rows of more than kLongRow values: 262144 threads in all
+// (2000 x 30000 bf16 34.5 us, with 2048 workgroups 41).
+constexpr int kQuantizeGrid = 2048, kLongRow = 16384, kLongThreads = 262144;
 
 // G lanes share a row: 16, or 64 (then row_threads / 64 waves do). NV runs of eight values a
 // thread. A workgroup walks over rows, the next row's loads in flight under this one. Bound by
-// memory: 16384 x 4096 bf16 41 us (4.9 TB/s, as a copy).
+// memory: 16384 x 4096 bf16 39 us (5.1 TB/s).
 template <bool B16, int G, int NV>
 __global__ __launch_bounds__(1024) void quantize_kernel(const QuantizeArgs p) {
   __shared__ uint32_t slot[2][16];
@@ -86,7 +88,7 @@ __global__ __launch_bounds__(1024) void quantize_kernel(const QuantizeArgs p) {
     for (int j = 0; j < NV; ++j) load_row(x[j], p.x, row * p.x_stride, 8 * (j * T + t), p.k);
   };
   const int64_t step = (int64_t)gridDim.x * groups;
-  constexpr bool kAhead = NV <= 2;
+  constexpr bool kAhead = NV <= 4;
   Vec8<B16> x[NV], next[kAhead ? NV : 1];
   if (kAhead) load(x, (int64_t)blockIdx.x * groups + g);
   int par = 0;
@@ -530,7 +532,9 @@ Launch pick(const LinearI8Args &a) {
 
 hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  const int nv = a.k_pad <= 8192 ? 1 : a.k_pad <= 16384 ? 2 : a.k_pad <= 32768 ? 4 : 8;
+  // fewer threads with more values each: 16384 x 2100 bf16 24 us with two runs a thread and 32
+  // with one, 8192 x 8192 36 with four and 58 with one
+  const int nv = a.k_pad <= 2048 ? 1 : a.k_pad <= 4096 ? 2 : a.k_pad <= kLongRow ? 4 : 8;
   const int vecs = (a.k_pad + 8 * nv - 1) / (8 * nv);
   QuantizeArgs args = a;
   args.row_threads = vecs <= 16 ? 16 : (vecs + 63) / 64 * 64;
@@ -540,10 +544,12 @@ hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t stream) {
                    : nv == 2  ? quantize_fn<64, 2>(a)
                    : nv == 4  ? quantize_fn<64, 4>(a)
                               : quantize_fn<64, 8>(a);
+  const int threads = args.row_threads * groups;
   const int64_t need = (a.rows + groups - 1) / groups;
+  const int64_t most = a.k_pad > kLongRow ? kLongThreads / threads : kQuantizeGrid;
   void *kargs[] = {&args};
-  return hipLaunchKernel(fn, dim3((unsigned)(need < kQuantizeGrid ? need : kQuantizeGrid)),
-                         dim3(args.row_threads * groups), kargs, 0, stream);
+  return hipLaunchKernel(fn, dim3((unsigned)(need < most ? need : most)), dim3(threads), kargs, 0,
+                         stream);
 }
 
 int64_t linear_i8_threads(const LinearI8Args &a) {

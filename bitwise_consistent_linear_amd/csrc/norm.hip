@@ -8,7 +8,7 @@
 // less the squared mean would cancel. A workgroup walks over rows with the weight (and bias)
 // in registers, the next row's loads in flight under the current one.
 //
-// Measured (bf16): forward of 16384 x 4096 50.5 us (5.3 TB/s), backward 78 us with its column
+// Measured (bf16): forward of 16384 x 4096 45 us (6.0 TB/s), backward 78 us with its column
 // sums (5.2 TB/s of the x, dy and dx that it cannot do without; a large copy reaches 4.9).
 // Rows of odd width use the same 16-byte accesses at their element's alignment: backward of
 // 4099 x 2049 binary32 26 us (3.8 TB/s: 257 of a row's 320 threads have values, and 4 us are the
@@ -22,7 +22,10 @@
 namespace gdn {
 namespace {
 
-constexpr int kFwdGrid = 2048;  // workgroups of a forward launch; more rows are walked over
+// Workgroups of a forward launch; more rows are walked over. Of the widest rows a workgroup of
+// 1024 threads for each compute unit: 2000 x 16384 bf16 takes 25 us so and 37 with 2048 of them
+// (16384 x 4096 the other way round, 45 with 2048 and 49 with 512).
+constexpr int kFwdGrid = 2048, kFwdGridWide = 256, kWide = 8192;
 constexpr int kBwdGrid = 256;   // blocks of rows of a backward launch
 
 // How a row is split: threads of one row, rows at a time, threads of a workgroup.
@@ -264,11 +267,14 @@ const void *bwd_fn(const NormArgs &a) {
                               : (const void *)norm_bwd_kernel<false, false, G, NV>);
 }
 
-// Eight values a thread up to 8192, sixteen above; a row of 16 lanes for 128 values and less.
-// `most` threads of a workgroup where a row needs fewer.
-Split split_of(int width, int most) {
+// Eight values a thread up to `single` values of a row, sixteen above; a row of 16 lanes for 128
+// values and less. `most` threads of a workgroup where a row needs fewer. The forward takes two
+// runs of eight from 4096 on: 8192 x 8192 bf16 43 us so, 61 with 1024 threads a row; the backward,
+// which has the columns' sums in registers too, from 8192 on.
+constexpr int kFwdSingle = 4096, kBwdSingle = 8192;
+Split split_of(int width, int most, int single) {
   Split s;
-  s.nv = width <= 8192 ? 1 : 2;
+  s.nv = width <= single ? 1 : 2;
   const int vecs = (width + 8 * s.nv - 1) / (8 * s.nv);
   s.row_threads = vecs <= 16 ? 16 : (vecs + 63) / 64 * 64;
   s.groups = s.row_threads >= most ? 1 : most / s.row_threads;
@@ -287,24 +293,25 @@ hipError_t run(const void *fn, const NormArgs &a, dim3 grid, int threads, hipStr
 // blocks than compute units only add partial sums to write and read: 16384 x 4096 bf16 took
 // 88.6 us with 256 blocks of two rows at a time, 93.0 with 512 and 99.9 with 1024.
 int norm_bwd_blocks(int64_t rows, int32_t width) {
-  const int groups = split_of(width, 1024).groups;
+  const int groups = split_of(width, 1024, kBwdSingle).groups;
   const int64_t need = (rows + groups - 1) / groups;
   return (int)(need < 1 ? 1 : need < kBwdGrid ? need : kBwdGrid);  // no rows: one writes zeros
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  const Split s = split_of(a.width, 256);
+  const Split s = split_of(a.width, 256, kFwdSingle);
   NormArgs args = a;
   args.row_threads = s.row_threads;
   const void *fn = s.row_threads == 16 ? fwd_fn<16, 1>(a) : s.nv == 1 ? fwd_fn<64, 1>(a)
                                                                       : fwd_fn<64, 2>(a);
   const int64_t need = (a.rows + s.groups - 1) / s.groups;
-  return run(fn, args, dim3((unsigned)(need < kFwdGrid ? need : kFwdGrid)), s.threads(), stream);
+  const int64_t most = a.width > kWide ? kFwdGridWide : kFwdGrid;
+  return run(fn, args, dim3((unsigned)(need < most ? need : most)), s.threads(), stream);
 }
 
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream) {
-  const Split s = split_of(a.width, 1024);
+  const Split s = split_of(a.width, 1024, kBwdSingle);
   NormArgs args = a;
   args.row_threads = s.row_threads;
   const void *fn = s.row_threads == 16 ? bwd_fn<16, 1>(a) : s.nv == 1 ? bwd_fn<64, 1>(a)
