@@ -1,5 +1,5 @@
-"""ctypes binding of libgdn_cpr.so (the C ABI declared in include/gdn_cpr.h) and of
-libgdn_policy.so (the policy-head operators, include/gdn_policy.h).
+"""Binding of libgdn_cpr.so (the C ABI declared in include/gdn_cpr.h) by ctypes, and of
+libgdn_policy.so (the policy-head operators, include/gdn_policy.h) by _policy_binding.so.
 
 Argument marshalling only: the functions check torch tensor dtypes, devices and
 contiguity, allocate outputs that the caller did not pass, and call the C entry point of
