@@ -629,7 +629,8 @@ def policy_lib():
             "gdn_layer_norm_bwd_workspace": [NS, SZP],
             "gdn_layer_norm_bwd": [NS, P, I64, P, I64, P, P, P, P, P, P, P, SZ, P],
             "gdn_quantize_rows": [P, I64, I64, I64, I32, P, P, P],
-            "gdn_linear_i8_fwd": [I64, I64, I64, P, P, P, P, I32, P, P],
+            "gdn_linear_i8_fwd_workspace": [I64, I64, I64, SZP],
+            "gdn_linear_i8_fwd": [I64, I64, I64, P, P, P, P, I32, P, P, SZ, P],
             "gdn_token_logprob_fwd_workspace": [LS, SZP],
             "gdn_token_logprob_fwd": [LS, P, P, P, P, P, P, SZ, P],
             "gdn_token_logprob_bwd": [LS, P, P, P, P, P, P, P, P],
@@ -761,19 +762,30 @@ def quantize_rows(x, *, xq=None, scale=None, stream=None):
     return _policy().quantize_rows(x, xq, scale)
 
 
-def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, stream=None):
+def linear_i8_fwd_workspace_bytes(m: int, n: int, k_pad: int) -> int:
+    """gdn_linear_i8_fwd_workspace: device bytes the 8-bit product needs (often 0)."""
+    b = ctypes.c_size_t(0)
+    _policy_check(policy_lib().gdn_linear_i8_fwd_workspace(m, n, k_pad, ctypes.byref(b)))
+    return b.value
+
+
+def linear_i8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, workspace=None,
+                  stream=None):
     """gdn_linear_i8_fwd: Y = (xq wq^T) x_scale w_scale with exact integer sums. xq int8
     [M, Kp], wq int8 [N, Kp] as quantize_rows returns them, x_scale [M], w_scale [N] float32.
-    Returns y [M, N] in out_dtype (float32 by default, or bfloat16)."""
+    ``workspace`` is a uint8 GPU tensor of at least linear_i8_fwd_workspace_bytes() bytes
+    (allocated here when omitted). Returns y [M, N] in out_dtype (float32 by default, or
+    bfloat16)."""
     if stream is not None:
         return _elsewhere(stream, linear_i8_fwd, xq, x_scale, wq, w_scale,
-                          out_dtype=out_dtype, y=y)
+                          out_dtype=out_dtype, y=y, workspace=workspace)
     torch = _torch()
     if out_dtype is None:
         out_dtype = torch.float32 if y is None else y.dtype
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
-    return _policy().linear_i8(xq, x_scale, wq, w_scale, out_dtype is torch.bfloat16, y)
+    return _policy().linear_i8(xq, x_scale, wq, w_scale, out_dtype is torch.bfloat16, y,
+                               workspace)
 
 
 def token_logprob_fwd_workspace_bytes(shape: GdnLogprobShape) -> int:

@@ -174,6 +174,11 @@ __device__ __forceinline__ f32x4 scaled(i32x4 acc, float xs, f32x4 ws) {
   return v;
 }
 
+// Results of a lane as they are stored: sums of a part of K as their bits.
+__device__ __forceinline__ f32x4 results(const LinearI8Args &p, i32x4 acc, float xs, f32x4 ws) {
+  return p.parts ? __builtin_bit_cast(f32x4, acc) : scaled(acc, xs, ws);
+}
+
 __device__ __forceinline__ f32x4 column_scales(const LinearI8Args &p, int64_t n) {
   f32x4 ws;
 #pragma unroll
@@ -192,16 +197,17 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
   const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t tiles_n = (p.n + 16 * NT - 1) / (16 * NT);
   const int64_t n0 = blockIdx.x % tiles_n * (16 * NT), m0 = blockIdx.x / tiles_n * (16 * MT);
+  const int k0 = (int)blockIdx.y * p.k_part, kn = min(p.k_part, p.k - k0);
   const int8_t *w[NT], *x[MT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int64_t row = n0 + 16 * j + l % 16;
-    w[j] = p.wq + (row < p.n ? row : p.n - 1) * p.k + 16 * (l / 16);
+    w[j] = p.wq + (row < p.n ? row : p.n - 1) * p.k + k0 + 16 * (l / 16);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t row = m0 + 16 * i + l % 16;
-    x[i] = p.xq + (row < p.m ? row : p.m - 1) * p.k + 16 * (l / 16);
+    x[i] = p.xq + (row < p.m ? row : p.m - 1) * p.k + k0 + 16 * (l / 16);
   }
   i32x4 acc[NT][MT];
 #pragma unroll
@@ -209,7 +215,7 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
   auto at = [](const int8_t *b, int k) { return *reinterpret_cast<const i32x4 *>(b + k); };
-  const int lines = p.k / 128;
+  const int lines = kn / 128;
   struct Turn {
     i32x4 w[U][2][NT], x[U][2][MT];
   };
@@ -255,14 +261,15 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
     for (int v = 1; v < 8; ++v) sum += part[v][wave][l];
     const int64_t m = m0 + wave % MT * 16 + l % 16, n = n0 + wave / MT * 16 + 4 * (l / 16);
     if (m < p.m) {
-      const f32x4 v = scaled(sum, p.x_scale[m], column_scales(p, n));
+      const f32x4 v = results(p, sum, p.x_scale[m], column_scales(p, n));
+      float *part = p.parts ? p.parts + blockIdx.y * p.m * p.n : static_cast<float *>(p.y);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (n + r < p.n) {
           if (YB)
             static_cast<uint16_t *>(p.y)[m * p.n + n + r] = to_bf16(v[r]);
           else
-            static_cast<float *>(p.y)[m * p.n + n + r] = v[r];
+            part[m * p.n + n + r] = v[r];
         }
     }
   }
@@ -270,11 +277,12 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
 
 // Sixteen bytes of row m of Y from column n on: 4 binary32 or 8 bf16 values.
 template <bool YB, bool Through>
-__device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, int64_t n, i32x4 v) {
+__device__ __forceinline__ void store_chunk(const LinearI8Args &p, void *to, int64_t m, int64_t n,
+                                            i32x4 v) {
   using unaligned = int __attribute__((ext_vector_type(4), aligned(YB ? 2 : 4)));
   constexpr int kChunk = YB ? 8 : 4;
   if (n + kChunk <= p.n) {
-    char *y = static_cast<char *>(p.y) + (m * p.n + n) * (YB ? 2 : 4);
+    char *y = static_cast<char *>(to) + (m * p.n + n) * (YB ? 2 : 4);
     if (Through)
       __builtin_nontemporal_store(v, reinterpret_cast<unaligned *>(y));
     else
@@ -284,10 +292,10 @@ __device__ __forceinline__ void store_chunk(const LinearI8Args &p, int64_t m, in
     for (int e = 0; e < kChunk; ++e)
       if (n + e < p.n) {
         if (YB)
-          static_cast<uint16_t *>(p.y)[m * p.n + n + e] =
+          static_cast<uint16_t *>(to)[m * p.n + n + e] =
               (uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2)));
         else
-          static_cast<int *>(p.y)[m * p.n + n + e] = v[e];
+          static_cast<int *>(to)[m * p.n + n + e] = v[e];
       }
   }
 }
@@ -367,7 +375,8 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
 
   // the wave's loads of a stage: a base in scalar registers and an offset per lane (below
   // 256 rows of 2^16 bytes); rows past the end repeat the last one
-  const int8_t *wbase = p.wq + n0 * p.k, *xbase = p.xq + m0 * p.k;
+  const int k0 = (int)blockIdx.y * p.k_part, kn = min(p.k_part, p.k - k0);
+  const int8_t *wbase = p.wq + n0 * p.k + k0, *xbase = p.xq + m0 * p.k + k0;
   const int last_w = (int)(p.n - n0 < BN ? p.n - n0 : BN) - 1;
   const int last_x = (int)(p.m - m0 < BM ? p.m - m0 : BM) - 1;
   uint32_t off[kLoads];
@@ -383,13 +392,13 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
   // k of rows 2^n bytes apart, they would ask the same few memory channels (16 x 65536 x 4096
   // takes 61 us that way against 51, 256 rows 83 against 75). Those of an XCD keep in step,
   // for the operands they share in its L2. The sums are integers: the order changes nothing.
-  int fk = (int)(blockIdx.x % 8) * (p.k / 64) / 8 * 64;
+  int fk = (int)(blockIdx.x % 8) * (kn / 64) / 8 * 64;
   auto fetch = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       load_to_lds(((wave * kLoads + i) * 16 < BN ? wbase : xbase) + fk, off[i],
                   lds_at + buf * kStage + i * 1024);
-    fk = fk + 64 < p.k ? fk + 64 : 0;
+    fk = fk + 64 < kn ? fk + 64 : 0;
   };
 
   i32x4 acc[NJ][MI], xf[2][MI], wf[2][NJ];
@@ -430,19 +439,20 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
   arrive<3 * kLoads>();
   read(0, 0);
   int k = 0;
-  for (; k + 256 <= p.k; k += 256) {
+  for (; k + 256 <= kn; k += 256) {
     step(0, 0);
     step(1, 1);
     step(2, 0);
     step(3, 1);
   }
-  if (k < p.k) {  // 128 bytes left
+  if (k < kn) {  // 128 bytes left
     step(0, 0);
     step(1, 1);
   }
 
   arrive<0>();  // every load has landed and every operand been read: LDS is free
   int8_t *own = lds + wave * (kStage * 4 / kWaves);
+  void *const to = p.parts ? p.parts + blockIdx.y * p.m * p.n : p.y;
   f32x4 ws[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) ws[j] = column_scales(p, n0 + wn + 16 * j + 4 * (l / 16));
@@ -454,7 +464,7 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
     constexpr int kChunk = YB ? 8 : 4, kChunks = TN / kChunk;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const f32x4 v = scaled(acc[j][i], xs, ws[j]);
+      const f32x4 v = results(p, acc[j][i], xs, ws[j]);
       const int r = l % 16, n = 16 * j + 4 * (l / 16), c = (n / kChunk) ^ (r % kChunks);
       int8_t *at = own + (r * kChunks + c) * 16;
       if (YB)
@@ -470,34 +480,51 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
       const int q = 64 * g + l, r = q / kChunks, c = q % kChunks;
       const i32x4 v = *reinterpret_cast<const i32x4 *>(own + (r * kChunks + (c ^ (r % kChunks))) * 16);
       const int64_t m = mi + r, n = n0 + wn + kChunk * c;
-      if (m < p.m) store_chunk<YB, Through>(p, m, n, v);
+      if (m < p.m) store_chunk<YB, Through>(p, to, m, n, v);
     }
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+// The parts' sums together, scaled: a row of Y a blockIdx.y, a value a thread.
+template <bool YB>
+__global__ __launch_bounds__(256) void linear_i8_join_kernel(const LinearI8Args p) {
+  const int64_t m = blockIdx.y, n = (int64_t)blockIdx.x * 256 + threadIdx.x, each = p.m * p.n;
+  if (n >= p.n) return;
+  const int *part = reinterpret_cast<const int *>(p.parts) + m * p.n + n;
+  int sum = part[0];
+#pragma unroll 4
+  for (int s = 1; s < p.splits; ++s) sum += part[s * each];
+  const float v = (float)sum * p.x_scale[m] * p.w_scale[n];
+  if (YB)
+    static_cast<uint16_t *>(p.y)[m * p.n + n] = to_bf16(v);
+  else
+    static_cast<float *>(p.y)[m * p.n + n] = v;
 }
 
 struct Launch {
   const void *fn;
   int threads;
   int64_t grid;
+  double us;  // of one round over the units, for 1024 k
 };
 
 template <int MT, int NT>
 Launch rows_launch(const LinearI8Args &a) {
   return {a.y_bf16 ? (const void *)linear_i8_rows_kernel<MT, NT, true>
                    : (const void *)linear_i8_rows_kernel<MT, NT, false>,
-          512, (a.m + 16 * MT - 1) / (16 * MT) * ((a.n + 16 * NT - 1) / (16 * NT))};
+          512, (a.m + 16 * MT - 1) / (16 * MT) * ((a.n + 16 * NT - 1) / (16 * NT)), 0.8};
 }
 
 template <int BM, int BN, int TM, int TN>
-Launch tile_launch(const LinearI8Args &a) {
+Launch tile_launch(const LinearI8Args &a, double round) {
   const int64_t total = (a.m + BM - 1) / BM * ((a.n + BN - 1) / BN);
   const bool whole = a.n % (a.y_bf16 ? 8 : 4) == 0;  // rows of Y of whole 16-byte chunks
   return {a.y_bf16 ? (whole ? (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, true, true>
                             : (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, true, false>)
                    : (whole ? (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, false, true>
                             : (const void *)linear_i8_tile_kernel<BM, BN, TM, TN, false, false>),
-          BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
+          BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8, round / 4};
 }
 
 // The kernel of a size. Up to 256 workgroups (one for each compute unit) the rows kernels'
@@ -520,11 +547,11 @@ Launch pick(const LinearI8Args &a) {
   const double t[5] = {time(256, 256, 62.0), time(128, 256, 37.0), time(128, 128, 23.0),
                        time(64, 128, 17.0), time(64, 64, 10.5)};
   switch (std::min_element(t, t + 5) - t) {
-    case 0: return tile_launch<256, 256, 64, 128>(a);
-    case 1: return tile_launch<128, 256, 64, 64>(a);
-    case 2: return tile_launch<128, 128, 64, 64>(a);
-    case 3: return tile_launch<64, 128, 32, 64>(a);
-    default: return tile_launch<64, 64, 32, 32>(a);
+    case 0: return tile_launch<256, 256, 64, 128>(a, 62.0);
+    case 1: return tile_launch<128, 256, 64, 64>(a, 37.0);
+    case 2: return tile_launch<128, 128, 64, 64>(a, 23.0);
+    case 3: return tile_launch<64, 128, 32, 64>(a, 17.0);
+    default: return tile_launch<64, 64, 32, 32>(a, 10.5);
   }
 }
 
@@ -557,12 +584,51 @@ int64_t linear_i8_threads(const LinearI8Args &a) {
   return go.grid * go.threads;
 }
 
+// Parts of K by workgroups of their own, where a launch would leave at least half of the compute
+// units idle for long enough: a unit fetches some 45 bytes/ns whatever its waves (16 x 4096 x
+// 4096 takes the same with 4, 8 or 16 of them), so only other units help. The second kernel with
+// its launch costs about 5.5 us. Whole and split: 85 x 69 x 15744 15.9 and 7.3 us, 21 x 568 x
+// 10752 11.7 and 7.9, 700 x 700 x 9344 24.6 and 19.0, 1 x 64 x 65536 36.4 and 8.7; 512 x 1024 x
+// 4096, which the rule leaves whole, 8.4 and 10.4.
+constexpr double kJoin = 5.5;
+int32_t linear_i8_splits(const LinearI8Args &a) {
+  const Launch go = pick(a);
+  if (go.grid > 128 || a.m > 65535) return 1;
+  const int64_t most = std::min<int64_t>(256 / go.grid, a.k / 1024);
+  const int64_t lines = a.k / 128, part = most > 1 ? (lines + most - 1) / most : lines;
+  const int64_t splits = (lines + part - 1) / part;  // none of them empty
+  const double saved = go.us * a.k / 1024 * (1.0 - 1.0 / (double)splits);
+  return saved > kJoin ? (int32_t)splits : 1;
+}
+
+int64_t linear_i8_parts_bytes(const LinearI8Args &a) {
+  if (a.m == 0 || a.n == 0) return 0;
+  const int64_t splits = linear_i8_splits(a);
+  return splits > 1 ? splits * a.m * a.n * 4 : 0;
+}
+
 hipError_t launch_linear_i8(const LinearI8Args &a, hipStream_t stream) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  const Launch go = pick(a);
   LinearI8Args args = a;
+  args.splits = linear_i8_splits(a);
   void *kargs[] = {&args};
-  return hipLaunchKernel(go.fn, dim3((unsigned)go.grid), dim3(go.threads), kargs, 0, stream);
+  if (args.splits == 1) {
+    const Launch go = pick(a);
+    args.k_part = a.k;
+    args.parts = nullptr;
+    return hipLaunchKernel(go.fn, dim3((unsigned)go.grid), dim3(go.threads), kargs, 0, stream);
+  }
+  args.k_part = (a.k / 128 + args.splits - 1) / args.splits * 128;
+  LinearI8Args sums = a;  // 4 bytes a sum
+  sums.y_bf16 = 0;
+  const Launch go = pick(sums);
+  hipError_t e = hipLaunchKernel(go.fn, dim3((unsigned)go.grid, (unsigned)args.splits),
+                                 dim3(go.threads), kargs, 0, stream);
+  if (e != hipSuccess) return e;
+  return hipLaunchKernel(a.y_bf16 ? (const void *)linear_i8_join_kernel<true>
+                                  : (const void *)linear_i8_join_kernel<false>,
+                         dim3((unsigned)((a.n + 255) / 256), (unsigned)a.m), dim3(256), kargs, 0,
+                         stream);
 }
 
 }  // namespace gdn

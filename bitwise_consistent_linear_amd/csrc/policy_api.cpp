@@ -70,6 +70,19 @@ size_t norm_workspace(const gdn_norm_shape_t *sh) {
   return (need + 255) / 256 * 256;
 }
 
+gdn_status_t linear_i8_shape(const char *fn, int64_t m, int64_t n, int64_t k_pad,
+                             LinearI8Args &a) {
+  if (m < 0 || m > kMaxInt32 || n < 0 || n > kMaxInt32)
+    return no(GDN_E_SHAPE, fn, "m and n must be in [0, 2^31)");
+  if (k_pad < GDN_I8_K_ALIGN || k_pad > 65536 || k_pad % GDN_I8_K_ALIGN != 0)
+    return no(GDN_E_UNSUPPORTED, fn, "k_pad must be a multiple of 128 in [128, 65536]");
+  a = LinearI8Args{};
+  a.m = m;
+  a.n = n;
+  a.k = (int32_t)k_pad;
+  return GDN_OK;
+}
+
 gdn_status_t logprob_shape(const char *fn, const gdn_logprob_shape_t *sh, LogprobArgs &a) {
   if (!sh) return no(GDN_E_NULL, fn, "shape is NULL");
   if (sh->rows < 0 || sh->rows > kMaxInt32) return no(GDN_E_SHAPE, fn, "rows must be in [0, 2^31)");
@@ -272,15 +285,26 @@ GDN_EXPORT gdn_status_t gdn_quantize_rows(const void *x, int64_t rows, int64_t k
   return gdn::launched(fn, gdn::launch_quantize(a, static_cast<hipStream_t>(stream)));
 }
 
+GDN_EXPORT gdn_status_t gdn_linear_i8_fwd_workspace(int64_t m, int64_t n, int64_t k_pad,
+                                                    size_t *bytes) {
+  const char *fn = "gdn_linear_i8_fwd_workspace";
+  if (!bytes) return gdn::no(GDN_E_NULL, fn, "bytes is NULL");
+  gdn::LinearI8Args a;
+  gdn_status_t st = gdn::linear_i8_shape(fn, m, n, k_pad, a);
+  if (st != GDN_OK) return st;
+  *bytes = (size_t)gdn::linear_i8_parts_bytes(a);
+  return gdn::ok();
+}
+
 GDN_EXPORT gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, const int8_t *xq,
                                           const float *x_scale, const int8_t *wq,
                                           const float *w_scale, int32_t y_dtype, void *y,
+                                          void *workspace, size_t workspace_bytes,
                                           void *stream) {
   const char *fn = "gdn_linear_i8_fwd";
-  if (m < 0 || m > gdn::kMaxInt32 || n < 0 || n > gdn::kMaxInt32)
-    return gdn::no(GDN_E_SHAPE, fn, "m and n must be in [0, 2^31)");
-  if (k_pad < GDN_I8_K_ALIGN || k_pad > 65536 || k_pad % GDN_I8_K_ALIGN != 0)
-    return gdn::no(GDN_E_UNSUPPORTED, fn, "k_pad must be a multiple of 128 in [128, 65536]");
+  gdn::LinearI8Args a;
+  gdn_status_t st = gdn::linear_i8_shape(fn, m, n, k_pad, a);
+  if (st != GDN_OK) return st;
   if (!gdn::known_dtype(y_dtype))
     return gdn::no(GDN_E_UNSUPPORTED, fn, "y_dtype must be F32 or BF16");
   if (m == 0 || n == 0) return gdn::ok();
@@ -289,10 +313,13 @@ GDN_EXPORT gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, c
   if (gdn::any_misaligned({xq, wq}, 16) || gdn::any_misaligned({x_scale, w_scale}, 4) ||
       !gdn::aligned(y, gdn::bytes_of(y_dtype)))
     return gdn::no(GDN_E_SHAPE, fn, "xq and wq must be 16-byte aligned, the others element aligned");
-  gdn::LinearI8Args a{};
-  a.m = m;
-  a.n = n;
-  a.k = (int32_t)k_pad;
+  const int64_t need = gdn::linear_i8_parts_bytes(a);
+  if (need > 0 && !workspace) return gdn::no(GDN_E_NULL, fn, "workspace is required");
+  if (need > 0 && !gdn::aligned(workspace, 16))
+    return gdn::no(GDN_E_SHAPE, fn, "workspace must be 16-byte aligned");
+  if (workspace_bytes < (size_t)need)
+    return gdn::no(GDN_E_SHAPE, fn, "workspace smaller than gdn_linear_i8_fwd_workspace reports");
+  a.parts = static_cast<float *>(workspace);
   a.y_bf16 = y_dtype == GDN_DTYPE_BF16;
   a.xq = xq;
   a.wq = wq;

@@ -280,7 +280,7 @@ PyObject *quantize_rows(PyObject *const *a) {
   return tuple(xq, scale);
 }
 
-// linear_i8(xq, x_scale, wq, w_scale, bf16, y)
+// linear_i8(xq, x_scale, wq, w_scale, bf16, y, workspace)
 PyObject *linear_i8(PyObject *const *a) {
   const at::Tensor &xq = need(a[0], "xq", kI8, 2), &wq = need(a[2], "wq", kI8, 2);
   const int64_t M = xq.size(0), K = xq.size(1), N = wq.size(0);
@@ -293,9 +293,12 @@ PyObject *linear_i8(PyObject *const *a) {
   const void *xs = take(a[1], "x_scale", kF32, {M}, dev), *ws = take(a[3], "w_scale", kF32, {N}, dev);
   const at::ScalarType yt = flag(a[4]) ? at::kBFloat16 : at::kFloat;
   Out y(a[5], "y", yt, {M, N}, dev);
+  const Workspace room = workspace(
+      a[6], dev, [&](size_t *bytes) { return gdn_linear_i8_fwd_workspace(M, N, K, bytes); });
   check(gdn_linear_i8_fwd(M, N, K, static_cast<const int8_t *>(xq.data_ptr()),
                           static_cast<const float *>(xs), static_cast<const int8_t *>(wq.data_ptr()),
-                          static_cast<const float *>(ws), code(yt), y.get(), stream));
+                          static_cast<const float *>(ws), code(yt), y.get(), room.ptr, room.bytes,
+                          stream));
   return y.release();
 }
 
@@ -475,7 +478,7 @@ PyMethodDef g_methods[] = {
     method<norm_fwd, 8>("norm_fwd"),
     method<norm_bwd, 11>("norm_bwd"),
     method<quantize_rows, 3>("quantize_rows"),
-    method<linear_i8, 6>("linear_i8"),
+    method<linear_i8, 7>("linear_i8"),
     method<logprob_fwd, 7>("logprob_fwd"),
     method<logprob_bwd, 8>("logprob_bwd"),
     method<policy_fwd, kPolicyArgs + 3>("policy_fwd"),

@@ -41,7 +41,10 @@ struct LinearI8Args {
   const int8_t *xq, *wq;
   const float *x_scale, *w_scale;
   void *y;
+  float *parts;  // sums of parts of K, [splits][m][n] as bits; NULL: a workgroup takes all of K
+  int32_t splits, k_part;  // set by the launcher; k_part a multiple of 128
 };
+int64_t linear_i8_parts_bytes(const LinearI8Args &args);  // 0: no parts
 int64_t linear_i8_threads(const LinearI8Args &args);  // of the launch; at most 2^32 - 1 fit one
 hipError_t launch_linear_i8(const LinearI8Args &args, hipStream_t stream);
 

@@ -106,18 +106,25 @@ gdn_status_t gdn_layer_norm_bwd(const gdn_norm_shape_t *shape, const void *dy,
 gdn_status_t gdn_quantize_rows(const void *x, int64_t rows, int64_t k, int64_t x_stride,
                                int32_t x_dtype, int8_t *q, float *scale, void *stream);
 
+/* Bytes of device workspace that gdn_linear_i8_fwd needs, into *bytes (host): 0 but for few
+ * tiles of Y and a long k_pad, which is then split over several workgroups. Host only. */
+gdn_status_t gdn_linear_i8_fwd_workspace(int64_t m, int64_t n, int64_t k_pad, size_t *bytes);
+
 /* Y [m, n] = (xq wq^T) * x_scale[m] * w_scale[n]: the products of 8-bit integers are summed
  * exactly in 32-bit integers, converted to binary32, multiplied by x_scale, then by w_scale,
  * and rounded to y_dtype.
  *   xq int8 [m, k_pad], wq int8 [n, k_pad], 16-byte aligned, as gdn_quantize_rows writes them
  *   x_scale float [m], w_scale float [n]
  *   y [m, n]  : F32 or BF16
+ *   workspace : device, 16-byte aligned, gdn_linear_i8_fwd_workspace() bytes (NULL where that
+ *               is 0); its contents on entry do not matter
  * Admitted: 0 <= m, n < 2^31; k_pad a multiple of GDN_I8_K_ALIGN in [128, 65536] (the sum of
  * 65536 products of 8 bits fits 32 bits). m == 0 or n == 0 does nothing. GDN_E_SHAPE also where
  * the tiles are too many for one launch (not under 2^30 rows or columns). */
 gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, const int8_t *xq,
                                const float *x_scale, const int8_t *wq, const float *w_scale,
-                               int32_t y_dtype, void *y, void *stream);
+                               int32_t y_dtype, void *y, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 /* Host struct of the token log-probability calls. Admitted: 0 <= rows < 2^31;
  * 1 <= vocab < 2^31; logits_dtype F32 or BF16; id_bytes 4 or 8 (int32 or int64 ids);

@@ -196,6 +196,15 @@ def test_rows_of_every_ending(D, dt):
                               d_entropy=dlp.to(DEV))
     want, bound = R.logprob_bwd_bounds(x, ids, lse.cpu(), dlp, 0.8, ent.cpu(), dlp, dt)
     R.check(d, want, bound, "d_logits")
+    # in place
+    api.layer_norm_bwd(dyd, xd, w.to(DEV), mean, rstd, dx=dyd)
+    same_bits(dyd, dx, "dx in dy's place")
+    z = xd.clone()
+    api.token_logprob_bwd(z, ids.to(DEV), lse, dlp.to(DEV), scale=0.8, entropy=ent,
+                          d_entropy=dlp.to(DEV), d_logits=z)
+    same_bits(z, d, "d_logits in the logits' place")
+    api.layer_norm_fwd(xd, w.to(DEV), b.to(DEV), y=xd)
+    same_bits(xd, y, "y in x's place")
 
 
 # --------------------------------------------------------------------------- 8-bit product
@@ -256,7 +265,10 @@ I8_SIZES = [(1, 1, 128), (1, 300, 256), (3, 17, 128), (16, 64, 4096), (17, 130, 
             # an even and an odd number of 128-byte lines, one line among them
             (300, 4000, 128), (320, 4032, 512), (600, 4100, 384), (1024, 2048, 256),
             (1100, 4100, 384), (2048, 2048, 128), (3500, 3700, 384), (3841, 3585, 128),
-            (200, 65537, 256)]
+            (200, 65537, 256),
+            # K split over workgroups: few rows, tiles, parts of unequal length, odd columns
+            (85, 69, 15744), (21, 568, 10752), (208, 2162, 13696), (400, 511, 16512),
+            (130, 1001, 65536), (1, 1, 65536), (700, 700, 9344)]
 
 
 @pytest.mark.parametrize("M,N,K", I8_SIZES)
@@ -270,6 +282,21 @@ def test_linear_i8(M, N, K):
     for dt in (F32, BF16):
         y = api.linear_i8_fwd(xq.to(DEV), xs.to(DEV), wq.to(DEV), ws.to(DEV), out_dtype=dt)
         same_bits(y.cpu(), R.linear_i8(xq, xs, wq, ws, dt), f"y {dt}")
+
+
+def test_linear_i8_workspace():
+    g = gen(23)
+    xq = torch.randint(-128, 128, (20, 20480), generator=g, dtype=torch.int8).to(DEV)
+    wq = torch.randint(-128, 128, (33, 20480), generator=g, dtype=torch.int8).to(DEV)
+    s = torch.rand(33, generator=g).to(DEV)
+    need = api.linear_i8_fwd_workspace_bytes(20, 33, 20480)
+    assert need > 0
+    room = torch.full((need + 64,), 85, dtype=torch.uint8, device=DEV)
+    y = api.linear_i8_fwd(xq, s[:20], wq, s, workspace=room[:need])
+    same_bits(y.cpu(), R.linear_i8(xq.cpu(), s[:20].cpu(), wq.cpu(), s.cpu(), F32), "y")
+    assert bool((room[need:] == 85).all())
+    with pytest.raises(api.GdnError, match="workspace"):
+        api.linear_i8_fwd(xq, s[:20], wq, s, workspace=room[:need - 16])
 
 
 def test_linear_i8_largest_sums():

@@ -29,7 +29,7 @@ def L():
 def test_exports_every_declared_function(L):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"\b(gdn_[a-z0-9_]+)\s*\(", text))
-    assert len(names) == 13, names
+    assert len(names) == 14, names
     out = subprocess.run(["nm", "-D", "--defined-only", api.POLICY_LIB_PATH],
                          capture_output=True, text=True, check=True).stdout
     assert set(re.findall(r"\s[TW]\s+(gdn_\w+)$", out, flags=re.M)) == names
@@ -58,8 +58,8 @@ def qr(L, x=FAKE, rows=4, k=64, stride=64, dt=F32, q=FAKE, scale=FAKE):
     return L.gdn_quantize_rows(x, rows, k, stride, dt, q, scale, None)
 
 
-def li(L, m=4, n=4, k=128, xq=FAKE, xs=FAKE, wq=FAKE, ws=FAKE, dt=F32, y=FAKE):
-    return L.gdn_linear_i8_fwd(m, n, k, xq, xs, wq, ws, dt, y, None)
+def li(L, m=4, n=4, k=128, xq=FAKE, xs=FAKE, wq=FAKE, ws=FAKE, dt=F32, y=FAKE, room=None, b=0):
+    return L.gdn_linear_i8_fwd(m, n, k, xq, xs, wq, ws, dt, y, room, b, None)
 
 
 def lp_shape(rows=4, vocab=64, stride=64, dt=F32, idb=8, scale=1.0):
@@ -152,6 +152,12 @@ REFUSALS = [
     ("linear too many tiles", lambda L: li(L, m=2**31 - 1, n=2**31 - 1), SHAPE),
     ("linear rows past one launch", lambda L: li(L, m=2**30, n=1), SHAPE),
     ("linear columns past one launch", lambda L: li(L, m=1, n=2**31 - 1), SHAPE),
+    ("linear no workspace", lambda L: li(L, k=65536), NULL),
+    ("linear short workspace", lambda L: li(L, k=65536, room=FAKE, b=16), SHAPE),
+    ("linear misaligned workspace", lambda L: li(L, k=65536, room=FAKE + 4, b=1 << 30), SHAPE),
+    ("linear workspace null", lambda L: L.gdn_linear_i8_fwd_workspace(4, 4, 128, None), NULL),
+    ("linear workspace k", lambda L: L.gdn_linear_i8_fwd_workspace(
+        4, 4, 130, ctypes.byref(ctypes.c_size_t(0))), UNSUP),
     ("logprob null shape", lambda L: lf(L, NO_LP), NULL),
     ("logprob vocab 0", lambda L: lf(L, lp_shape(vocab=0)), SHAPE),
     ("logprob rows", lambda L: lf(L, lp_shape(rows=-1)), SHAPE),
@@ -221,6 +227,9 @@ def test_workspaces_grow_with_the_sizes():
     big = api.layer_norm_bwd_workspace_bytes(api.GdnNormShape(4096, 100, 0, F32, F32))
     assert small >= 2 * 100 * 4 and big > small and small % 256 == big % 256 == 0
     a = api.policy_loss_workspace_bytes(api.GdnPolicyShape(100, 3, 0, 0, 0.2, 0.2, 0, 0, 0))
+    d = api.linear_i8_fwd_workspace_bytes
+    assert d(16, 4096, 4096) == d(16384, 4096, 65536) == d(0, 4, 65536) == d(4, 4, 128) == 0
+    assert d(85, 69, 15744) % (85 * 69 * 4) == 0 < d(85, 69, 15744)
     c = lambda rows, vocab: api.token_logprob_fwd_workspace_bytes(  # noqa: E731
         api.GdnLogprobShape(rows, vocab, vocab, F32, 8, 1.0))
     assert c(1, 1000) == c(100000, 1 << 20) == 0 < c(1, 1 << 20) < c(2, 1 << 20) < c(2, 1 << 21)
