@@ -813,8 +813,9 @@ def token_logprob_fwd(logits, ids, *, scale=1.0, entropy=False, logp=None, lse=N
 def token_logprob_bwd(logits, ids, lse, d_logp, *, scale=1.0, entropy=None, d_entropy=None,
                       d_logits=None, stream=None):
     """gdn_token_logprob_bwd: the gradient of token_logprob_fwd's logp, and of its entropy
-    where entropy and d_entropy [M] are given, with respect to the logits. Returns d_logits
-    [M, V] in the logits' dtype; d_logits=logits overwrites them."""
+    where entropy and d_entropy [M] are given, with respect to the logits; lse and entropy as
+    token_logprob_fwd returned them. Returns d_logits [M, V] in the logits' dtype;
+    d_logits=logits overwrites them."""
     if stream is not None:
         return _elsewhere(stream, token_logprob_bwd, logits, ids, lse, d_logp, scale=scale,
                           entropy=entropy, d_entropy=d_entropy, d_logits=d_logits)

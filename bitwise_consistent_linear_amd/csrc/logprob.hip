@@ -66,6 +66,25 @@ __device__ __forceinline__ void merge(Softmax &a, Softmax b, float c) {
   a.t += b.t;
 }
 
+// Runs of eight logits into a.
+template <bool ENT, bool B16, int N>
+__device__ __forceinline__ void add_values(Softmax &a, const Vec8<B16> (&x)[N], float c) {
+  float top = a.m;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, x[j].get(e));
+  rebase(a, top, c);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = x[j].get(e) - top, k = __builtin_amdgcn_exp2f(d * c);
+      a.s += k;
+      if (ENT) a.t = fmaf(k, fmaxf(d, kFar), a.t);
+    }
+}
+
 // A thread's 32 logits of a tile: four runs of eight, `threads` runs apart, -infinity past the
 // row's end.
 constexpr int kFwdVecs = 4;
@@ -87,24 +106,6 @@ struct Tile {
 #pragma unroll
     for (int j = 0; j < kFwdVecs; ++j) settle_row(x[j], col(c0, j), p.vocab, kNegInf);
   }
-  // the thread's logits into a
-  template <bool ENT>
-  __device__ __forceinline__ void add_to(Softmax &a, float c) const {
-    float top = a.m;
-#pragma unroll
-    for (int j = 0; j < kFwdVecs; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[j].get(e));
-    rebase(a, top, c);
-#pragma unroll
-    for (int j = 0; j < kFwdVecs; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = x[j].get(e) - top, k = __builtin_amdgcn_exp2f(d * c);
-        a.s += k;
-        if (ENT) a.t = fmaf(k, fmaxf(d, kFar), a.t);
-      }
-  }
 };
 
 // Tiles that a thread adds up from nothing before it merges the sum into its row's: 65536
@@ -122,7 +123,7 @@ __device__ __forceinline__ Softmax thread_sums(const LogprobArgs &p, int64_t off
   Tile<B16> x, next;
   int tiles = 0;
   auto add = [&]() {
-    x.template add_to<ENT>(g, c);
+    add_values<ENT>(g, x.x, c);
     if (++tiles == kGroupTiles) {
       merge(a, g, c);
       g = Softmax{kLowest, 0.0f, 0.0f};
@@ -242,14 +243,44 @@ constexpr int kBwdThreads = 256;
 constexpr int bwd_vecs(bool bf16) { return bf16 ? 2 : 1; }
 constexpr int bwd_span(bool bf16) { return kBwdThreads * 8 * bwd_vecs(bf16); }
 
+// Rows whose |lse| is below this take log p = scale x - lse with the lse of the forward, whose
+// rounding (half a step, at most 2^-19) is then no more than the exponential's own of a distance
+// of 32. In an lse far from zero the logarithm of the sum is lost, or it is past binary32's range,
+// so such a row's maximum and sum are formed again and log p = scale (x - max) - log(sum).
+constexpr float kNearLse = 64.0f;
+
+// Maximum and sum of the exponentials of a row by a workgroup, in every thread.
+template <bool B16>
+__device__ __forceinline__ Softmax row_again(const LogprobArgs &p, int64_t off) {
+  constexpr int J = bwd_vecs(B16), kWaves = kBwdThreads / 64;
+  __shared__ Softmax part[kWaves];
+  const float c = p.scale_log2e;
+  Softmax a{kLowest, 0.0f, 0.0f};
+  for (int64_t c0 = 0; c0 < p.vocab; c0 += bwd_span(B16)) {
+    Vec8<B16> x[J];
+    auto col = [&](int j) { return c0 + 8 * (j * kBwdThreads + (int)threadIdx.x); };
+#pragma unroll
+    for (int j = 0; j < J; ++j) load_row(x[j], p.logits, off, col(j), p.vocab, kNegInf);
+#pragma unroll
+    for (int j = 0; j < J; ++j) settle_row(x[j], col(j), p.vocab, kNegInf);
+    add_values<false>(a, x, c);
+  }
+  a = over_lanes(a, c);
+  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = a;
+  __syncthreads();
+  a = part[0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) merge(a, part[i], c);
+  return a;
+}
+
+// The gradient of the span of a row that begins at c0, with log p = scale (x - m) - ls; zeros
+// where the row is not used.
 template <bool B16, bool ENT>
-__global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobArgs p) {
-  constexpr int J = bwd_vecs(B16), kSpan = bwd_span(B16);
-  const int64_t V = p.vocab, spans = (V + kSpan - 1) / kSpan;
-  const int64_t row = blockIdx.x / spans, c0 = (blockIdx.x % spans) * kSpan;
-  const int64_t id = id_of(p, row);
-  const float lse = p.lse[row];
-  const bool use = id >= 0 && id < V && lse != kNegInf;
+__device__ __forceinline__ void put_gradient(const LogprobArgs &p, int64_t row, int64_t id,
+                                             bool use, float m, float ls, int64_t c0) {
+  constexpr int J = bwd_vecs(B16);
+  const int64_t V = p.vocab;
   const float scale = p.scale;
   const float g = use ? p.d_logp[row] * scale : 0.0f;
   const float h = ENT && use ? p.d_entropy[row] * scale : 0.0f;
@@ -268,17 +299,45 @@ __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobA
     for (int e = 0; e < 8; ++e) d[e] = 0.0f;
     if (use) {
       settle_row(x[j], c, V);
+      const int at = id >= c && id < c + 8 ? (int)(id - c) : -1;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float z = fmaf(x[j].get(e), scale, -lse), q = exp_of(z);
+        const float z = fmaf(x[j].get(e) - m, scale, -ls), q = exp_of(z);
         float k = g;
         if (ENT) k = fmaf(h, z + H, g);
         d[e] = q == 0.0f ? 0.0f : -q * k;
-        if (c + e == id) d[e] += g;
+        if (e == at) d[e] += g;
       }
     }
     store_row<B16>(p.d_logits, row * V, c, V, d);
   }
+}
+
+// A workgroup takes a span of a row. All of a row far from zero is one workgroup's, and the row's
+// others have nothing to do; which one it is changes with the row so that they spread over the
+// XCDs, which take workgroups in turn (8192 x 65536 bf16 720 us where near rows take 343, and
+// 4600 with the first workgroup of every row; 8 x 131072 binary32 60 and 3). The registers of
+// the far rows' loops are the near ones' too: with 64 of them 64 x 131072 bf16 near zero took
+// 8.2 us, with 36 7.4.
+template <bool B16, bool ENT>
+__global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobArgs p) {
+  constexpr int kSpan = bwd_span(B16);
+  const int64_t spans = (p.vocab + kSpan - 1) / kSpan;
+  const int64_t row = blockIdx.x / spans, span = blockIdx.x % spans;
+  const int64_t id = id_of(p, row);
+  const float lse = p.lse[row];
+  const bool use = scored(p, id);
+  if (__builtin_expect(!use || fabsf(lse) < kNearLse, 1)) {
+    put_gradient<B16, ENT>(p, row, id, use, 0.0f, lse, span * kSpan);
+    return;
+  }
+  const int64_t low = spans % 8 == 0 ? 8 : spans & -spans;  // row * spans mod 8: 8 / low places
+  if (span != row * low / 8 % spans) return;
+  const Softmax a = row_again<B16>(p, row * p.stride);
+  const bool any = a.s != 0.0f;  // else every logit is -infinity; a NaN stays
+  const float ls = logf(a.s);
+  for (int64_t c0 = 0; c0 < p.vocab; c0 += kSpan)
+    put_gradient<B16, ENT>(p, row, id, any, a.m, ls, c0);
 }
 
 // A launch holds at most 2^32 - 1 threads, so more rows go in several: `fn` over runs of rows

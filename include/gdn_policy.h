@@ -150,7 +150,8 @@ gdn_status_t gdn_token_logprob_fwd_workspace(const gdn_logprob_shape_t *shape, s
  *   workspace      : device, 4-byte aligned, gdn_token_logprob_fwd_workspace() bytes (NULL
  *                    where that is 0); its contents on entry do not matter
  * A logit of -infinity has p = 0 and adds nothing to the entropy; a scored row of nothing but
- * -infinity has lse and logp -infinity and entropy 0; a row with NaN or +infinity gives NaN.
+ * -infinity has lse and logp -infinity and entropy 0; a row with NaN or +infinity gives NaN. An
+ * lse past binary32's range is an infinity; logp and entropy come from differences and are not.
  * Errors: GDN_E_NULL, GDN_E_SHAPE (sizes, stride, scale, alignment), GDN_E_UNSUPPORTED
  * (dtype, id_bytes), GDN_E_DEVICE. rows == 0 does nothing. */
 gdn_status_t gdn_token_logprob_fwd(const gdn_logprob_shape_t *shape, const void *logits,
@@ -161,8 +162,11 @@ gdn_status_t gdn_token_logprob_fwd(const gdn_logprob_shape_t *shape, const void 
  *   d_logits[c] = scale * (d_logp * ([c == id] - p[c])
  *                          - d_entropy * p[c] * (log p[c] + entropy))
  * with log p = z - lse. Rows that are not scored get 0. Where p[c] is 0 the entropy's term
- * is 0; a row whose lse is -infinity gets 0.
- *   lse, d_logp float [rows]; entropy, d_entropy float [rows]: both or neither (NULL)
+ * is 0; a row of nothing but -infinity gets 0.
+ *   lse, d_logp float [rows]; entropy, d_entropy float [rows]: both or neither (NULL). lse and
+ *                    entropy as the forward wrote them. From |lse| = 64 on, where its rounding
+ *                    would be seen in p (and where it overflows), a row's log-sum-exp is formed
+ *                    again from its logits, at the price of a second reading of them.
  *   d_logits [rows, vocab]: the logits' dtype; may be the logits themselves when their
  *                    stride is vocab. */
 gdn_status_t gdn_token_logprob_bwd(const gdn_logprob_shape_t *shape, const void *logits,
