@@ -172,10 +172,17 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(const NormArgs p) {
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      settle_row(cur.x[j], 8 * (j * T + t), D);
+      settle_row(cur.x[j], 8 * (j * T + t), D, cur.mean);
+      if constexpr (G == 16)
+        if (D < 8) cur.x[j].fill_from(D - 8 * t, cur.mean);
       settle_row(cur.dy[j], 8 * (j * T + t), D);
     }
-    float c[2] = {0.0f, 0.0f};  // sums of g xh and of g; dy is 0 past the row's end
+    // Sums of g xh and of g. Past the row's end dy is 0 and x the mean: with x 0 there, xh would be
+    // -mean rstd, an infinity in a row of equal large values, and 0 times it would reach the sums.
+    // A bf16 x is the mean cut to its upper half: where mean rstd passes the range the row's values
+    // are equal, so the mean is one of them and the cut takes nothing. (A choice of xh = 0 for every
+    // value took 87.9 us for 16384 x 4095 bf16, this 84.6.)
+    float c[2] = {0.0f, 0.0f};
     float xh[NV][8], gw[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j)

@@ -44,7 +44,16 @@ struct Vec8<true> {
     for (int e = 0; e < 8; ++e) w[e / 2] |= (e < n ? (uint32_t)b[e] : f) << (16 * (e % 2));
     r = u32x4_a2{w[0], w[1], w[2], w[3]};
   }
-  // the last 8 - s values first, `fill` after them; s in 0 .. 8
+  // the values from the n-th on are `fill` (its upper half; n may be below 0)
+  __device__ __forceinline__ void fill_from(int n, float fill) {
+    const uint32_t h = __float_as_uint(fill);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (2 * i >= n) r[i] = (r[i] & 0xFFFF0000u) | h >> 16;
+      if (2 * i + 1 >= n) r[i] = (r[i] & 0xFFFFu) | (h & 0xFFFF0000u);
+    }
+  }
+  // the last 8 - s values first, `fill` (its upper half) after them; s in 0 .. 8
   __device__ __forceinline__ void drop(int s, float fill) {
     const uint32_t h = __float_as_uint(fill), f = (h & 0xFFFF0000u) | h >> 16;
     if (s & 12) r = u32x4_a2{r[2], r[3], f, f};
@@ -86,6 +95,11 @@ struct Vec8<false> {
     const float *b = static_cast<const float *>(base) + idx;
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e / 4][e % 4] = e < n ? b[e] : fill;
+  }
+  __device__ __forceinline__ void fill_from(int n, float fill) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e >= n) r[e / 4][e % 4] = fill;
   }
   __device__ __forceinline__ void drop(int s, float fill) {
     const f32x4_a4 f = {fill, fill, fill, fill};
