@@ -327,7 +327,7 @@ GDN_EXPORT gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, c
   a.w_scale = w_scale;
   a.y = y;
   if (gdn::linear_i8_threads(a) > int64_t(0xFFFFFFFF))
-    return gdn::no(GDN_E_SHAPE, fn, "m * n is too large for one launch");
+    return gdn::no(GDN_E_SHAPE, fn, "the tiles of m * n values are too many for one launch");
   return gdn::launched(fn, gdn::launch_linear_i8(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -399,7 +399,7 @@ GDN_EXPORT gdn_status_t gdn_token_logprob_bwd(const gdn_logprob_shape_t *shape, 
   a.d_entropy = d_entropy;
   a.d_logits = d_logits;
   if (gdn::logprob_bwd_grid(a) > gdn::kMaxInt32)
-    return gdn::no(GDN_E_SHAPE, fn, "rows * vocab is too large for one launch");
+    return gdn::no(GDN_E_SHAPE, fn, "rows * ceil(vocab / 2048, BF16 4096) must be under 2^31");
   return gdn::launched(fn, gdn::launch_logprob_bwd(a, static_cast<hipStream_t>(stream)));
 }
 

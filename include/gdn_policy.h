@@ -23,7 +23,7 @@
  * the text of the calling thread's last error. All functions are thread-safe.
  *
  * Row strides are in elements; rows are contiguous inside. An input's stride may be any
- * value >= 0 (0 repeats one row); outputs are dense.
+ * value in [0, 2^31] (0 repeats one row); outputs are dense.
  */
 #ifndef GDN_POLICY_H
 #define GDN_POLICY_H
@@ -120,7 +120,8 @@ gdn_status_t gdn_linear_i8_fwd_workspace(int64_t m, int64_t n, int64_t k_pad, si
  *               is 0); its contents on entry do not matter
  * Admitted: 0 <= m, n < 2^31; k_pad a multiple of GDN_I8_K_ALIGN in [128, 65536] (the sum of
  * 65536 products of 8 bits fits 32 bits). m == 0 or n == 0 does nothing. GDN_E_SHAPE also where
- * the tiles are too many for one launch (not under 2^30 rows or columns). */
+ * the tiles of Y take more threads than one launch holds (2^32 - 1), which they never do for m * n
+ * under 2^35, m and n rounded up to multiples of 64. */
 gdn_status_t gdn_linear_i8_fwd(int64_t m, int64_t n, int64_t k_pad, const int8_t *xq,
                                const float *x_scale, const int8_t *wq, const float *w_scale,
                                int32_t y_dtype, void *y, void *workspace,
@@ -168,7 +169,9 @@ gdn_status_t gdn_token_logprob_fwd(const gdn_logprob_shape_t *shape, const void 
  *                    would be seen in p (and where it overflows), a row's log-sum-exp is formed
  *                    again from its logits, at the price of a second reading of them.
  *   d_logits [rows, vocab]: the logits' dtype; may be the logits themselves when their
- *                    stride is vocab. */
+ *                    stride is vocab.
+ * Errors as for gdn_token_logprob_fwd; GDN_E_SHAPE also where rows * ceil(vocab / 2048) (4096 for
+ * BF16) passes 2^31 - 1, which no gradient under 2^41 values does. */
 gdn_status_t gdn_token_logprob_bwd(const gdn_logprob_shape_t *shape, const void *logits,
                                    const void *ids, const float *lse, const float *d_logp,
                                    const float *entropy, const float *d_entropy,
