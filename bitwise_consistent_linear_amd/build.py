@@ -165,5 +165,5 @@ def device_asm(out_path: str, sources=None) -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True))
-    print(build_policy(verbose=True))
     print(build_probe(verbose=True))
+    print(build_policy(verbose=True))
