@@ -274,17 +274,19 @@ __device__ __forceinline__ Softmax row_again(const LogprobArgs &p, int64_t off) 
   return a;
 }
 
+// What a row's gradient is made of: scale d_logp, scale d_entropy, the entropy.
+struct RowGrad {
+  float g, h, H;
+};
+
 // The gradient of the span of a row that begins at c0, with log p = scale (x - m) - ls; zeros
 // where the row is not used.
 template <bool B16, bool ENT>
 __device__ __forceinline__ void put_gradient(const LogprobArgs &p, int64_t row, int64_t id,
-                                             bool use, float m, float ls, int64_t c0) {
+                                             bool use, RowGrad r, float m, float ls, int64_t c0) {
   constexpr int J = bwd_vecs(B16);
   const int64_t V = p.vocab;
   const float scale = p.scale;
-  const float g = use ? p.d_logp[row] * scale : 0.0f;
-  const float h = ENT && use ? p.d_entropy[row] * scale : 0.0f;
-  const float H = ENT && use ? p.entropy[row] : 0.0f;
   Vec8<B16> x[J];
   if (use) {
 #pragma unroll
@@ -303,10 +305,10 @@ __device__ __forceinline__ void put_gradient(const LogprobArgs &p, int64_t row, 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float z = fmaf(x[j].get(e) - m, scale, -ls), q = exp_of(z);
-        float k = g;
-        if (ENT) k = fmaf(h, z + H, g);
+        float k = r.g;
+        if (ENT) k = fmaf(r.h, z + r.H, r.g);
         d[e] = q == 0.0f ? 0.0f : -q * k;
-        if (e == at) d[e] += g;
+        if (e == at) d[e] += r.g;
       }
     }
     store_row<B16>(p.d_logits, row * V, c, V, d);
@@ -315,10 +317,11 @@ __device__ __forceinline__ void put_gradient(const LogprobArgs &p, int64_t row, 
 
 // A workgroup takes a span of a row. All of a row far from zero is one workgroup's, and the row's
 // others have nothing to do; which one it is changes with the row so that they spread over the
-// XCDs, which take workgroups in turn (8192 x 65536 bf16 720 us where near rows take 343, and
-// 4600 with the first workgroup of every row; 8 x 131072 binary32 60 and 3). The registers of
-// the far rows' loops are the near ones' too: with 64 of them 64 x 131072 bf16 near zero took
-// 8.2 us, with 36 7.4.
+// XCDs, which take workgroups in turn (8192 x 65536 bf16 674 us where near rows take 337, and
+// 4600 with the first workgroup of every row; 8 x 131072 binary32 55 and 4). The registers of the
+// far rows' loops are the near ones' too: with 66 of them 64 x 131072 bf16 near zero took 8.2 us,
+// with 34 7.2. The row's values are read before the branch, where they are scalar loads: after
+// it, through the vector memory, the 337 us were 356.
 template <bool B16, bool ENT>
 __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobArgs p) {
   constexpr int kSpan = bwd_span(B16);
@@ -327,8 +330,14 @@ __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobA
   const int64_t id = id_of(p, row);
   const float lse = p.lse[row];
   const bool use = scored(p, id);
+  RowGrad r{0.0f, 0.0f, 0.0f};
+  if (use) {
+    r.g = p.d_logp[row] * p.scale;
+    if (ENT) r.h = p.d_entropy[row] * p.scale;
+    if (ENT) r.H = p.entropy[row];
+  }
   if (__builtin_expect(!use || fabsf(lse) < kNearLse, 1)) {
-    put_gradient<B16, ENT>(p, row, id, use, 0.0f, lse, span * kSpan);
+    put_gradient<B16, ENT>(p, row, id, use, r, 0.0f, lse, span * kSpan);
     return;
   }
   const int64_t low = spans % 8 == 0 ? 8 : spans & -spans;  // row * spans mod 8: 8 / low places
@@ -337,7 +346,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprob_bwd_kernel(const LogprobA
   const bool any = a.s != 0.0f;  // else every logit is -infinity; a NaN stays
   const float ls = logf(a.s);
   for (int64_t c0 = 0; c0 < p.vocab; c0 += kSpan)
-    put_gradient<B16, ENT>(p, row, id, any, a.m, ls, c0);
+    put_gradient<B16, ENT>(p, row, id, any, r, a.m, ls, c0);
 }
 
 // A launch holds at most 2^32 - 1 threads, so more rows go in several: `fn` over runs of rows
