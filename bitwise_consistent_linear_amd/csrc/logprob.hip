@@ -11,7 +11,8 @@
 // the vocabulary alone and a row has the same bits in any batch.
 //
 // Backward: elementwise in the logits, bound by reading them and writing the gradient: 8192 x
-// 65536 bf16 with the entropy's term 348 us (6.0 TB/s), 1021 x 50021 binary32 74 us (5.3 TB/s).
+// 65536 bf16 with the entropy's term 338 us (6.2 TB/s), 1021 x 50021 binary32 73 us (5.4 TB/s).
+// It takes differences too: from the lse where that is next to zero, else from the row's maximum.
 
 #include "policy_internal.h"
 #include "policy_rows.hpp"
@@ -237,8 +238,8 @@ int fwd_threads(int64_t vocab) {
   const int64_t tiles = (vocab + kMost - 1) / kMost, each = (vocab + tiles - 1) / tiles;
   return (int)((each + 64 * 8 * kFwdVecs - 1) / (64 * 8 * kFwdVecs)) * 64;
 }
-// Runs of eight values a thread: 32 bytes of either type (4096 x 65536 binary32 takes 344 us
-// with one run and 372 with two, 8192 x 65536 bf16 355 with two and 402 with one).
+// Runs of eight values a thread: 32 bytes of either type (4096 x 65536 binary32 takes 342 us
+// with one run and 363 with two, 8192 x 65536 bf16 345 with two and 405 with one).
 constexpr int kBwdThreads = 256;
 constexpr int bwd_vecs(bool bf16) { return bf16 ? 2 : 1; }
 constexpr int bwd_span(bool bf16) { return kBwdThreads * 8 * bwd_vecs(bf16); }

@@ -9,9 +9,9 @@
 // in registers, the next row's loads in flight under the current one.
 //
 // Measured (bf16): forward of 16384 x 4096 45 us (6.0 TB/s), backward 78 us with its column
-// sums (5.2 TB/s of the x, dy and dx that it cannot do without; a large copy reaches 4.9).
+// sums (5.2 TB/s of the x, dy and dx that it cannot do without; a large copy reaches 4.7 to 4.9).
 // Rows of odd width use the same 16-byte accesses at their element's alignment: backward of
-// 4099 x 2049 binary32 24.8 us (4.1 TB/s: 257 of a row's 320 threads have values, and 4 us are
+// 4099 x 2049 binary32 24 us (4.2 TB/s: 257 of a row's 320 threads have values, and 4 us are
 // the second launch).
 //
 // The reduction order depends on the width alone, so a row has the same bits in every batch.
