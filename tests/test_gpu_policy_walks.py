@@ -1,8 +1,8 @@
-"""Loops over rows and sequences past their first round. Sizes follow the launch rules: more rows
+"""Loops over rows and sequences past their first iteration. Sizes follow the launch rules: more rows
 than a launch has groups of threads for (forward norm 2048 workgroups, 256 of rows wider than
 8192; backward 256; quantisation 2048, or 262144 threads of rows longer than 16384; sums of
 sequences 65536 workgroups of 64), in every variant of a kernel. The same bits as in batches
-small enough for one round, and the last rows against the 64-bit form."""
+small enough for one iteration, and the last rows against the 64-bit form."""
 
 import numpy as np
 import pytest
@@ -106,7 +106,7 @@ def policy(logp, old, adv, ref, ent, mask, cu, clip, kl_coef, ent_coef, reductio
 @pytest.mark.parametrize("reduction", ["token", "sequence"])
 @pytest.mark.parametrize("N,T", [(5000, 90000), (300000, 200000), (4300000, 150000)])
 def test_policy_of_many_sequences(N, T, reduction):
-    """A search of three rounds (over 4096 sequences) and of four (over 262144), and more than
+    """A search in three steps (over 4096 sequences) and in four (over 262144), and more than
     65536 workgroups' sequences; short and empty ones, many more than tokens at the last."""
     log(f"policy {N} sequences {T} tokens {reduction}")
     rng = np.random.default_rng(N)
