@@ -1,5 +1,7 @@
-"""Binding of libgdn_cpr.so (the C ABI declared in include/gdn_cpr.h) by ctypes, and of
-libgdn_policy.so (the policy-head operators, include/gdn_policy.h) by _policy_binding.so.
+"""Binding of libgdn_cpr.so (the C ABI declared in include/gdn_cpr.h) by ctypes, of
+libgdn_policy.so (the policy-head operators, include/gdn_policy.h) by _policy_binding.so, and of
+libgdn_step.so (sampling, the 8-bit floating-point product and the optimiser,
+include/gdn_step.h) by _step_binding.so.
 
 Argument marshalling only: the functions check torch tensor dtypes, devices and
 contiguity, allocate outputs that the caller did not pass, and call the C entry point of
@@ -16,6 +18,7 @@ from functools import lru_cache
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn_cpr.so")
 POLICY_LIB_PATH = os.path.join(PKG, "libgdn_policy.so")
+STEP_LIB_PATH = os.path.join(PKG, "libgdn_step.so")
 
 GDN_OK, GDN_E_NULL, GDN_E_SHAPE, GDN_E_UNSUPPORTED, GDN_E_IDENTITY, GDN_E_DEVICE = range(6)
 GDN_DTYPE_F32, GDN_DTYPE_BF16 = 0, 1
@@ -679,24 +682,32 @@ def _refuse_rows(t, name, dtypes):
 _policy_calls = None
 
 
+def _setup_calls(calls):
+    """Hands a binding module torch's functions, those that raise for a tensor, and the tuples
+    of dtypes for them (in the order of Types in csrc/torch_binding.hpp)."""
+    torch = _torch()
+    f32, bf16, i32, i64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+    e4m3, e5m2 = torch.float8_e4m3fn, torch.float8_e5m2
+    calls.setup(torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _refuse,
+                _refuse_rows, _need, GdnError,
+                ((f32,), (f32, bf16), (torch.int8,), (i32, i64), (torch.bool, torch.uint8),
+                 (i32,), (torch.uint8,), (bf16,), (e4m3, e5m2), (e4m3,), (e5m2,),
+                 (torch.float8_e8m0fnu,), (f32, torch.float64), (i64,)))
+
+
 def _policy():
     """The module that checks tensors, allocates outputs and enters libgdn_policy.so
     (csrc/policy_binding.cpp): these calls take microseconds on the GPU, and so do as many
     steps in Python. Raises if it has not been built."""
     global _policy_calls
     if _policy_calls is None:
-        torch = _torch()
         policy_lib()
         try:
             from . import _policy_binding as calls
         except ImportError as e:
             raise RuntimeError("_policy_binding.so is missing or of another torch: build it "
                                "with __graft_entry__.build()") from e
-        f32, bf16 = torch.float32, torch.bfloat16
-        calls.setup(torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _refuse,
-                    _refuse_rows, _need, GdnError,
-                    ((f32,), (f32, bf16), (torch.int8,), (torch.int32, torch.int64),
-                     (torch.bool, torch.uint8), (torch.int32,), (torch.uint8,), (bf16,)))
+        _setup_calls(calls)
         _policy_calls = calls
     return _policy_calls
 
@@ -873,3 +884,254 @@ def policy_loss_bwd(logp, old_logp, advantages, weight, *, ref_logp=None, entrop
     return _policy().policy_bwd(logp, old_logp, advantages, ref_logp, entropy, mask, cu_seqlens,
                                 _reduction(reduction), clip_low, clip_high, dual_clip, kl_coef,
                                 entropy_coef, weight, d_loss, d_logp, d_entropy)
+
+
+# ------------------------------------------------------------- operators around the policy head
+
+GDN_F8_E4M3, GDN_F8_E5M2 = 0, 1
+GDN_STATE_F32, GDN_STATE_8BIT = 0, 1
+GDN_MOMENT_M, GDN_MOMENT_V = 0, 1
+F8_BLOCK = 128     # GDN_F8_BLOCK
+ADAMW_BLOCK = 256  # GDN_ADAMW_BLOCK
+_F8_FORMATS = {"e4m3": GDN_F8_E4M3, "e5m2": GDN_F8_E5M2}
+_F8_LAYOUTS = {"rows": 1, "columns": 2, "both": 3}
+
+
+class GdnLinearF8Shape(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("dy_stride", ctypes.c_int64), ("dy_dtype", ctypes.c_int32),
+                ("dy_format", ctypes.c_int32), ("dx_dtype", ctypes.c_int32),
+                ("dw_dtype", ctypes.c_int32)]
+
+
+class GdnSampleShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("logits_stride", ctypes.c_int64), ("logits_dtype", ctypes.c_int32),
+                ("u_bytes", ctypes.c_int32), ("id_bytes", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("temperature", ctypes.c_double),
+                ("top_p", ctypes.c_double), ("min_p", ctypes.c_double)]
+
+
+class GdnGradTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("grad", ctypes.c_void_p)]
+
+
+class GdnAdamwTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64)] + [(name, ctypes.c_void_p) for name in (
+        "param", "grad", "m", "v", "m_scale", "v_scale", "master")]
+
+
+class GdnAdamwShape(ctypes.Structure):
+    _fields_ = [("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("state", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("step", ctypes.c_int64)]
+
+
+_step_lib = None
+
+
+def step_lib():
+    """The loaded libgdn_step.so; raises if it has not been built."""
+    global _step_lib
+    if _step_lib is None:
+        if not os.path.exists(STEP_LIB_PATH):
+            raise RuntimeError(f"{STEP_LIB_PATH} is missing: build it with "
+                               "__graft_entry__.build()")
+        L = ctypes.CDLL(STEP_LIB_PATH)
+        P, I32, I64, D = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+        SZ, SZP = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        FS, SS, GT, AT, AS = (ctypes.POINTER(c) for c in (
+            GdnLinearF8Shape, GdnSampleShape, GdnGradTensor, GdnAdamwTensor, GdnAdamwShape))
+        for name, args in {
+            "gdn_step_abi_version": [],
+            "gdn_quantize_f8": [P, I64, I64, I64, I32, I32, P, P, P, P, P],
+            "gdn_linear_f8_fwd": [I64, I64, I64, I32, P, P, P, P, I32, P, P],
+            "gdn_linear_f8_bwd_workspace": [FS, SZP],
+            "gdn_linear_f8_bwd": [FS, P, P, P, P, P, P, P, P, SZ, P],
+            "gdn_sample_tokens_workspace": [SS, SZP],
+            "gdn_sample_tokens": [SS, P, P, P, P, P, P, P, P, P, SZ, P],
+            "gdn_grad_norm_workspace": [GT, I64, SZP],
+            "gdn_grad_norm": [GT, I64, I32, D, P, P, P, SZ, P],
+            "gdn_adamw_step": [AS, AT, I64, P, P, P, P],
+            "gdn_adamw_state_values": [P, P, I64, I32, P, P],
+        }.items():
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = I32, args
+        L.gdn_step_last_error.restype = ctypes.c_char_p
+        L.gdn_step_last_error.argtypes = []
+        _step_lib = L
+    return _step_lib
+
+
+def _step_check(status: int):
+    if status != GDN_OK:
+        raise GdnError(status, step_lib().gdn_step_last_error().decode())
+
+
+def step_abi_version() -> int:
+    return step_lib().gdn_step_abi_version()
+
+
+_step_calls = None
+
+
+def _step():
+    """As _policy(), for libgdn_step.so (csrc/step_binding.cpp)."""
+    global _step_calls
+    if _step_calls is None:
+        step_lib()
+        try:
+            from . import _step_binding as calls
+        except ImportError as e:
+            raise RuntimeError("_step_binding.so is missing or of another torch: build it "
+                               "with __graft_entry__.build()") from e
+        _setup_calls(calls)
+        _step_calls = calls
+    return _step_calls
+
+
+def _f8_format(fmt):
+    if fmt not in _F8_FORMATS:
+        raise ValueError(f"fmt must be 'e4m3' or 'e5m2', got {fmt!r}")
+    return _F8_FORMATS[fmt]
+
+
+def _is_bf16(dtype, name):
+    torch = _torch()
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
+    return dtype is torch.bfloat16
+
+
+def quantize_f8(x, *, fmt="e4m3", layout="rows", q=None, scale=None, qt=None, scale_t=None,
+                stream=None):
+    """gdn_quantize_f8: x [M, K] (float32 or bfloat16; rows may have a stride) in 8-bit floating
+    point, "e4m3" or "e5m2", with a power-of-two scale for each block of F8_BLOCK values. Serves
+    a linear layer's inputs and its weights [N, K]; by columns, what its gradients need of them.
+    layout "rows": (q [M, K rounded up to F8_BLOCK, zeros in the padding], scale
+    float8_e8m0fnu [ceil(K / 512), M rounded up to 4, 4]); "columns": the transpose's, (qt [K, M
+    rounded up], scale_t); "both": the four, from one reading of x. Row i's block b has its scale
+    at [b // 4, i, b % 4]."""
+    if stream is not None:
+        return _elsewhere(stream, quantize_f8, x, fmt=fmt, layout=layout, q=q, scale=scale,
+                          qt=qt, scale_t=scale_t)
+    if layout not in _F8_LAYOUTS:
+        raise ValueError(f"layout must be 'rows', 'columns' or 'both', got {layout!r}")
+    return _step().quantize_f8(x, _f8_format(fmt), _F8_LAYOUTS[layout], q, scale, qt, scale_t)
+
+
+def linear_f8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, stream=None):
+    """gdn_linear_f8_fwd: Y = X W^T of the values that 8-bit operands stand for, summed in
+    binary32 in an order that the sizes do not change. xq [M, Kp] float8_e4m3fn or float8_e5m2,
+    wq [N, Kp] float8_e4m3fn, with their scales, as quantize_f8 returns them. Returns y [M, N] in
+    out_dtype (float32 by default, or bfloat16)."""
+    if stream is not None:
+        return _elsewhere(stream, linear_f8_fwd, xq, x_scale, wq, w_scale, out_dtype=out_dtype,
+                          y=y)
+    if out_dtype is None:
+        out_dtype = _torch().float32 if y is None else y.dtype
+    return _step().linear_f8(xq, x_scale, wq, w_scale, _is_bf16(out_dtype, "out_dtype"), y)
+
+
+def linear_f8_bwd_workspace_bytes(shape: GdnLinearF8Shape) -> int:
+    """gdn_linear_f8_bwd_workspace: device bytes the product's backward needs."""
+    n = ctypes.c_size_t(0)
+    _step_check(step_lib().gdn_linear_f8_bwd_workspace(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def linear_f8_bwd(dy, wtq=None, wt_scale=None, xtq=None, xt_scale=None, *, fmt="e4m3",
+                  dx_dtype=None, dw_dtype=None, dx=None, dw=None, workspace=None, stream=None):
+    """gdn_linear_f8_bwd: gradients of Y = X W^T given dy [M, N] (float32 or bfloat16; rows may
+    have a stride), which is held in 8 bits of format ``fmt`` for both products. wtq [K, N
+    rounded up] and wt_scale are quantize_f8(w, layout="columns"), xtq [K, M rounded up] and
+    xt_scale that of x; without one of the pairs its gradient is None. ``workspace`` is a uint8
+    GPU tensor of at least linear_f8_bwd_workspace_bytes() bytes (allocated here when omitted).
+    Returns (dx [M, K] in dx_dtype, dy's by default, dw [N, K] in dw_dtype, float32 by
+    default)."""
+    if stream is not None:
+        return _elsewhere(stream, linear_f8_bwd, dy, wtq, wt_scale, xtq, xt_scale, fmt=fmt,
+                          dx_dtype=dx_dtype, dw_dtype=dw_dtype, dx=dx, dw=dw,
+                          workspace=workspace)
+    torch = _torch()
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch tensor")
+    if dx_dtype is None:
+        dx_dtype = dy.dtype if dx is None else dx.dtype
+    if dw_dtype is None:
+        dw_dtype = torch.float32 if dw is None else dw.dtype
+    return _step().linear_f8_bwd(dy, wtq, wt_scale, xtq, xt_scale, _f8_format(fmt),
+                                 _is_bf16(dx_dtype, "dx_dtype"), _is_bf16(dw_dtype, "dw_dtype"),
+                                 dx, dw, workspace)
+
+
+def sample_tokens_workspace_bytes(shape: GdnSampleShape) -> int:
+    """gdn_sample_tokens_workspace: device bytes the draw needs (often 0)."""
+    n = ctypes.c_size_t(0)
+    _step_check(step_lib().gdn_sample_tokens_workspace(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def sample_tokens(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, id_dtype=None,
+                  ids=None, logp=None, workspace=None, stream=None):
+    """gdn_sample_tokens: one token of each row of logits [M, V] (float32 or bfloat16; rows may
+    have a stride) by the random numbers u [M] in [0, 1) (float32 or float64). temperature, top_p
+    and min_p are numbers or float32 tensors [M], top_k a number or an int32 tensor [M];
+    temperature 0 is the largest logit, top_k 0, top_p 1 and min_p 0 are off. A row's token does
+    not depend on the others. ``workspace`` is a uint8 GPU tensor of at least
+    sample_tokens_workspace_bytes() bytes (allocated here when omitted).
+    Returns (ids [M] in id_dtype, int64 by default or int32, -1 for a row without a token,
+    logp [M] float32: the log-probability of the token among those that were left)."""
+    if stream is not None:
+        return _elsewhere(stream, sample_tokens, logits, u, temperature=temperature, top_k=top_k,
+                          top_p=top_p, min_p=min_p, id_dtype=id_dtype, ids=ids, logp=logp,
+                          workspace=workspace)
+    torch = _torch()
+    if id_dtype is None:
+        id_dtype = torch.int64 if ids is None else ids.dtype
+    if id_dtype is not torch.int64 and id_dtype is not torch.int32:
+        raise TypeError(f"id_dtype must be torch.int32 or torch.int64, got {id_dtype}")
+    return _step().sample_tokens(logits, u, temperature, top_k, top_p, min_p,
+                                 id_dtype is torch.int64, ids, logp, workspace)
+
+
+def grad_norm(grads, *, max_norm=float("inf"), norm=None, factor=None, workspace=None,
+              stream=None):
+    """gdn_grad_norm: the 2-norm of all values of the gradients together (a list of dense tensors
+    of one dtype, float32 or bfloat16) and the factor min(1, max_norm / (norm + 1e-6)) that clips
+    it, NaN where the norm is not finite. ``workspace`` is a uint8 GPU tensor as large as
+    gdn_grad_norm_workspace says (allocated here when omitted). Returns (norm [1], factor [1]),
+    float32; nothing is copied to the host."""
+    if stream is not None:
+        return _elsewhere(stream, grad_norm, grads, max_norm=max_norm, norm=norm, factor=factor,
+                          workspace=workspace)
+    return _step().grad_norm(grads, max_norm, norm, factor, workspace)
+
+
+def adamw_step(params, grads, m, v, step, *, m_scale=None, v_scale=None, master=None, lr=1e-3,
+               betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=None, stream=None):
+    """gdn_adamw_step: one AdamW update of lists of dense tensors in place, all in one launch for
+    up to 52 of them. params and grads float32 or bfloat16, each list of one dtype; m and v
+    float32, or m float8_e4m3fn and v uint8 with float32 lists m_scale and v_scale of
+    ceil(numel / ADAMW_BLOCK) values (all zeros at the start); master: float32 weights behind
+    bfloat16 params. step (1 for the first) is a number or an int64 tensor [1], lr a number or
+    a float32 tensor [1]; grad_scale a float32 tensor [1] that gradients are multiplied by, such
+    as grad_norm's factor: one that is not finite skips the step."""
+    if stream is not None:
+        return _elsewhere(stream, adamw_step, params, grads, m, v, step, m_scale=m_scale,
+                          v_scale=v_scale, master=master, lr=lr, betas=betas, eps=eps,
+                          weight_decay=weight_decay, grad_scale=grad_scale)
+    beta1, beta2 = betas
+    _step().adamw_step(params, grads, m, v, step, m_scale, v_scale, master, lr, beta1, beta2,
+                       eps, weight_decay, grad_scale)
+
+
+def adamw_state_values(codes, scale, *, out=None, stream=None):
+    """gdn_adamw_state_values: the float32 values that an 8-bit state of adamw_step stands for: m
+    of float8_e4m3fn codes, v of uint8 codes, with their scales. Returns a tensor of the codes'
+    shape."""
+    if stream is not None:
+        return _elsewhere(stream, adamw_state_values, codes, scale, out=out)
+    return _step().adamw_state_values(codes, scale, out)

@@ -1,4 +1,5 @@
-"""Build libgdn_cpr.so and libgdn_policy.so in-tree with hipcc for gfx950 (cross-compiles without a GPU).
+"""Build libgdn_cpr.so, libgdn_policy.so and libgdn_step.so in-tree with hipcc for gfx950
+(cross-compiles without a GPU).
 
 Flags that the contract depends on:
   -ffp-contract=off                  no fusion other than the explicit fmaf
@@ -41,6 +42,9 @@ FLAGS = [
 POLICY_LIB = os.path.join(PKG, "libgdn_policy.so")
 POLICY_BINDING = os.path.join(PKG, "_policy_binding.so")
 POLICY_SOURCES = ["norm.hip", "linear_i8.hip", "logprob.hip", "policy_loss.hip", "policy_api.cpp"]
+STEP_LIB = os.path.join(PKG, "libgdn_step.so")
+STEP_BINDING = os.path.join(PKG, "_step_binding.so")
+STEP_SOURCES = ["linear_f8.hip", "sample.hip", "adamw.hip", "step_api.cpp"]
 
 
 def _build(sources, lib, verbose):
@@ -93,6 +97,14 @@ def build_policy(verbose: bool = False) -> str:
     return lib
 
 
+def build_step(verbose: bool = False) -> str:
+    """Build bitwise_consistent_linear_amd/libgdn_step.so (sampling, the 8-bit floating-point
+    product and the optimiser) and its Python binding, with the same flags; return its path."""
+    lib = _build(STEP_SOURCES, STEP_LIB, verbose)
+    build_step_binding(verbose)
+    return lib
+
+
 PROBE_LIB = os.path.join(PKG, "libgdn_probe.so")
 
 
@@ -114,33 +126,43 @@ def build_probe(verbose: bool = False) -> str:
 KERNEL_SOURCES = [s for s in SOURCES if s.endswith(".hip")]
 
 
-def build_policy_binding(verbose: bool = False) -> str:
-    """Build _policy_binding.so, the policy head's Python calls, against the installed torch;
-    return its path. Host code only. libgdn_policy.so is found beside it."""
+def _build_binding(source, library, module, verbose):
+    """Build a Python binding against the installed torch; return its path. Host code only. Its
+    library is found beside it."""
     import sysconfig
 
     import torch
 
     base = os.path.dirname(torch.__file__)
     abi = int(torch.compiled_with_cxx11_abi())
-    tmp = POLICY_BINDING + ".tmp"
+    tmp = module + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE,
            "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "policy_binding.cpp"), "-o", tmp,
+           os.path.join(CSRC, source), "-o", tmp,
            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_hip", "-ltorch_cpu",
            "-ltorch", "-lc10",
-           "-L", PKG, "-l:" + os.path.basename(POLICY_LIB), "-Wl,-rpath,$ORIGIN"]
+           "-L", PKG, "-l:" + os.path.basename(library), "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("failed to build _policy_binding.so")
-    os.replace(tmp, POLICY_BINDING)
-    return POLICY_BINDING
+        raise RuntimeError(f"failed to build {os.path.basename(module)}")
+    os.replace(tmp, module)
+    return module
+
+
+def build_policy_binding(verbose: bool = False) -> str:
+    """Build _policy_binding.so, the policy head's Python calls."""
+    return _build_binding("policy_binding.cpp", POLICY_LIB, POLICY_BINDING, verbose)
+
+
+def build_step_binding(verbose: bool = False) -> str:
+    """Build _step_binding.so, the Python calls of libgdn_step.so."""
+    return _build_binding("step_binding.cpp", STEP_LIB, STEP_BINDING, verbose)
 
 
 def device_asm(out_path: str, sources=None) -> str:
@@ -167,3 +189,4 @@ if __name__ == "__main__":
     print(build(verbose=True))
     print(build_probe(verbose=True))
     print(build_policy(verbose=True))
+    print(build_step(verbose=True))

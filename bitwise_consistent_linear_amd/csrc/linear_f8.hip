@@ -1,0 +1,677 @@
+// The linear region in 8-bit floating point on gfx950: blocks of 128 values quantised with a
+// power-of-two scale each, by rows and by columns, and the product of two such matrices on the
+// scaled matrix instructions.
+//
+// A scale is a power of two because the matrix unit applies those itself: the sums stay in the
+// unit's binary32 accumulator from the first block to the last, without a rescaling on the vector
+// unit for each block, and quantising is exact but for its one rounding. A value keeps as many
+// bits as with any other scale; what is lost is at most a factor 2 of the format's range below.
+//
+// Every kernel adds the products of a value of Y in one chain of the same instruction over
+// ascending k, so tile, schedule and number of rows change no bit of it.
+//
+// The instruction goes by Y's type. The 8-bit instructions add the products of eight neighbouring
+// k with every one cut off 13 bits below the largest's power of two (measured: beside 2^16 a
+// product of 2^3 is kept and one of 2^2 lost; eight places on all is kept), and the sums of eight
+// in binary32. Random operands come out 1.5e-5 off in the 2-norm, a hundredth of what rounding Y
+// to bf16 does (1.7e-3), so Y in bf16 takes them. Y in binary32 takes the bf16 instruction, half
+// as fast: an 8-bit value with its scale is exact in bf16, products are exact and their sums
+// binary32's (1e-7 off).
+
+#include <algorithm>
+
+#include "lds_tiles.hpp"
+#include "policy_rows.hpp"
+#include "step_internal.h"
+
+namespace gdn {
+namespace {
+
+using i32x8 = int __attribute__((ext_vector_type(8)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using f32x16 = float __attribute__((ext_vector_type(16)));
+
+// ------------------------------------------------------------------------- quantisation
+
+template <int N>
+__device__ __forceinline__ uint32_t max_rotated(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 | N, 0xF, 0xF, true));
+}
+// Largest over each row of 16 lanes.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  return max_rotated<1>(max_rotated<2>(max_rotated<4>(max_rotated<8>(v))));
+}
+
+// The bits of |x|, 0 for what is not finite.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? b : 0u;
+}
+
+// Exponent + 127 of a block's scale from the bits of its largest magnitude: the least e with
+// max <= 1.75 * 2^(emax + e), and -127 at the least.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t scale_of(uint32_t top) {
+  constexpr int emax = E5M2 ? 15 : 8;
+  const int e = (int)(top >> 23) - emax + ((top & 0x7FFFFFu) > 0x600000u);
+  return top == 0 ? 127u : (uint32_t)max(e, 0);
+}
+
+// 2^-e for a scale byte e + 127 (at most 247).
+__device__ __forceinline__ float inverse_of(uint32_t scale) {
+  return __uint_as_float((254u - scale) << 23);
+}
+
+// Four values rounded to the format, the first in the low byte.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d) {
+  if constexpr (E5M2) {
+    const int w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+  } else {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  }
+}
+
+// By rows: a wave takes 512 values of a row, four blocks of 16 lanes, and the word of their
+// scales. Rows up to a multiple of four only have their scales written.
+template <bool XB, bool E5M2>
+__global__ __launch_bounds__(256) void quantize_f8_rows_kernel(const QuantizeF8Args p) {
+  const int lane = threadIdx.x % 64;
+  const int64_t k_pad = (p.k + 127) / 128 * 128, groups = (p.k + 511) / 512;
+  const int64_t rows4 = (p.rows + 3) / 4 * 4, total = rows4 * groups;
+  for (int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; w < total;
+       w += (int64_t)gridDim.x * 4) {
+    const int64_t row = w / groups, g = w % groups, col = g * 512 + 8 * lane;
+    uint32_t scale = 127;
+    if (row < p.rows) {
+      Vec8<XB> x;
+      load_row(x, p.x, row * p.x_stride, col, p.k);
+      settle_row(x, col, p.k);
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, finite_bits(x.get(e)));
+      scale = scale_of<E5M2>(max16(top));
+      const float up = inverse_of(scale);
+      if (col < k_pad) {
+        uint32_t v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[h] = pack_f8<E5M2>(x.get(4 * h) * up, x.get(4 * h + 1) * up, x.get(4 * h + 2) * up,
+                               x.get(4 * h + 3) * up);
+        *reinterpret_cast<uint2 *>(p.q + row * k_pad + col) = make_uint2(v[0], v[1]);
+      } else {
+        scale = 127;
+      }
+    }
+    auto of = [&](int l) { return (uint32_t)__builtin_amdgcn_readlane((int)scale, l); };
+    const uint32_t word = of(0) | of(16) << 8 | of(32) << 16 | of(48) << 24;
+    if (lane == 0) reinterpret_cast<uint32_t *>(p.scale)[g * rows4 + row] = word;
+  }
+}
+
+// By columns, and by rows on the way where they are wanted: a workgroup takes a tile of 128 x
+// 128 values, its 16 groups of 16 lanes eight rows each, a lane eight columns. The transposed
+// bytes of a lane's 8 x 8 values go through LDS, a line of it for each column, so that columns
+// are stored 128 bytes at a time.
+template <bool XB, bool E5M2>
+__global__ __launch_bounds__(256) void quantize_f8_columns_kernel(const QuantizeF8Args p) {
+  constexpr int kLine = 128 + 16;
+  __shared__ __align__(16) uint8_t tile[128 * kLine];
+  __shared__ uint32_t tops[4][128];
+  const int lane = threadIdx.x % 16, group = threadIdx.x / 16, wave = threadIdx.x / 64;
+  const int64_t blocks_k = (p.k + 127) / 128, blocks_r = (p.rows + 127) / 128;
+  const int64_t k_pad = blocks_k * 128, rows_pad = blocks_r * 128;
+  const int64_t rows4 = (p.rows + 3) / 4 * 4, k4 = (p.k + 3) / 4 * 4;
+  const int64_t bk = blockIdx.x % blocks_k, br = blockIdx.x / blocks_k;
+  const int64_t col = bk * 128 + 8 * lane, row0 = br * 128 + 8 * group;
+  Vec8<XB> x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = row0 + i < p.rows ? row0 + i : p.rows - 1;
+    load_row(x[i], p.x, row * p.x_stride, col, p.k);
+  }
+  uint32_t top[8] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    settle_row(x[i], col, p.k);
+    if (row0 + i >= p.rows) x[i].zero();
+    uint32_t across = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = finite_bits(x[i].get(e));
+      across = max(across, b);
+      top[e] = max(top[e], b);
+    }
+    if (p.q) {
+      const uint32_t scale = scale_of<E5M2>(max16(across));
+      const float up = inverse_of(scale);
+      const int64_t row = row0 + i;
+      if (row < p.rows)
+        *reinterpret_cast<uint2 *>(p.q + row * k_pad + col) =
+            make_uint2(pack_f8<E5M2>(x[i].get(0) * up, x[i].get(1) * up, x[i].get(2) * up,
+                                     x[i].get(3) * up),
+                       pack_f8<E5M2>(x[i].get(4) * up, x[i].get(5) * up, x[i].get(6) * up,
+                                     x[i].get(7) * up));
+      if (lane == 0 && row < rows4) {
+        uint8_t *to = p.scale + (bk / 4 * rows4 + row) * 4;
+        to[bk % 4] = (uint8_t)scale;
+        if (bk == blocks_k - 1)
+          for (int b = (int)(bk % 4) + 1; b < 4; ++b) to[b] = 127;
+      }
+    }
+  }
+  // a column's largest value: over the wave's four groups, then over the waves
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    top[e] = max(top[e], (uint32_t)__shfl_xor((int)top[e], 16));
+    top[e] = max(top[e], (uint32_t)__shfl_xor((int)top[e], 32));
+    if (group % 4 == 0) tops[wave][8 * lane + e] = top[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = 8 * lane + e;
+    const uint32_t scale =
+        scale_of<E5M2>(max(max(tops[0][c], tops[1][c]), max(tops[2][c], tops[3][c])));
+    const float up = inverse_of(scale);
+    *reinterpret_cast<uint2 *>(tile + c * kLine + 8 * group) =
+        make_uint2(pack_f8<E5M2>(x[0].get(e) * up, x[1].get(e) * up, x[2].get(e) * up,
+                                 x[3].get(e) * up),
+                   pack_f8<E5M2>(x[4].get(e) * up, x[5].get(e) * up, x[6].get(e) * up,
+                                 x[7].get(e) * up));
+    if (group == 0 && bk * 128 + c < k4) {
+      uint8_t *to = p.scale_t + (br / 4 * k4 + bk * 128 + c) * 4;
+      to[br % 4] = (uint8_t)scale;
+      if (br == blocks_r - 1)
+        for (int b = (int)(br % 4) + 1; b < 4; ++b) to[b] = 127;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = j * 256 + threadIdx.x, c = at / 8, part = at % 8 * 16;
+    if (bk * 128 + c < p.k)
+      *reinterpret_cast<i32x4 *>(p.qt + (bk * 128 + c) * rows_pad + br * 128 + part) =
+          *reinterpret_cast<const i32x4 *>(tile + c * kLine + part);
+  }
+}
+
+// ------------------------------------------------------------------------------ product
+
+// v_mfma_scale_f32_32x32x64_f8f6f4: lane l gives 32 values of row l % 32 of either operand, of
+// the first half of 64 k or (l >= 32) of the second, and their scale, byte `Sel` of a word; it
+// holds the results of rows 8 g + 4 (l / 32) + 0 .. 3 of the first operand, g = 0 .. 3, and row
+// l % 32 of the second. The first operand is W, so four results are neighbours in a row of Y.
+// Which of the 64 k a lane's bytes are is free as long as both operands agree.
+template <bool E5M2, int Sel>
+__device__ __forceinline__ f32x16 mfma(i32x8 w, i32x8 x, f32x16 acc, int ws, int xs) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 0, E5M2 ? 1 : 0, Sel, ws, Sel,
+                                                         xs);
+}
+
+// The same 64 k in four steps of v_mfma_f32_32x32x16_bf16: step t takes bytes 8 t .. + 7 of
+// either half's 32, widened with their scale (the exponent of a binary32).
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+template <bool E5M2>
+__device__ __forceinline__ bf16x8 widen(int lo, int hi, float scale) {
+  bf16x2 v[4];
+  if constexpr (E5M2) {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)lo, scale, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)lo, scale, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)hi, scale, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)hi, scale, true);
+  } else {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, scale, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, scale, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, scale, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, scale, true);
+  }
+  return bf16x8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+}
+template <int Sel>
+__device__ __forceinline__ float scale_as_float(int word) {
+  return __uint_as_float(((uint32_t)word >> (8 * Sel) & 255u) << 23);
+}
+
+__device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Few rows: W's bytes are what counts, each read once by a group of 32 MT rows, straight into
+// the operand registers. A wave takes 16 columns of Y and all of k, four blocks of 128 at a
+// time with the next four on their way; lanes of the instruction's other 16 columns hold zeros.
+template <int MT, bool E5M2, bool YB>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void linear_f8_rows_kernel(const LinearF8Args p) {
+  const int l = threadIdx.x, r = l % 32, half = l / 32;
+  const int64_t tiles_n = (p.n + 15) / 16;
+  const int64_t n0 = blockIdx.x % tiles_n * 16, m0 = blockIdx.x / tiles_n * (32 * MT);
+  const int64_t n4 = (p.n + 3) / 4 * 4, m4 = (p.m + 3) / 4 * 4;
+  const bool holds = r < 16;
+  const int64_t wrow = n0 + r % 16 < p.n ? n0 + r % 16 : p.n - 1;
+  const uint8_t *w = p.wq + wrow * p.k + 32 * half;
+  const uint32_t *ws = reinterpret_cast<const uint32_t *>(p.w_scale) + wrow;
+  const uint8_t *x[MT];
+  const uint32_t *xs[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = m0 + 32 * i + r < p.m ? m0 + 32 * i + r : p.m - 1;
+    x[i] = p.xq + row * p.k + 32 * half;
+    xs[i] = reinterpret_cast<const uint32_t *>(p.x_scale) + row;
+  }
+  f32x16 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x16{};
+  struct Turn {
+    i32x4 w[8][2], x[MT][8][2];
+    uint32_t ws, xs[MT];
+  };
+  const i32x4 zero = {0, 0, 0, 0};
+  auto at = [](const uint8_t *b, int k) { return *reinterpret_cast<const i32x4 *>(b + k); };
+  auto load = [&](Turn &t, int k0) {  // what lies past the end is zeros
+    const bool any = k0 < p.k;
+    t.ws = any ? ws[k0 / 512 * n4] : 0x7F7F7F7Fu;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) t.xs[i] = any ? xs[i][k0 / 512 * m4] : 0x7F7F7F7Fu;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int k = k0 + 64 * s;
+      const bool in = k < p.k;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        t.w[s][h] = in && holds ? at(w, k + 16 * h) : zero;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) t.x[i][s][h] = in ? at(x[i], k + 16 * h) : zero;
+      }
+    }
+  };
+  auto two = [&](const Turn &t, auto sel) {
+    constexpr int S = decltype(sel)::value;
+#pragma unroll
+    for (int s = 2 * S; s < 2 * S + 2; ++s)
+      if constexpr (YB) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          acc[i] = mfma<E5M2, S>(join(t.w[s][0], t.w[s][1]), join(t.x[i][s][0], t.x[i][s][1]),
+                                 acc[i], (int)t.ws, (int)t.xs[i]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bf16x8 w = widen<false>(t.w[s][q / 2][q % 2 * 2], t.w[s][q / 2][q % 2 * 2 + 1],
+                                        scale_as_float<S>((int)t.ws));
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                w, widen<E5M2>(t.x[i][s][q / 2][q % 2 * 2], t.x[i][s][q / 2][q % 2 * 2 + 1],
+                               scale_as_float<S>((int)t.xs[i])),
+                acc[i], 0, 0, 0);
+        }
+      }
+  };
+  auto multiply = [&](const Turn &t) {
+    two(t, std::integral_constant<int, 0>{});
+    two(t, std::integral_constant<int, 1>{});
+    two(t, std::integral_constant<int, 2>{});
+    two(t, std::integral_constant<int, 3>{});
+  };
+  Turn t0, t1;
+  load(t0, 0);
+  for (int k = 0; k < p.k; k += 1024) {
+    load(t1, k + 512);
+    multiply(t0);
+    load(t0, k + 1024);
+    multiply(t1);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = m0 + 32 * i + r;
+    if (m < p.m)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t n = n0 + 8 * g + 4 * half + e;
+          if (n < p.n) {
+            if (YB)
+              static_cast<uint16_t *>(p.y)[m * p.n + n] = to_bf16(acc[i][4 * g + e]);
+            else
+              static_cast<float *>(p.y)[m * p.n + n] = acc[i][4 * g + e];
+          }
+        }
+  }
+}
+
+__device__ __forceinline__ void load_word_to_lds(const void *base, uint32_t offset, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %2"
+      :: "s"(to), "v"(offset), "s"(base) : "memory", "m0");
+}
+
+// A BN x BM tile of Y by (BN / TN) x (BM / TM) waves, each TN columns by TM rows.
+//
+// K goes through LDS in stages of 64 bytes of every row of the tile, four buffers of one stage
+// each: loads straight from memory into LDS run three stages ahead, and the operands of the
+// next stage are read from LDS under the products of the current one, interleaved with them. A
+// stage has one barrier: past it, the next stage has arrived for every wave and the buffer of
+// the current one, in registers by now, is free for the stage four ahead. The loads and their
+// waits are the instructions themselves (see load_to_lds and arrive).
+//
+// A row's 64 bytes are four 16-byte chunks, chunk c of row r at place c ^ (r / 4 % 4). 16 lanes
+// of an operand read are served together (0 - 3, 12 - 15 and 20 - 27, the others likewise): of
+// four rows that begin at the same of the 64 banks, these have the keys 0 to 3, so the lanes
+// meet no bank twice.
+//
+// The scales of eight stages, a word for each row, are loaded eight stages ahead into one of
+// two buffers beside the operands'.
+constexpr int chunk_key_shift = 2;
+__device__ __forceinline__ int chunk_key(int r) { return r >> chunk_key_shift & 3; }
+
+template <int BM, int BN, int TM, int TN, bool E5M2, bool YB, bool Through>
+__global__ __launch_bounds__(BM / TM *(BN / TN) * 64) __attribute__((amdgpu_waves_per_eu(2)))
+void linear_f8_tile_kernel(const LinearF8Args p) {
+  constexpr int kWaves = BM / TM * (BN / TN), MI = TM / 32, NJ = TN / 32;
+  constexpr int kLoads = (BM + BN) / 16 / kWaves;  // 1 KiB (16 rows) each, per wave and stage
+  constexpr int kStage = (BM + BN) * 64, kWords = (BM + BN) / 64;
+  static_assert((BM + BN) / 16 % kWaves == 0, "whole loads");
+  static_assert(kWords <= kWaves, "a load of scales a wave at most");
+  static_assert(kStage * 4 / kWaves >= 32 * TN * 4, "a wave's share of LDS holds 32 rows");
+  __shared__ __align__(128) uint8_t lds[4 * kStage];
+  __shared__ __align__(128) uint32_t scales[2][BM + BN];
+  const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  // tiles: each XCD (workgroup % 8) a run of neighbours, in bands of 8 tiles of rows
+  const int64_t tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
+  const int64_t total = tiles_m * tiles_n, per = (total + 7) / 8;
+  const int64_t tile = blockIdx.x % 8 * per + blockIdx.x / 8;
+  if (tile >= total) return;
+  const int64_t band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
+  const int64_t height = tiles_m - 8 * band < 8 ? tiles_m - 8 * band : 8;
+  const int64_t m0 = (8 * band + in_band % height) * BM, n0 = in_band / height * BN;
+
+  // the wave's loads of a stage: a base in scalar registers and an offset per lane (below
+  // 256 rows of 2^20 bytes); rows past the end repeat the last one
+  const uint8_t *wbase = p.wq + n0 * p.k, *xbase = p.xq + m0 * p.k;
+  const int last_w = (int)(p.n - n0 < BN ? p.n - n0 : BN) - 1;
+  const int last_x = (int)(p.m - m0 < BM ? p.m - m0 : BM) - 1;
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = (wave * kLoads + i) * 16, r = at + l / 4;  // W's rows, then X's
+    const int row = at < BN ? (r < last_w ? r : last_w) : (r - BN < last_x ? r - BN : last_x);
+    off[i] = (uint32_t)row * p.k + 16 * (l % 4 ^ chunk_key(r));
+  }
+  auto place = [](const void *s) {
+    return __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)s);
+  };
+  const uint32_t lds_at = place(lds) + wave * kLoads * 1024;
+  int fk = 0;
+  auto fetch = [&](int buf) {  // past the last stage the first ones again, unread
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(((wave * kLoads + i) * 16 < BN ? wbase : xbase) + fk, off[i],
+                  lds_at + buf * kStage + i * 1024);
+    fk = fk + 64 < p.k ? fk + 64 : 0;
+  };
+  // scales: wave i loads the words of rows 64 i .. + 63 of W's, then X's
+  const int word_row = wave * 64 + l;
+  const bool of_w = wave * 64 < BN;
+  const uint32_t word_off =
+      4u * (of_w ? (word_row < last_w ? word_row : last_w)
+                 : (word_row - BN < last_x ? word_row - BN : last_x));
+  const int64_t group_bytes = ((of_w ? p.n : p.m) + 3) / 4 * 16;
+  const uint8_t *word_base = of_w ? p.w_scale + n0 * 4 : p.x_scale + m0 * 4;
+  const uint32_t words_at = place(scales) + wave * 256;
+  auto fetch_scales = [&](int buf) {
+    if (wave < kWords) load_word_to_lds(word_base, word_off, words_at + buf * (BM + BN) * 4);
+    word_base += group_bytes;
+  };
+
+  f32x16 acc[NJ][MI];
+  i32x4 xf[2][MI][2], wf[2][NJ][2];
+  int xsc[MI], wsc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < MI; ++i) acc[j][i] = f32x16{};
+  const int wn = wave % (BN / TN) * TN, wm = wave / (BN / TN) * TM;
+  const int r = l % 32, half = l / 32;
+  int lane_at[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) lane_at[h] = r * 64 + 16 * ((2 * half + h) ^ chunk_key(r));
+  auto read = [&](int buf, int b) {
+    const uint8_t *from = lds + buf * kStage;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        xf[b][i][h] =
+            *reinterpret_cast<const i32x4 *>(from + (BN + wm + 32 * i) * 64 + lane_at[h]);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        wf[b][j][h] = *reinterpret_cast<const i32x4 *>(from + (wn + 32 * j) * 64 + lane_at[h]);
+  };
+  auto read_scales = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) xsc[i] = (int)scales[buf][BN + wm + 32 * i + r];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) wsc[j] = (int)scales[buf][wn + 32 * j + r];
+  };
+  // One stage: the two stages after the next one may still be on their way.
+  auto step = [&](int cur, int b, auto sel) {
+    arrive<2 * kLoads>();
+    fetch(cur);
+    read((cur + 1) % 4, 1 - b);
+    constexpr int S = decltype(sel)::value;
+    if constexpr (YB) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+          acc[j][i] = mfma<E5M2, S>(join(wf[b][j][0], wf[b][j][1]),
+                                    join(xf[b][i][0], xf[b][i][1]), acc[j][i], wsc[j], xsc[i]);
+      // operand reads between the products
+#pragma unroll
+      for (int q = 0; q < MI * NJ; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x100, (2 * (MI + NJ) + MI * NJ - 1) / (MI * NJ), 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x8 x[MI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+          x[i] = widen<E5M2>(xf[b][i][q / 2][q % 2 * 2], xf[b][i][q / 2][q % 2 * 2 + 1],
+                             scale_as_float<S>(xsc[i]));
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const bf16x8 w = widen<false>(wf[b][j][q / 2][q % 2 * 2], wf[b][j][q / 2][q % 2 * 2 + 1],
+                                        scale_as_float<S>(wsc[j]));
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+            acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x[i], acc[j][i], 0, 0, 0);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  using S2 = std::integral_constant<int, 2>;
+  using S3 = std::integral_constant<int, 3>;
+  fetch_scales(0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fetch(i);
+  arrive<3 * kLoads>();  // the scales and the first stage are there
+  read(0, 0);
+  const int left = p.k % 512;
+  int k = 0, sb = 0;
+  for (; k + 512 <= p.k; k += 512, sb ^= 1) {
+    read_scales(sb);
+    if (k + 512 < p.k) fetch_scales(sb ^ 1);
+    step(0, 0, S0{});
+    step(1, 1, S0{});
+    step(2, 0, S1{});
+    step(3, 1, S1{});
+    step(0, 0, S2{});
+    step(1, 1, S2{});
+    step(2, 0, S3{});
+    step(3, 1, S3{});
+  }
+  if (left > 0) {
+    read_scales(sb);
+    step(0, 0, S0{});
+    step(1, 1, S0{});
+  }
+  if (left > 128) {
+    step(2, 0, S1{});
+    step(3, 1, S1{});
+  }
+  if (left > 256) {
+    step(0, 0, S2{});
+    step(1, 1, S2{});
+  }
+
+  // Results go through LDS, 32 rows of a wave at a time, so that neighbouring lanes store
+  // neighbouring values.
+  arrive<0>();  // every load has landed and every operand been read: LDS is free
+  uint8_t *own = lds + wave * (kStage * 4 / kWaves);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t mi = m0 + wm + 32 * i;
+    // row r of 32: TN values as 16-byte chunks (4 binary32 or 8 bf16), chunk c at c ^ r
+    constexpr int kChunk = YB ? 8 : 4, kChunks = TN / kChunk;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int n = 32 * j + 8 * g + 4 * half, c = (n / kChunk) ^ (r % kChunks);
+        uint8_t *at = own + (r * kChunks + c) * 16;
+        const float v[4] = {acc[j][i][4 * g], acc[j][i][4 * g + 1], acc[j][i][4 * g + 2],
+                            acc[j][i][4 * g + 3]};
+        if (YB)
+          *reinterpret_cast<uint2 *>(at + n % kChunk * 2) =
+              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else
+          *reinterpret_cast<f32x4 *>(at) = f32x4{v[0], v[1], v[2], v[3]};
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int g = 0; g < kChunks / 2; ++g) {
+      const int q = 64 * g + l, row = q / kChunks, c = q % kChunks;
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(
+          own + (row * kChunks + (c ^ (row % kChunks))) * 16);
+      const int64_t m = mi + row, n = n0 + wn + kChunk * c;
+      if (m < p.m) store_chunk<YB, Through>(p.n, p.y, m, n, v);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// A product over no k.
+__global__ __launch_bounds__(256) void linear_f8_zero_kernel(uint16_t *y, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    y[i] = 0;
+}
+
+struct Launch {
+  const void *fn;
+  int threads;
+  int64_t grid;
+};
+
+template <int MT, bool E>
+Launch rows_launch(const LinearF8Args &a) {
+  return {a.y_bf16 ? (const void *)linear_f8_rows_kernel<MT, E, true>
+                   : (const void *)linear_f8_rows_kernel<MT, E, false>,
+          64, (a.m + 32 * MT - 1) / (32 * MT) * ((a.n + 15) / 16)};
+}
+
+template <int BM, int BN, int TM, int TN, bool E>
+Launch tile_launch(const LinearF8Args &a) {
+  const int64_t total = (a.m + BM - 1) / BM * ((a.n + BN - 1) / BN);
+  const bool whole = a.n % (a.y_bf16 ? 8 : 4) == 0;  // rows of Y of whole 16-byte chunks
+  return {a.y_bf16 ? (whole ? (const void *)linear_f8_tile_kernel<BM, BN, TM, TN, E, true, true>
+                            : (const void *)linear_f8_tile_kernel<BM, BN, TM, TN, E, true, false>)
+                   : (whole ? (const void *)linear_f8_tile_kernel<BM, BN, TM, TN, E, false, true>
+                            : (const void *)linear_f8_tile_kernel<BM, BN, TM, TN, E, false, false>),
+          BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
+}
+
+template <bool E>
+Launch pick(const LinearF8Args &a) {
+  auto count = [&](int rows, int cols) {
+    return (a.m + rows - 1) / rows * ((a.n + cols - 1) / cols);
+  };
+  if (count(32, 16) <= 256) return rows_launch<1, E>(a);
+  if (count(64, 16) <= 256) return rows_launch<2, E>(a);
+  auto time = [&](int rows, int cols, double round) {
+    return (double)((count(rows, cols) + 255) / 256) * round;
+  };
+  const double t[5] = {time(256, 256, 62.0), time(128, 256, 37.0), time(128, 128, 23.0),
+                       time(64, 128, 17.0), time(64, 64, 10.5)};
+  switch (std::min_element(t, t + 5) - t) {
+    case 0: return tile_launch<256, 256, 64, 128, E>(a);
+    case 1: return tile_launch<128, 256, 64, 64, E>(a);
+    case 2: return tile_launch<128, 128, 64, 64, E>(a);
+    case 3: return tile_launch<64, 128, 32, 64, E>(a);
+    default: return tile_launch<64, 64, 32, 32, E>(a);
+  }
+}
+
+Launch pick(const LinearF8Args &a) { return a.e5m2 ? pick<true>(a) : pick<false>(a); }
+
+}  // namespace
+
+hipError_t launch_quantize_f8(const QuantizeF8Args &a, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  QuantizeF8Args args = a;
+  void *kargs[] = {&args};
+  if (!a.qt) {
+    const void *fn = a.x_bf16 ? (a.e5m2 ? (const void *)quantize_f8_rows_kernel<true, true>
+                                        : (const void *)quantize_f8_rows_kernel<true, false>)
+                              : (a.e5m2 ? (const void *)quantize_f8_rows_kernel<false, true>
+                                        : (const void *)quantize_f8_rows_kernel<false, false>);
+    const int64_t need = (f8_scale_rows(a.rows) * ((a.k + 511) / 512) + 3) / 4;
+    return hipLaunchKernel(fn, dim3((unsigned)std::min<int64_t>(need, 1 << 20)), dim3(256), kargs,
+                           0, stream);
+  }
+  const void *fn = a.x_bf16 ? (a.e5m2 ? (const void *)quantize_f8_columns_kernel<true, true>
+                                      : (const void *)quantize_f8_columns_kernel<true, false>)
+                            : (a.e5m2 ? (const void *)quantize_f8_columns_kernel<false, true>
+                                      : (const void *)quantize_f8_columns_kernel<false, false>);
+  const int64_t tiles = (a.rows + 127) / 128 * ((a.k + 127) / 128);  // at most 2^26
+  return hipLaunchKernel(fn, dim3((unsigned)tiles), dim3(256), kargs, 0, stream);
+}
+
+int64_t linear_f8_threads(const LinearF8Args &a) {
+  if (a.m == 0 || a.n == 0 || a.k == 0) return 0;
+  const Launch go = pick(a);
+  return go.grid * go.threads;
+}
+
+hipError_t launch_linear_f8(const LinearF8Args &a, hipStream_t stream) {
+  if (a.m == 0 || a.n == 0) return hipSuccess;
+  if (a.k == 0) {
+    int64_t halves = a.m * a.n * (a.y_bf16 ? 1 : 2);
+    uint16_t *y = static_cast<uint16_t *>(a.y);
+    void *kargs[] = {&y, &halves};
+    return hipLaunchKernel((const void *)linear_f8_zero_kernel,
+                           dim3((unsigned)std::min<int64_t>((halves + 255) / 256, 1 << 16)),
+                           dim3(256), kargs, 0, stream);
+  }
+  LinearF8Args args = a;
+  void *kargs[] = {&args};
+  const Launch go = pick(a);
+  return hipLaunchKernel(go.fn, dim3((unsigned)go.grid), dim3(go.threads), kargs, 0, stream);
+}
+
+}  // namespace gdn

@@ -7,13 +7,13 @@
 
 #include <algorithm>
 
+#include "lds_tiles.hpp"
 #include "policy_internal.h"
 #include "policy_rows.hpp"
 
 namespace gdn {
 namespace {
 
-using i32x4 = int __attribute__((ext_vector_type(4)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------------- quantisation
@@ -275,31 +275,6 @@ __global__ __launch_bounds__(512) void linear_i8_rows_kernel(const LinearI8Args 
   }
 }
 
-// Sixteen bytes of row m of Y from column n on: 4 binary32 or 8 bf16 values.
-template <bool YB, bool Through>
-__device__ __forceinline__ void store_chunk(const LinearI8Args &p, void *to, int64_t m, int64_t n,
-                                            i32x4 v) {
-  using unaligned = int __attribute__((ext_vector_type(4), aligned(YB ? 2 : 4)));
-  constexpr int kChunk = YB ? 8 : 4;
-  if (n + kChunk <= p.n) {
-    char *y = static_cast<char *>(to) + (m * p.n + n) * (YB ? 2 : 4);
-    if (Through)
-      __builtin_nontemporal_store(v, reinterpret_cast<unaligned *>(y));
-    else
-      *reinterpret_cast<unaligned *>(y) = v;
-  } else {
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e)
-      if (n + e < p.n) {
-        if (YB)
-          static_cast<uint16_t *>(to)[m * p.n + n + e] =
-              (uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2)));
-        else
-          static_cast<int *>(to)[m * p.n + n + e] = v[e];
-      }
-  }
-}
-
 // A BN x BM tile of Y by (BN / TN) x (BM / TM) waves, each TN columns by TM rows.
 //
 // K goes through LDS in stages of 64 bytes of every row of the tile, four buffers of one
@@ -332,27 +307,6 @@ __device__ __forceinline__ void store_chunk(const LinearI8Args &p, void *to, int
 // 82). Where rows start inside a 16-byte chunk the caches put the parts of a line together:
 // 597 x 38941 x 293 to binary32 took 47 us past them and 33 through them.
 __device__ __forceinline__ int chunk_key(int r) { return (r >> 3 & 1) * 3; }
-
-// 16 bytes per lane from base + offset to LDS, lane after lane from `to` (uniform) on.
-__device__ __forceinline__ void load_to_lds(const int8_t *base, uint32_t offset, uint32_t to) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"  // a wait state between writing m0 and its use
-      "global_load_lds_dwordx4 %1, %2"
-      :: "s"(to), "v"(offset), "s"(base) : "memory", "m0");
-}
-
-// At most `Loads` of the wave's loads are still on their way, every read of LDS is done, and
-// all waves are here.
-template <int Loads>
-__device__ __forceinline__ void arrive() {
-  static_assert(Loads < 64, "six bits of the counter");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Loads) : "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt = 0, which the compiler then knows
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 template <int BM, int BN, int TM, int TN, bool YB, bool Through>
 __global__ __launch_bounds__(BM / TM *(BN / TN) * 64) __attribute__((amdgpu_waves_per_eu(TM * TN > 8192 ? 1 : 2)))
@@ -480,7 +434,7 @@ void linear_i8_tile_kernel(const LinearI8Args p) {
       const int q = 64 * g + l, r = q / kChunks, c = q % kChunks;
       const i32x4 v = *reinterpret_cast<const i32x4 *>(own + (r * kChunks + (c ^ (r % kChunks))) * 16);
       const int64_t m = mi + r, n = n0 + wn + kChunk * c;
-      if (m < p.m) store_chunk<YB, Through>(p, to, m, n, v);
+      if (m < p.m) store_chunk<YB, Through>(p.n, to, m, n, v);
     }
     __builtin_amdgcn_wave_barrier();
   }
