@@ -33,6 +33,7 @@ inline int64_t f8_scale_bytes(int64_t r, int64_t c) {
 
 struct SampleArgs {
   int64_t rows, vocab, stride;
+  int64_t first;  // row of the launch, set by the launcher
   int32_t bf16, u64, id64, top_k, shift;  // a weight of 1 is 2^shift
   double temperature, top_p, min_p;
   const void *logits, *u;
