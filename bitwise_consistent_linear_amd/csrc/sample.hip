@@ -22,7 +22,7 @@ constexpr int kBins = 2048;
 constexpr int kList = 4096;       // candidates that LDS holds
 constexpr int kFew = 64;          // candidates that one wave ranks
 constexpr float kBinsPerNat = 64.0f;
-constexpr int kTable = 1024;      // steps of an octave in the table of powers of two
+constexpr int kTable = 32;        // steps of an octave in the table of powers of two
 
 __device__ __forceinline__ uint32_t key_of(float x) {  // a NaN above all, -0 as 0
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -89,8 +89,10 @@ struct Request {
 
 // exp((x - top) / T) in units of 2^-shift, to the nearest: y = (x - top) log2(e) / T in steps of
 // the table is split into a whole number and a rest of at most half a step, whose power of two
-// four terms of its series give to 2^-51. The table holds 2^(shift + i / kTable); a whole power
-// is added to its exponent.
+// six terms of its series give to 2^-48. The table holds 2^(shift + i / kTable); a whole power
+// is added to its exponent. Its 32 values lie in 64 banks of LDS, so that lanes never wait for
+// each other (with 1024 of them and four terms a random read took 23 cycles a wave and bounded
+// as much as these six do, and took a step of the kernel to fill).
 struct Weigh {
   const double *power;
   double top, rate, least;  // rate: kTable log2(e) / T
@@ -102,45 +104,31 @@ struct Weigh {
       power[i] = exp2((double)i / kTable + (double)shift);
   }
   static constexpr u64 kNone = 0x4330000000000000ull;  // the bits of 2^52
+  static constexpr double kMagic = 0x1.8p52;
+  // y to the nearest whole number, in the low word
+  __device__ __forceinline__ double whole(double d) const { return fma(d, rate, kMagic); }
+  __device__ __forceinline__ static int low(double t) { return (int)(uint32_t)(u64)__double_as_longlong(t); }
+  __device__ __forceinline__ double below(float x) const { return fmax((double)x - top, least); }
+  // the steps from x up to the top, 0 .. 64 kTable
+  __device__ __forceinline__ int steps(float x) const { return -low(whole(below(x))); }
   // the weight added to kNone
-  __device__ __forceinline__ u64 raw(float x) const {
-    const double d = fmax((double)x - top, least);
-    constexpr double magic = 0x1.8p52, c = 0.69314718055994530942 / kTable;
-    const double t = fma(d, rate, magic), r = fma(d, rate, magic - t);
-    const int n = (int)(uint32_t)(u64)__double_as_longlong(t);
-    const double q = r * fma(r, fma(r, c * c * c / 6, c * c / 2), c);
+  __device__ __forceinline__ u64 raw(float x) const { return raw_at(below(x)); }
+  __device__ __forceinline__ u64 raw_at(double d) const {
+    constexpr double c = 0.69314718055994530942 / kTable;
+    const double t = whole(d), r = fma(d, rate, kMagic - t);
+    const int n = low(t);
+    const double q =
+        r * fma(r, fma(r, fma(r, fma(r, c * c * c * c * c / 120, c * c * c * c / 24), c * c * c / 6),
+                       c * c / 2),
+                c);
     const u64 bits = (u64)__double_as_longlong(power[n & (kTable - 1)]) +
-                     ((u64)(uint32_t)((n & ~(kTable - 1)) << 10) << 32);
+                     ((u64)(uint32_t)((n & ~(kTable - 1)) << 15) << 32);
     const double w = __longlong_as_double((long long)bits);
     return (u64)__double_as_longlong(fma(w, q, w) + 0x1p52);
   }
   __device__ __forceinline__ u64 operator()(float x) const { return raw(x) - kNone; }
   __device__ __forceinline__ u64 operator()(u64 place) const {
     return (*this)(logit_of((uint32_t)(place >> 32)));
-  }
-};
-
-// The weights of a row's bf16 logits from 2^-12 to 2^7 in magnitude, by their bits: looked up for
-// a quarter of the instructions that computing them takes. The few logits outside are computed.
-struct Weights16 {
-  static constexpr int kFrom = (127 - 12) << 7, kEach = 19 << 7, kValues = 2 * kEach;
-  static constexpr int64_t kWorth = 16384;  // ids of a row that pay for the table
-  const u64 *table;
-  __device__ __forceinline__ static void fill(u64 *table, const Weigh &weigh, int thread, int threads) {
-#pragma unroll 1
-    for (int i = thread; i < kValues; i += threads) {
-      const uint32_t h = i < kEach ? kFrom + i : 0x8000 + kFrom + i - kEach;
-      table[i] = weigh(__uint_as_float(h << 16));
-    }
-  }
-  __device__ __forceinline__ static bool has(uint32_t h) {  // bf16 bits
-    return (h & 0x7FFFu) - kFrom < (uint32_t)kEach;
-  }
-  // 0 for one that the table has not
-  __device__ __forceinline__ u64 operator()(uint32_t h) const {
-    const uint32_t i = (h & 0x7FFFu) - kFrom;
-    const u64 w = table[i < (uint32_t)kEach ? i + (h >> 15) * kEach : 0];
-    return i < (uint32_t)kEach ? w : 0;
   }
 };
 
@@ -197,49 +185,16 @@ __device__ __forceinline__ void over(const SampleArgs &p, int64_t off, int64_t f
 }
 
 // Sum of the weights of ids [from, to) that this thread sees: of those at or above `floor`.
-template <bool B16, class W>
+template <bool B16>
 __device__ __forceinline__ u64 thread_mass(const SampleArgs &p, int64_t off, int64_t from, int64_t to,
-                                           int thread, int threads, const Weigh &weigh,
-                                           const W &weigh16, u64 floor) {
-  u64 sum = 0;
-  if constexpr (B16) {
-    if (p.vocab >= Weights16::kWorth) {
-      auto one = [&](float x, int64_t) {
-        const u64 w = weigh(x);
-        sum += w >= floor ? w : 0;
-      };
-      over_runs<true, 4>(
-          p, off, from, to, thread, threads,
-          [&](const Vec8<true> &v, int64_t id) {
-            bool all = true;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t h[2] = {v.r[e] & 0xFFFFu, v.r[e] >> 16};
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const u64 w = weigh16(h[i]);
-                sum += w >= floor ? w : 0;
-                all &= Weights16::has(h[i]);
-              }
-            }
-            if (!all)  // rare
-#pragma unroll 1
-              for (int e = 0; e < 8; ++e) {
-                const uint16_t h = static_cast<const uint16_t *>(p.logits)[off + id + e];
-                if (!Weights16::has(h)) one(bf16_lo(h), id + e);
-              }
-          },
-          one);
-      return sum;
-    }
-  }
+                                           int thread, int threads, const Weigh &weigh, u64 floor) {
+  u64 sum = 0, n = 0;
   if (floor == 0) {
-    u64 raw = 0, n = 0;
-    over<B16, 2>(p, off, from, to, thread, threads, [&](float x, int64_t) {
-      raw += weigh.raw(x);
+    over<B16, 4>(p, off, from, to, thread, threads, [&](float x, int64_t) {
+      sum += weigh.raw(x);
       ++n;
     });
-    return raw - n * Weigh::kNone;
+    return sum - n * Weigh::kNone;
   }
   over<B16, 1>(p, off, from, to, thread, threads, [&](float x, int64_t) {
     const u64 w = weigh(x);
@@ -310,6 +265,16 @@ __device__ __forceinline__ u64 most_of(u64 a, u64 b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t wave_top(uint32_t k) { return (uint32_t)wave_all(k, most_of); }
 __device__ __forceinline__ u64 wave_sum(u64 v) { return wave_all(v, add); }
 // Sums of the lanes up to each.
+__device__ __forceinline__ uint32_t wave_run(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);
+  auto of = [&](int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); };
+  const uint32_t a = of(15), b = a + of(31), c = b + of(47);
+  const int row = threadIdx.x % 64 / 16;
+  return v + (row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c);
+}
 __device__ __forceinline__ u64 wave_run(u64 v) {
   v += dpp<0x111>(v);  // from 1, 2, 4, 8 lanes below
   v += dpp<0x112>(v);
@@ -399,7 +364,6 @@ template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_plain_kernel(const SampleArgs p) {
   constexpr int kWaves = kThreads / 64;
   __shared__ double power[kTable];
-  __shared__ u64 weights[B16 ? Weights16::kValues : 1];
   __shared__ u64 sums[kWaves], found;
   __shared__ uint32_t tops[kWaves];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
@@ -424,12 +388,7 @@ __global__ __launch_bounds__(kThreads) void sample_plain_kernel(const SampleArgs
   const float top = logit_of(top_key);
   const Weigh weigh(power, top, r.T);
   const u64 floor = r.floor(p.shift);
-  if (B16 && V >= Weights16::kWorth) {
-    Weights16::fill(weights, weigh, tid, kThreads);
-    __syncthreads();
-  }
-  const u64 sum = wave_sum(
-      thread_mass<B16>(p, off, begin, end, lane, 64, weigh, Weights16{weights}, floor));
+  const u64 sum = wave_sum(thread_mass<B16>(p, off, begin, end, lane, 64, weigh, floor));
   if (lane == 0) sums[wave] = sum;
   __syncthreads();
   u64 all = 0;
@@ -558,7 +517,6 @@ __global__ __launch_bounds__(kSliceThreads) void sample_slice_kernel(const Sampl
 
 struct Shared {
   double power[kTable];
-  u64 weights[Weights16::kValues];
   u64 mass[kBins];
   uint32_t count[kBins];
   u64 list[kList];
@@ -696,31 +654,35 @@ __device__ __forceinline__ u64 share(double top_p, u64 all) {  // where top_p cu
   return t > 0 ? t : 1;
 }
 
-constexpr int64_t kLeft = -2;  // in place of an id: the row is left to sample_left_kernel
+// What sample_cut_kernel leaves of a row to sample_left_kernel, in two words of the workspace:
+// nothing, the draw behind a cut (its place, above 0, and the largest key), or all of it.
+constexpr u64 kNothingLeft = ~0ull, kAllLeft = 0;
 
 // Rows whose cuts keep more than LDS holds, or whose candidates did not fit there: bins of the
 // logits and then of places narrow every cut down in the row itself. A kernel of its own, as its
-// registers would make the common path's spill (256 x 65536 bf16 top_p 151 us so).
+// registers would make the common path's spill.
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs p) {
   constexpr int kWaves = kThreads / 64;
   __shared__ Shared s;
   const int tid = threadIdx.x;
   const int64_t row = p.first + blockIdx.x, off = row * p.stride, V = p.vocab;
-  if ((p.id64 ? static_cast<const int64_t *>(p.ids)[row]
-              : (int64_t)static_cast<const int32_t *>(p.ids)[row]) != kLeft)
-    return;
+  const u64 state = static_cast<const u64 *>(p.workspace)[2 * row];
+  if (state == kNothingLeft) return;
   Weigh::fill(s.power, p.shift, tid, kThreads);
-  const uint32_t mine = thread_top<B16>(p, off, 0, V, tid, kThreads);
-  const uint32_t top_key = (uint32_t)block_range(s, {0, 0, mine, mine}).hi;
+  uint32_t top_key = (uint32_t) static_cast<const u64 *>(p.workspace)[2 * row + 1];
+  if (state == kAllLeft) {
+    const uint32_t mine = thread_top<B16>(p, off, 0, V, tid, kThreads);
+    top_key = (uint32_t)block_range(s, {0, 0, mine, mine}).hi;
+  }
   const Request r(p, row);
   const float top = logit_of(top_key);
   const Weigh weigh(s.power, top, r.T);
   const float bins = (float)fmin((double)kBinsPerNat / r.T, 0x1p100);
   auto bin_of = [&](float x) { return (int)fminf((top - x) * bins, (float)(kBins - 1)); };
   const u64 floor = r.floor(p.shift);
-  u64 cut = 0;  // the least place that is kept
-  for (int by_mass = 0; by_mass < 2; ++by_mass) {
+  u64 cut = state;  // the least place that is kept
+  for (int by_mass = 0; by_mass < 2 && state == kAllLeft; ++by_mass) {
     if (by_mass ? !(r.top_p < 1.0) : !(r.k > 0 && r.k < V)) continue;
     auto value = [&](u64 c) { return by_mass ? weigh(c) : 1ull; };
     clear_bins(s);
@@ -765,13 +727,18 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs 
                   },
                   [](u64 c) { return c; }, value);
   }
+  const float last = cut ? logit_of((uint32_t)(cut >> 32)) : -__builtin_inff();
+  const int64_t last_id = cut ? (int64_t)(uint32_t)~(uint32_t)cut : V;
   auto value = [&](float x, int64_t i) {
-    const u64 w = place_of(x, i) >= cut ? weigh(x) : 0;
+    const u64 w = x > last || (x == last && i <= last_id) ? weigh(x) : 0;
     return w >= floor ? w : 0;
   };
   const int wave = tid / 64;
   const int64_t each = ((V + kWaves - 1) / kWaves + 511) / 512 * 512, begin = wave * each;
-  const u64 sum = wave_mass<B16>(p, off, begin, begin + each < V ? begin + each : V, value);
+  u64 sum = 0;
+  over<B16, 4>(p, off, begin, begin + each < V ? begin + each : V, tid % 64, 64,
+               [&](float x, int64_t i) { sum += value(x, i); });
+  sum = wave_sum(sum);
   __syncthreads();
   if (tid % 64 == 0) s.wave2[wave] = sum;
   __syncthreads();
@@ -786,20 +753,25 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs 
   if (tid == 0) answer(p, row, place, top, r.T, all);
 }
 
-// A row a workgroup at a time. What the cuts can keep is gathered into LDS first:
+// A row by a workgroup. What the cuts can keep is gathered into LDS first:
 //   top-k : the k-th largest of the threads' maxima has k logits at or above it;
-//   top-p : the logits from the median of the threads' maxima on, if they hold top_p of the sum;
-// then each cut and the draw itself is a search among these, by the same steps.
+//   top-p alone : the weights are added up in bins of a 32nd of an octave, so that the run's
+//           end is known to a bin, and the logits down to there are gathered;
+// then each cut and the draw itself is a search among these, by the same steps. A run too long
+// for LDS is cut among its last bin's logits and drawn from by sample_left_kernel.
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p) {
   __shared__ Shared s;
   const int tid = threadIdx.x;
-  const int64_t V = p.vocab;
+  const int64_t row = p.first + blockIdx.x, off = row * p.stride, V = p.vocab;
+  u64 *const left = static_cast<u64 *>(p.workspace);
+  const bool small = V <= kList;  // the list takes the row
   Weigh::fill(s.power, p.shift, tid, kThreads);
-  const int64_t row = p.first + blockIdx.x, off = row * p.stride;
-  const uint32_t mine = thread_top<B16>(p, off, 0, V, tid, kThreads);
-  const uint32_t top_key = (uint32_t)block_range(s, {0, 0, mine, mine}).hi;
+  if (tid == 0 && !small) left[2 * row] = kNothingLeft;
   const Request r(p, row);
+  const uint32_t mine = thread_top<B16>(p, off, 0, V, tid, kThreads);
+  const Range tops = block_range(s, {0, 0, mine, mine});
+  const uint32_t top_key = (uint32_t)tops.hi;
   if (!r.drawn(top_key)) {
     if (tid == 0) answer(p, row, -1, 0.0);
     return;
@@ -813,44 +785,136 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
   const Weigh weigh(s.power, top, r.T);
   const u64 floor = r.floor(p.shift);
   const bool by_count = r.k > 0 && r.k < V, by_mass = r.top_p < 1.0;
+  if (!small && (by_count ? r.k > kThreads : !by_mass)) {
+    if (tid == 0) left[2 * row] = kAllLeft;
+    return;
+  }
   u64 cut = 0;     // the least place that is kept
-  u64 goal = 0;    // where top_p cuts the row's sum off, if the list is cut by it alone
+  u64 goal = 0;    // where top_p cuts the sum off, if that is known
   uint32_t n = 0;  // places in the list
-  bool hard = false;
-  enum { kTops, kCount, kMass, kDraw };
-  // no cut after all (parameters of this row), or too long a one
-  if (V > kList && (by_count ? r.k > kThreads : !by_mass)) hard = true;
-  for (int stage = V <= kList ? kCount : kTops; stage <= kDraw && !hard; ++stage) {
-    if (stage == kTops) {
-      s.list[tid] = (u64)mine << 32 | (uint32_t)~tid;
-      n = kThreads;
-      __syncthreads();
-    } else if (n == 0) {
-      // the candidates: all of a short row, else from the last stage's find on
-      const float least = V <= kList ? -__builtin_inff() : logit_of((uint32_t)(cut >> 32));
-      cut = 0;
-      if (tid == 0) s.n = 0;
-      if (B16 && by_mass && !by_count && V >= Weights16::kWorth)
-        Weights16::fill(s.weights, weigh, tid, kThreads);
-      __syncthreads();
-      auto append = [&](float x, int64_t i) {
-        if (x >= least) {
-          const uint32_t to = atomicAdd(&s.n, 1u);
-          if (to < kList) s.list[to] = place_of(x, i);
+  bool whole = true;  // the list holds all that is kept
+  // Logits from `lowest` to `highest` into the list, of them those of bin `only` where that is one;
+  // a wave takes room for its eight times 64 at once.
+  auto gather = [&](float lowest, float highest, int only) {
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    auto append = [&](uint32_t mine, auto get, int64_t id) {  // bit e: get(e) may go in
+      if (__ballot(mine != 0) == 0) return;
+      if (only >= 0)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (weigh.steps(get(e)) != only) mine &= ~(1u << e);
+      const uint32_t run = wave_run((uint32_t)__popc(mine));
+      uint32_t room = 0;
+      if (tid % 64 == 63 && run > 0) room = atomicAdd(&s.n, run);
+      uint32_t to = (uint32_t)__builtin_amdgcn_readlane((int)room, 63) + run - __popc(mine);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (mine >> e & 1) {
+          if (to < kList) s.list[to] = place_of(get(e), id + e);
+          ++to;
         }
-      };
-      over<B16, 4>(p, off, 0, V, tid, kThreads, append);
-      if (by_mass && !by_count) {
-        Range w = kNothing;
-        w.sum = thread_mass<B16>(p, off, 0, V, tid, kThreads, weigh, Weights16{s.weights}, 0);
-        goal = share(r.top_p, block_range(s, w).sum);
+    };
+    constexpr int kAhead = 4;
+    const int64_t whole_runs = V / 8 * 8;
+    const int runs = (int)(V / 8);
+#pragma unroll 1
+    for (int i0 = 0; i0 < runs; i0 += kAhead * kThreads) {  // all lanes stay: append speaks to them
+      Vec8<B16> v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kThreads + tid;
+        v[u].load(p.logits, off + 8 * (int64_t)(i < runs ? i : runs - 1));
       }
-      __syncthreads();
-      n = s.n;
-      __syncthreads();
-      if (n > kList) hard = true;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kThreads + tid;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          mine |= v[u].get(e) >= lowest && v[u].get(e) <= highest ? 1u << e : 0u;
+        append(i < runs ? mine : 0, [&](int e) { return v[u].get(e); }, 8 * (int64_t)i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    if (hard || (stage == kCount && !by_count) || (stage == kMass && !by_mass)) continue;
+    if (tid < V - whole_runs) {  // the last few, one each
+      const int64_t id = whole_runs + tid;
+      const float x = B16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[off + id])
+                          : static_cast<const float *>(p.logits)[off + id];
+      if (x >= lowest && x <= highest && (only < 0 || weigh.steps(x) == only)) {
+        const uint32_t to = atomicAdd(&s.n, 1u);
+        if (to < kList) s.list[to] = place_of(x, id);
+      }
+    }
+    __syncthreads();
+    n = s.n;
+    __syncthreads();
+  };
+  const float infinite = __builtin_inff();
+  enum { kTops, kCount, kMass, kDraw };
+  int stage = kCount;
+  // what the next search goes over, where that is known without a look at the list
+  Range known = kNothing;
+  auto between = [&](uint32_t lo, uint32_t hi) {
+    known = {0, n, (u64)lo << 32, (u64)hi << 32 | 0xFFFFFFFFu};
+  };
+  if (small) {
+    gather(-infinite, infinite, -1);
+  } else if (by_count) {
+    stage = kTops;
+    s.list[tid] = (u64)mine << 32 | (uint32_t)~tid;
+    n = kThreads;
+    between((uint32_t)tops.lo, top_key);
+    __syncthreads();
+  } else {
+    // The run ends above a weight of (1 - top_p) / vocab: from such a one on all weigh less than
+    // 1 - top_p together, and the sum is at least 1. Smaller ones need no bin.
+    const double part = r.top_p > 0.0 ? 1.0 - r.top_p : 1.0;
+    const u64 tail = part_of(part / (double)V * (1.0 - 0x1p-50), 1ull << p.shift, false);
+    clear_bins(s);
+    Range w = kNothing;
+    over<B16, 4>(p, off, 0, V, tid, kThreads, [&](float x, int64_t) {
+      const double d = weigh.below(x);
+      const u64 wx = weigh.raw_at(d) - Weigh::kNone;
+      w.sum += wx;
+      if (wx > tail) atomicAdd(&s.mass[-Weigh::low(weigh.whole(d))], wx);
+    });
+    goal = share(r.top_p, block_range(s, w).sum);
+    find_bin(s, goal, [&](int b) { return s.mass[b]; });
+    const int bin = (int)s.bin;
+    const u64 before = s.before;
+    __syncthreads();
+    // how many logits that is, at most: none of a bin lies a whole step below it
+    w = kNothing;
+    for (int b = tid; b <= bin; b += kThreads) {
+      // 2^(shift - (b + 1) / kTable)
+      const double next = ldexp(s.power[-(b + 1) & (kTable - 1)], -(b + kTable) / kTable);
+      w.sum += (u64)fmin((double)s.mass[b] / fmax(next - 1.0, 1.0) + 1.0, 0x1p40);
+    }
+    whole = block_range(s, w).sum <= kList;
+    if (!whole) goal -= before;
+    // from a little below the bin, which is behind the cut anyway; else a little more than the bin
+    auto edge = [&](double steps, double slack) {
+      const double x = (double)top - steps / weigh.rate;
+      return (float)(x + slack * fabs(x));
+    };
+    const float lowest = edge(bin + 0.75, -0x1p-20), highest = edge(bin - 0.75, 0x1p-20);
+    gather(lowest, whole ? infinite : highest, whole ? -1 : bin);
+    between(key_of(lowest), whole ? top_key : key_of(highest));
+    if (n > kList) {
+      if (tid == 0) left[2 * row] = kAllLeft;
+      return;
+    }
+  }
+  for (; stage <= kDraw; ++stage) {
+    if ((stage == kCount && !by_count) || (stage == kMass && !by_mass)) continue;
+    if (stage == kDraw && !whole) {
+      if (tid == 0) {
+        left[2 * row] = cut;
+        left[2 * row + 1] = top_key;
+      }
+      return;
+    }
     const u64 least = stage == kDraw ? floor : 0;
     auto value = [&](u64 c) {
       if (stage < kMass) return 1ull;
@@ -864,25 +928,29 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
         if (c >= cut && (stage != kDraw || value(c) > 0)) f(c);
       }
     };
-    Range w = kNothing;
-    walk([&](u64 c) { join(w, value(c), 1, order(c), order(c)); });
-    w = block_range(s, w);
-    u64 target = stage == kTops ? (by_count ? (u64)r.k : kThreads / 2) : (u64)r.k;
+    Range w = known;
+    known = kNothing;
+    if (w.count == 0) {
+      walk([&](u64 c) { join(w, value(c), 1, order(c), order(c)); });
+      w = block_range(s, w);
+    }
+    u64 target = (u64)r.k;
     if (stage == kMass) target = goal ? goal : share(r.top_p, w.sum);
     if (stage == kDraw) target = r.point(w.sum) + 1;
-    if (target > w.sum) {  // the list does not hold the run to its end
-      hard = true;
-      continue;
-    }
     const u64 found = resolve(s, w.lo, w.hi, w.count, target, walk, order, value);
     if (stage == kDraw) {
       if (tid == 0) answer(p, row, found, top, r.T, w.sum);
+    } else if (stage == kTops) {
+      gather(logit_of((uint32_t)(found >> 32)), infinite, -1);
+      between((uint32_t)(found >> 32), top_key);
+      if (n > kList) {
+        if (tid == 0) left[2 * row] = kAllLeft;
+        return;
+      }
     } else {
       cut = found;
-      if (stage == kTops) n = 0;
     }
   }
-  if (hard && tid == 0) answer(p, row, kLeft, 0.0);
 }
 
 bool cuts(const SampleArgs &a) { return a.top_ks || a.top_k > 0 || a.top_ps || a.top_p < 1.0; }
@@ -903,7 +971,10 @@ Slices slices_of(const SampleArgs &a) {
 
 int64_t sample_workspace_bytes(const SampleArgs &a) {
   const Slices s = slices_of(a);
-  return s.count > 1 ? (a.rows * s.count * 12 + 255) / 256 * 256 : 0;
+  const int64_t slices = s.count > 1 ? a.rows * s.count * 12 : 0;
+  // what is left of each row; a row's own parameters, which the sizes do not show, may cut too
+  const int64_t left = a.vocab > kList ? a.rows * 16 : 0;
+  return (std::max(slices, left) + 255) / 256 * 256;
 }
 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {

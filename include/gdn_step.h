@@ -127,8 +127,9 @@ typedef struct gdn_sample_shape {
   double temperature, top_p, min_p;
 } gdn_sample_shape_t;
 
-/* Bytes of device workspace that gdn_sample_tokens needs, into *bytes (host): 0 but for few
- * rows of a long vocabulary, which are split over several workgroups. Host only. */
+/* Bytes of device workspace that gdn_sample_tokens needs, into *bytes (host): 0 for a vocabulary
+ * of up to 4096, else a few for each row, and more for few rows of a long vocabulary, which are
+ * split over several workgroups. Host only. */
 gdn_status_t gdn_sample_tokens_workspace(const gdn_sample_shape_t *shape, size_t *bytes);
 
 /* Draws one token of each row. With M the row's largest logit, token i weighs
