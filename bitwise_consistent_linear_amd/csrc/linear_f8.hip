@@ -240,108 +240,183 @@ __device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Few rows: W's bytes are what counts, each read once by a group of 32 MT rows, straight into
-// the operand registers. A wave takes 16 columns of Y and all of k, four blocks of 128 at a
-// time with the next four on their way; lanes of the instruction's other 16 columns hold zeros.
-template <int MT, bool E5M2, bool YB>
-__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void linear_f8_rows_kernel(const LinearF8Args p) {
-  const int l = threadIdx.x, r = l % 32, half = l / 32;
-  const int64_t tiles_n = (p.n + 15) / 16;
-  const int64_t n0 = blockIdx.x % tiles_n * 16, m0 = blockIdx.x / tiles_n * (32 * MT);
-  const int64_t n4 = (p.n + 3) / 4 * 4, m4 = (p.m + 3) / 4 * 4;
-  const bool holds = r < 16;
-  const int64_t wrow = n0 + r % 16 < p.n ? n0 + r % 16 : p.n - 1;
-  const uint8_t *w = p.wq + wrow * p.k + 32 * half;
-  const uint32_t *ws = reinterpret_cast<const uint32_t *>(p.w_scale) + wrow;
-  const uint8_t *x[MT];
-  const uint32_t *xs[MT];
+// The results of 64 k by one wave: 32 columns of W (first operand) by 32 rows of X.
+template <bool E5M2, bool YB, int Sel>
+__device__ __forceinline__ f32x16 products(const i32x4 (&w)[2], const i32x4 (&x)[2], f32x16 acc,
+                                           int ws, int xs) {
+  if constexpr (YB) {
+    return mfma<E5M2, Sel>(join(w[0], w[1]), join(x[0], x[1]), acc, ws, xs);
+  } else {
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t row = m0 + 32 * i + r < p.m ? m0 + 32 * i + r : p.m - 1;
-    x[i] = p.xq + row * p.k + 32 * half;
-    xs[i] = reinterpret_cast<const uint32_t *>(p.x_scale) + row;
+    for (int q = 0; q < 4; ++q)
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          widen<false>(w[q / 2][q % 2 * 2], w[q / 2][q % 2 * 2 + 1], scale_as_float<Sel>(ws)),
+          widen<E5M2>(x[q / 2][q % 2 * 2], x[q / 2][q % 2 * 2 + 1], scale_as_float<Sel>(xs)), acc, 0,
+          0, 0);
+    return acc;
   }
-  f32x16 acc[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = f32x16{};
-  struct Turn {
-    i32x4 w[8][2], x[MT][8][2];
-    uint32_t ws, xs[MT];
+}
+
+// A word per lane from an address per lane to LDS, lane after lane from `to` (uniform) on.
+__device__ __forceinline__ void load_words_to_lds(const void *from, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, off"
+      :: "s"(to), "v"(from) : "memory", "m0");
+}
+
+// Few rows: W's bytes are what counts. A workgroup takes 16 columns of Y, up to MR rows, and all
+// of k in one chain by one wave for each 32 rows, as every kernel here; what it can spread is the
+// loading, so four waves keep LDS full of the chunks of 512 k that follow (112 KB of them for 16
+// rows: 16 x 4096 x 4096 NNN us against 14.2 by one wave that loads into registers).
+//
+// A row's 32 chunks of 16 bytes lie at c ^ (row % 16): the 16 lanes of an operand read that are
+// served together have rows of 16 different remainders, so they meet no bank twice.
+template <int MR, bool E5M2, bool YB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void linear_f8_rows_kernel(const LinearF8Args p) {
+  constexpr int R = 16 + MR, kBufs = MR == 16 ? 8 : MR == 32 ? 6 : 3, kAhead = kBufs - 1;
+  constexpr int kLoads = R / 8, kWords = (R + 63) / 64;  // of a wave for a chunk: 1 KiB, and words
+  static_assert((kAhead - 1) * (kLoads + kWords) < 64, "the loads that a wait counts");
+  __shared__ __align__(128) uint8_t lds[kBufs][R * 512];
+  __shared__ __align__(128) uint32_t scales[kBufs][kWords * 64];
+  const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t tiles_n = (p.n + 15) / 16;
+  const int64_t n0 = blockIdx.x % tiles_n * 16, m0 = blockIdx.x / tiles_n * MR;
+  const int64_t n4 = (p.n + 3) / 4 * 4, m4 = (p.m + 3) / 4 * 4;
+  const int last_w = (int)(p.n - n0 < 16 ? p.n - n0 : 16) - 1;
+  const int last_x = (int)(p.m - m0 < MR ? p.m - m0 : MR) - 1;
+  const uint8_t *const wbase = p.wq + n0 * p.k, *const xbase = p.xq + m0 * p.k;
+  const int chunks = (p.k + 511) / 512;
+  auto place = [](const void *s) {
+    return __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)s);
   };
-  const i32x4 zero = {0, 0, 0, 0};
-  auto at = [](const uint8_t *b, int k) { return *reinterpret_cast<const i32x4 *>(b + k); };
-  auto load = [&](Turn &t, int k0) {  // what lies past the end is zeros
-    const bool any = k0 < p.k;
-    t.ws = any ? ws[k0 / 512 * n4] : 0x7F7F7F7Fu;
+  const uint32_t lds_at = place(lds), scales_at = place(scales);
+  // loads: two rows each, W's first; rows past the end repeat the last one
+  uint32_t off[kLoads], at[kLoads];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) t.xs[i] = any ? xs[i][k0 / 512 * m4] : 0x7F7F7F7Fu;
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = (wave * kLoads + i) * 2 + l / 32;
+    const int row = r < 16 ? (r < last_w ? r : last_w) : (r - 16 < last_x ? r - 16 : last_x);
+    off[i] = (uint32_t)row * p.k;
+    at[i] = 16 * (l % 32 ^ r % 16);
+  }
+  const uint8_t *words[kWords];
+  int64_t words_step[kWords];
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const int k = k0 + 64 * s;
-      const bool in = k < p.k;
+  for (int i = 0; i < kWords; ++i) {
+    const int r = 64 * i + l;
+    const bool w = r < 16;
+    const int row = w ? (r < last_w ? r : last_w) : (r - 16 < last_x ? r - 16 : last_x);
+    words[i] = (w ? p.w_scale + n0 * 4 : p.x_scale + m0 * 4) + 4 * row;
+    words_step[i] = 4 * (w ? n4 : m4);
+  }
+  auto fetch = [&](int c) {  // past the last chunk that one again, unread
+    const int buf = c % kBufs;
+    if (c >= chunks) c = chunks - 1;
+    const int k0 = c * 512;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t k = k0 + at[i] < (uint32_t)p.k ? k0 + at[i] : 0;  // a chunk's end is not read
+      load_to_lds((wave * kLoads + i) * 2 < 16 ? wbase : xbase, off[i] + k,
+                  lds_at + buf * R * 512 + (wave * kLoads + i) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)  // by every wave, the same words
+      load_words_to_lds(words[i] + c * words_step[i], scales_at + (buf * kWords + i) * 256);
+  };
+
+  // a wave that multiplies reads a chunk's operands under the products of the chunk before
+  const int r = l % 32, half = l / 32, xrow = MR == 16 ? r % 16 : wave * 32 + r;
+  const bool multiplies = wave < (MR + 31) / 32;
+  struct Operands {
+    i32x4 w[8][2], x[8][2];
+    int ws, xs;
+  };
+  auto read = [&](Operands &o, int c) {
+    const int buf = c % kBufs;
+    const uint8_t *w = lds[buf] + r % 16 * 512, *x = lds[buf] + (16 + xrow) * 512;
+    o.ws = (int)scales[buf][r % 16];
+    o.xs = (int)scales[buf][16 + xrow];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        t.w[s][h] = in && holds ? at(w, k + 16 * h) : zero;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) t.x[i][s][h] = in ? at(x[i], k + 16 * h) : zero;
+        const int chunk = 4 * s + 2 * half + h;
+        o.w[s][h] = *reinterpret_cast<const i32x4 *>(w + 16 * (chunk ^ r % 16));
+        o.x[s][h] = *reinterpret_cast<const i32x4 *>(x + 16 * (chunk ^ xrow % 16));
       }
-    }
   };
-  auto two = [&](const Turn &t, auto sel) {
+  f32x16 acc = {};
+  auto two = [&](const Operands &o, auto sel) {
     constexpr int S = decltype(sel)::value;
+    acc = products<E5M2, YB, S>(o.w[2 * S], o.x[2 * S], acc, o.ws, o.xs);
+    acc = products<E5M2, YB, S>(o.w[2 * S + 1], o.x[2 * S + 1], acc, o.ws, o.xs);
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  using S2 = std::integral_constant<int, 2>;
+  using S3 = std::integral_constant<int, 3>;
+  auto arrive_and_fetch = [&](int c) {
+    arrive<(kAhead - 1) * (kLoads + kWords)>();
+    fetch(c + kAhead);  // into the buffer of the chunk before, which every wave is past
+  };
+  auto turn = [&](int c, Operands &now, const Operands &before) {
+    arrive_and_fetch(c);
+    if (!multiplies) return;
+    read(now, c);
+    two(before, S0{});
+    two(before, S1{});
+    two(before, S2{});
+    two(before, S3{});
 #pragma unroll
-    for (int s = 2 * S; s < 2 * S + 2; ++s)
-      if constexpr (YB) {
+    for (int q = 0; q < 8; ++q) {  // four operand reads between the products of 64 k
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, YB ? 1 : 4, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto last = [&](const Operands &o) {
+    const int left = p.k - (chunks - 1) * 512;
+    two(o, S0{});
+    if (left > 128) two(o, S1{});
+    if (left > 256) two(o, S2{});
+    if (left > 384) two(o, S3{});
+  };
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          acc[i] = mfma<E5M2, S>(join(t.w[s][0], t.w[s][1]), join(t.x[i][s][0], t.x[i][s][1]),
-                                 acc[i], (int)t.ws, (int)t.xs[i]);
-      } else {
+  for (int c = 0; c < kAhead; ++c) fetch(c);
+  Operands o0, o1;
+  arrive_and_fetch(0);
+  if (multiplies) read(o0, 0);
+  int c = 1;
+  for (; c + 1 < chunks; c += 2) {
+    turn(c, o1, o0);
+    turn(c + 1, o0, o1);
+  }
+  if (c < chunks) turn(c, o1, o0);
+  if (multiplies) {
+    if (chunks % 2)
+      last(o0);
+    else
+      last(o1);
+  }
+  arrive<0>();  // no load may land in LDS that is another workgroup's by then
+  const int64_t m = m0 + (MR == 16 ? r : wave * 32 + r);
+  if (wave < (MR + 31) / 32 && m < p.m && (MR > 16 || r < 16))
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bf16x8 w = widen<false>(t.w[s][q / 2][q % 2 * 2], t.w[s][q / 2][q % 2 * 2 + 1],
-                                        scale_as_float<S>((int)t.ws));
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                w, widen<E5M2>(t.x[i][s][q / 2][q % 2 * 2], t.x[i][s][q / 2][q % 2 * 2 + 1],
-                               scale_as_float<S>((int)t.xs[i])),
-                acc[i], 0, 0, 0);
+      for (int e = 0; e < 4; ++e) {
+        const int64_t n = n0 + 8 * g + 4 * half + e;
+        if (n < p.n) {
+          if (YB)
+            static_cast<uint16_t *>(p.y)[m * p.n + n] = to_bf16(acc[4 * g + e]);
+          else
+            static_cast<float *>(p.y)[m * p.n + n] = acc[4 * g + e];
         }
       }
-  };
-  auto multiply = [&](const Turn &t) {
-    two(t, std::integral_constant<int, 0>{});
-    two(t, std::integral_constant<int, 1>{});
-    two(t, std::integral_constant<int, 2>{});
-    two(t, std::integral_constant<int, 3>{});
-  };
-  Turn t0, t1;
-  load(t0, 0);
-  for (int k = 0; k < p.k; k += 1024) {
-    load(t1, k + 512);
-    multiply(t0);
-    load(t0, k + 1024);
-    multiply(t1);
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + 32 * i + r;
-    if (m < p.m)
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t n = n0 + 8 * g + 4 * half + e;
-          if (n < p.n) {
-            if (YB)
-              static_cast<uint16_t *>(p.y)[m * p.n + n] = to_bf16(acc[i][4 * g + e]);
-            else
-              static_cast<float *>(p.y)[m * p.n + n] = acc[i][4 * g + e];
-          }
-        }
-  }
 }
 
 __device__ __forceinline__ void load_word_to_lds(const void *base, uint32_t offset, uint32_t to) {
@@ -588,11 +663,11 @@ struct Launch {
   int64_t grid;
 };
 
-template <int MT, bool E>
+template <int MR, bool E>
 Launch rows_launch(const LinearF8Args &a) {
-  return {a.y_bf16 ? (const void *)linear_f8_rows_kernel<MT, E, true>
-                   : (const void *)linear_f8_rows_kernel<MT, E, false>,
-          64, (a.m + 32 * MT - 1) / (32 * MT) * ((a.n + 15) / 16)};
+  return {a.y_bf16 ? (const void *)linear_f8_rows_kernel<MR, E, true>
+                   : (const void *)linear_f8_rows_kernel<MR, E, false>,
+          256, (a.m + MR - 1) / MR * ((a.n + 15) / 16)};
 }
 
 template <int BM, int BN, int TM, int TN, bool E>
@@ -611,8 +686,9 @@ Launch pick(const LinearF8Args &a) {
   auto count = [&](int rows, int cols) {
     return (a.m + rows - 1) / rows * ((a.n + cols - 1) / cols);
   };
-  if (count(32, 16) <= 256) return rows_launch<1, E>(a);
-  if (count(64, 16) <= 256) return rows_launch<2, E>(a);
+  if (a.m <= 16 && count(16, 16) <= 256) return rows_launch<16, E>(a);
+  if (count(32, 16) <= 256) return rows_launch<32, E>(a);
+  if (count(64, 16) <= 256) return rows_launch<64, E>(a);
   auto time = [&](int rows, int cols, double round) {
     return (double)((count(rows, cols) + 255) / 256) * round;
   };
