@@ -16,10 +16,25 @@ using f32x2 = float __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------------- values of a tensor
 
-// Four consecutive values at i of n; those past n are 0 and not read.
+// Four consecutive values at i of n; those past n are 0 and not read. Once: past the caches, for
+// what is not looked at again before the next step (60 million values with binary32 states take
+// 280 us so, 6.0 TB/s, and 326 through them).
+template <bool Once, class T>
+__device__ __forceinline__ T fetched(const void *from) {
+  return Once ? __builtin_nontemporal_load(static_cast<const T *>(from)) : *static_cast<const T *>(from);
+}
+template <bool Once, class T>
+__device__ __forceinline__ void put(void *to, T v) {
+  if (Once)
+    __builtin_nontemporal_store(v, static_cast<T *>(to));
+  else
+    *static_cast<T *>(to) = v;
+}
+
+template <bool Once = true>
 __device__ __forceinline__ void load4(const float *b, int64_t i, int64_t n, float (&v)[4]) {
   if (i + 4 <= n) {
-    const f32x4_a4 r = *reinterpret_cast<const f32x4_a4 *>(b + i);
+    const f32x4_a4 r = fetched<Once, f32x4_a4>(b + i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = r[e];
   } else {
@@ -27,9 +42,10 @@ __device__ __forceinline__ void load4(const float *b, int64_t i, int64_t n, floa
     for (int e = 0; e < 4; ++e) v[e] = i + e < n ? b[i + e] : 0.0f;
   }
 }
+template <bool Once = true>
 __device__ __forceinline__ void load4(const uint16_t *b, int64_t i, int64_t n, float (&v)[4]) {
   if (i + 4 <= n) {
-    const u32x2_a2 r = *reinterpret_cast<const u32x2_a2 *>(b + i);
+    const u32x2_a2 r = fetched<Once, u32x2_a2>(b + i);
     v[0] = bf16_lo(r[0]);
     v[1] = bf16_hi(r[0]);
     v[2] = bf16_lo(r[1]);
@@ -40,25 +56,27 @@ __device__ __forceinline__ void load4(const uint16_t *b, int64_t i, int64_t n, f
   }
 }
 __device__ __forceinline__ uint32_t load4(const uint8_t *b, int64_t i, int64_t n) {
-  if (i + 4 <= n) return *reinterpret_cast<const u32_a1 *>(b + i);
+  if (i + 4 <= n) return fetched<true, u32_a1>(b + i);
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) w |= i + e < n ? (uint32_t)b[i + e] << (8 * e) : 0u;
   return w;
 }
 
+template <bool Once>
 __device__ __forceinline__ void store4(float *b, int64_t i, int64_t n, const float (&v)[4]) {
   if (i + 4 <= n) {
-    *reinterpret_cast<f32x4_a4 *>(b + i) = f32x4_a4{v[0], v[1], v[2], v[3]};
+    put<Once>(b + i, f32x4_a4{v[0], v[1], v[2], v[3]});
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (i + e < n) b[i + e] = v[e];
   }
 }
+template <bool Once>
 __device__ __forceinline__ void store4(uint16_t *b, int64_t i, int64_t n, const float (&v)[4]) {
   if (i + 4 <= n) {
-    *reinterpret_cast<u32x2_a2 *>(b + i) = u32x2_a2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    put<Once>(b + i, u32x2_a2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -67,7 +85,7 @@ __device__ __forceinline__ void store4(uint16_t *b, int64_t i, int64_t n, const 
 }
 __device__ __forceinline__ void store4(uint8_t *b, int64_t i, int64_t n, uint32_t w) {
   if (i + 4 <= n) {
-    *reinterpret_cast<u32_a1 *>(b + i) = w;
+    put<true, u32_a1>(b + i, w);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -171,7 +189,10 @@ __host__ __device__ inline Rates rates_of(const AdamwArgs &a, int64_t step, doub
 // Tensors of one launch, in its arguments (4 KiB of them are safe): nothing is copied to the GPU
 // ahead of the kernel, so the host may change its list as soon as the call is back.
 constexpr int kTensors = 52;
-constexpr int kChunk = 2048;  // values a workgroup takes at a time
+// Values a workgroup takes at a time: 4 or 8 a thread. Blocks of 8-bit states are bound by their
+// arithmetic and want two on their way (280 million values 667 us, with one 692), binary32 by
+// memory and by the latency of short tensors (600000 values 5.2 us, with two 6.4).
+constexpr int chunk_of(bool eight) { return eight ? 2048 : 1024; }
 constexpr int kGrid = 1 << 20;
 
 struct AdamwLaunch {
@@ -204,13 +225,16 @@ __device__ __forceinline__ void update(const gdn_adamw_tensor_t &t, int64_t i, c
     rc = load4(static_cast<const uint8_t *>(t.v), i, n);
     ms = t.m_scale[block];
     rs = t.v_scale[block];
+  } else {
+    load4(static_cast<const float *>(t.m), i, n, m);
+    load4(static_cast<const float *>(t.v), i, n, v);
+  }
+  if (!(fabsf(factor) < __builtin_inff())) return;  // looked at with the values on their way
+  if (Eight) {
     decode_m(mc, ms, m);
     decode_r(rc, rs, r);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = r[e] * r[e];
-  } else {
-    load4(static_cast<const float *>(t.m), i, n, m);
-    load4(static_cast<const float *>(t.v), i, n, v);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -220,8 +244,8 @@ __device__ __forceinline__ void update(const gdn_adamw_tensor_t &t, int64_t i, c
     r[e] = sqrtf(v[e]);
     p[e] = p[e] * k.decay - m[e] / (r[e] * k.root + k.eps) * k.rate;
   }
-  store4(static_cast<P *>(t.param), i, n, p);
-  if (PB && t.master) store4(t.master, i, n, p);
+  store4<false>(static_cast<P *>(t.param), i, n, p);  // the next forward pass reads it
+  if (PB && t.master) store4<true>(t.master, i, n, p);
   if (Eight) {
     if (i + 4 > n)  // values past the tensor's end: no part of the block's peaks
 #pragma unroll
@@ -235,8 +259,8 @@ __device__ __forceinline__ void update(const gdn_adamw_tensor_t &t, int64_t i, c
     store4(static_cast<uint8_t *>(t.v), i, n, encode_r(r, up));
     if (threadIdx.x % 64 == 0) t.v_scale[block] = scale;
   } else {
-    store4(static_cast<float *>(t.m), i, n, m);
-    store4(static_cast<float *>(t.v), i, n, v);
+    store4<true>(static_cast<float *>(t.m), i, n, m);
+    store4<true>(static_cast<float *>(t.v), i, n, v);
   }
 }
 
@@ -244,12 +268,12 @@ template <bool PB, bool GB, bool Eight>
 __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch p) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const float factor = p.args.factor ? *p.args.factor : 1.0f;
-  if (!(fabsf(factor) < __builtin_inff())) return;
   Rates k = p.rates;
   if (p.args.step_at || p.args.lr_at) {
     const int64_t step = p.args.step_at ? *p.args.step_at : p.args.step;
     k = rates_of(p.args, step < 1 ? 1 : step, p.args.lr_at ? (double)*p.args.lr_at : p.args.lr);
   }
+  constexpr int kChunk = chunk_of(Eight);
   const int64_t first = lane < p.count ? p.start[lane] : INT64_MAX;
   for (int64_t chunk = blockIdx.x; chunk < p.start[p.count]; chunk += gridDim.x) {
     // the tensor: the last one that starts at or before the chunk (empty ones start where the
@@ -280,7 +304,7 @@ __global__ __launch_bounds__(256) void adamw_values_kernel(const uint8_t *codes,
     } else {
       decode_m(w, s, v);
     }
-    store4(out, i, n, v);
+    store4<true>(out, i, n, v);
   }
 }
 
@@ -327,7 +351,7 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(const NormLaunch p) {
 #pragma unroll
     for (int j = 0; j < kNormChunk / 1024; ++j) {
       float g[4];
-      load4(static_cast<const G *>(t.grad), base + 1024 * j, t.numel, g);
+      load4<false>(static_cast<const G *>(t.grad), base + 1024 * j, t.numel, g);  // for the step
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum = fma((double)g[e], (double)g[e], sum);
     }
@@ -380,12 +404,13 @@ hipError_t launch_adamw(const AdamwArgs &a, const gdn_adamw_tensor_t *tensors, i
   p.args = a;
   p.rates = rates_of(a, a.step, a.lr);
   hipError_t e = hipSuccess;
-  each_launch(tensors, count, kTensors, kChunk, [&](int64_t i, int64_t j, int64_t chunks) {
+  const int64_t chunk = chunk_of(a.eight);
+  each_launch(tensors, count, kTensors, chunk, [&](int64_t i, int64_t j, int64_t chunks) {
     p.count = (int32_t)(j - i);
     p.start[0] = 0;
     for (int64_t t = i; t < j; ++t) {
       p.tensor[t - i] = tensors[t];
-      p.start[t - i + 1] = p.start[t - i] + chunks_of(tensors[t].numel, kChunk);
+      p.start[t - i + 1] = p.start[t - i] + chunks_of(tensors[t].numel, chunk);
     }
     void *kargs[] = {&p};
     if (e == hipSuccess)

@@ -681,6 +681,11 @@ Launch tile_launch(const LinearF8Args &a) {
           BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
 }
 
+// The kernel of a size. Up to 256 workgroups of 16 columns (one for each compute unit) the rows
+// kernels: 16 x 4096 x 4096 takes 8 us in them and 11.5 in 64 of 64 x 64 tiles, 128 x 2048 x 4096
+// 9.7, 64 x 1024 x 16384 18.6 against 34.6. Past that, the tile whose rounds over the units take
+// the least: the microseconds of a round of 4096 k are below, to bf16 and to binary32 (measured
+// from 128 x 4096 x 4096 to 65536 x 4096 x 4096).
 template <bool E>
 Launch pick(const LinearF8Args &a) {
   auto count = [&](int rows, int cols) {
@@ -689,11 +694,12 @@ Launch pick(const LinearF8Args &a) {
   if (a.m <= 16 && count(16, 16) <= 256) return rows_launch<16, E>(a);
   if (count(32, 16) <= 256) return rows_launch<32, E>(a);
   if (count(64, 16) <= 256) return rows_launch<64, E>(a);
-  auto time = [&](int rows, int cols, double round) {
-    return (double)((count(rows, cols) + 255) / 256) * round;
+  auto time = [&](int rows, int cols, double bf16, double f32) {
+    return (double)((count(rows, cols) + 255) / 256) * (a.y_bf16 ? bf16 : f32);
   };
-  const double t[5] = {time(256, 256, 62.0), time(128, 256, 37.0), time(128, 128, 23.0),
-                       time(64, 128, 17.0), time(64, 64, 10.5)};
+  const double t[5] = {time(256, 256, 60.0, 102.0), time(128, 256, 36.5, 55.0),
+                       time(128, 128, 20.5, 28.0), time(64, 128, 15.0, 19.5),
+                       time(64, 64, 10.5, 13.0)};
   switch (std::min_element(t, t + 5) - t) {
     case 0: return tile_launch<256, 256, 64, 128, E>(a);
     case 1: return tile_launch<128, 256, 64, 64, E>(a);

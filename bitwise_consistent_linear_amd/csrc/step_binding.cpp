@@ -181,24 +181,33 @@ class List {
   // The i-th, a dense tensor on GPU `dev` (-1: any) of `numel` values (-1: any).
   const at::Tensor &at(int64_t i, Types types, int64_t numel, int dev) const {
     PyObject *o = PySequence_Fast_GET_ITEM(list_, i);
-    const std::string name = std::string(name_) + "[" + std::to_string(i) + "]";
     if (THPVariable_Check(o)) {
       const at::Tensor &t = THPVariable_Unpack(o);
       if (t.is_cuda() && (dev < 0 || t.get_device() == dev) && admits(types, t.scalar_type()) &&
-          t.is_contiguous()) {
-        if (numel < 0 || t.numel() == numel) return t;
-        value_error(name + " must have " + std::to_string(numel) + " values, got " +
-                    std::to_string(t.numel()));
-      }
-      if (t.is_cuda() && dev >= 0 && t.get_device() != dev)
-        value_error(name + " is on GPU " + std::to_string(t.get_device()) + ", expected GPU " +
-                    std::to_string(dev));
-      refuse(g_need, Py_BuildValue("(OsOi)", o, name.c_str(), g_dtypes[types], (int)t.dim()));
+          t.is_contiguous() && (numel < 0 || t.numel() == numel))
+        return t;
     }
-    refuse(g_need, Py_BuildValue("(OsOi)", o, name.c_str(), g_dtypes[types], 1));
+    refuse_at(i, types, numel, dev);
   }
 
  private:
+  [[noreturn]] void refuse_at(int64_t i, Types types, int64_t numel, int dev) const {
+    PyObject *o = PySequence_Fast_GET_ITEM(list_, i);
+    const std::string name = std::string(name_) + "[" + std::to_string(i) + "]";
+    int dim = 1;
+    if (THPVariable_Check(o)) {
+      const at::Tensor &t = THPVariable_Unpack(o);
+      dim = (int)t.dim();
+      if (t.is_cuda() && dev >= 0 && t.get_device() != dev)
+        value_error(name + " is on GPU " + std::to_string(t.get_device()) + ", expected GPU " +
+                    std::to_string(dev));
+      if (t.is_cuda() && admits(types, t.scalar_type()) && t.is_contiguous())
+        value_error(name + " must have " + std::to_string(numel) + " values, got " +
+                    std::to_string(t.numel()));
+    }
+    refuse(g_need, Py_BuildValue("(OsOi)", o, name.c_str(), g_dtypes[types], dim));
+  }
+
   PyObject *list_;
   const char *name_;
   int64_t size_;
