@@ -18,11 +18,11 @@ namespace {
 using u64 = unsigned long long;
 
 constexpr int kThreads = 1024;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;       // a weight above 0 lies in the first 46.5 * 32
 constexpr int kList = 4096;       // candidates that LDS holds
 constexpr int kFew = 64;          // candidates that one wave ranks
 constexpr float kBinsPerNat = 64.0f;
-constexpr int kTable = 32;        // steps of an octave in the table of powers of two
+constexpr int kTable = 64;        // steps of an octave in the table of powers of two
 
 __device__ __forceinline__ uint32_t key_of(float x) {  // a NaN above all, -0 as 0
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -89,10 +89,10 @@ struct Request {
 
 // exp((x - top) / T) in units of 2^-shift, to the nearest: y = (x - top) log2(e) / T in steps of
 // the table is split into a whole number and a rest of at most half a step, whose power of two
-// six terms of its series give to 2^-48. The table holds 2^(shift + i / kTable); a whole power
-// is added to its exponent. Its 32 values lie in 64 banks of LDS, so that lanes never wait for
-// each other (with 1024 of them and four terms a random read took 23 cycles a wave and bounded
-// as much as these six do, and took a step of the kernel to fill).
+// five terms of its series give to 2^-44. The table holds 2^(shift + i / kTable); a whole power
+// is added to its exponent, and the last product rounds to whole numbers by the sum with 2^52. Its
+// 64 values lie two to a bank of LDS, so that lanes hardly wait for each other (1024 values and
+// four terms: a random read takes 23 cycles a wave, as long as the terms that it saves).
 struct Weigh {
   const double *power;
   double top, rate, least;  // rate: kTable log2(e) / T
@@ -109,22 +109,21 @@ struct Weigh {
   __device__ __forceinline__ double whole(double d) const { return fma(d, rate, kMagic); }
   __device__ __forceinline__ static int low(double t) { return (int)(uint32_t)(u64)__double_as_longlong(t); }
   __device__ __forceinline__ double below(float x) const { return fmax((double)x - top, least); }
-  // the steps from x up to the top, 0 .. 64 kTable
-  __device__ __forceinline__ int steps(float x) const { return -low(whole(below(x))); }
+  // Two steps to a bin, from the top down: bin b of y in [-2 b - 1.5, -2 b + 0.5].
+  static constexpr int kPerOctave = kTable / 2;
+  __device__ __forceinline__ int bin_at(double d) const { return -low(whole(d)) >> 1; }
+  __device__ __forceinline__ int bin(float x) const { return bin_at(below(x)); }
   // the weight added to kNone
   __device__ __forceinline__ u64 raw(float x) const { return raw_at(below(x)); }
   __device__ __forceinline__ u64 raw_at(double d) const {
     constexpr double c = 0.69314718055994530942 / kTable;
     const double t = whole(d), r = fma(d, rate, kMagic - t);
     const int n = low(t);
-    const double q =
-        r * fma(r, fma(r, fma(r, fma(r, c * c * c * c * c / 120, c * c * c * c / 24), c * c * c / 6),
-                       c * c / 2),
-                c);
-    const u64 bits = (u64)__double_as_longlong(power[n & (kTable - 1)]) +
-                     ((u64)(uint32_t)((n & ~(kTable - 1)) << 15) << 32);
-    const double w = __longlong_as_double((long long)bits);
-    return (u64)__double_as_longlong(fma(w, q, w) + 0x1p52);
+    const double q = fma(r, fma(r, fma(r, fma(r, c * c * c * c / 24, c * c * c / 6), c * c / 2), c), 1.0);
+    const u64 bits = (u64)__double_as_longlong(power[n & (kTable - 1)]);
+    const uint32_t high = (uint32_t)(bits >> 32) + ((uint32_t)(n & ~(kTable - 1)) << 14);
+    const double w = __longlong_as_double((long long)((u64)high << 32 | (uint32_t)bits));
+    return (u64)__double_as_longlong(fma(w, q, 0x1p52));
   }
   __device__ __forceinline__ u64 operator()(float x) const { return raw(x) - kNone; }
   __device__ __forceinline__ u64 operator()(u64 place) const {
@@ -295,13 +294,14 @@ __device__ __forceinline__ u64 wave_mass(const SampleArgs &p, int64_t off, int64
 }
 
 // Where the running sum of value(x, id) over ids [from, to) passes `rest` (less than the whole):
-// a part of the range for each wave, then of that part, down to 512 ids. The place, in every
-// thread; `sums` holds a value for each wave.
+// a part of the range for each wave, then of that part, down to eight ids a lane. from is a
+// multiple of 512, to too or the row's end. The place, in every thread; `sums` holds a value for
+// each wave.
 template <bool B16, int Waves, class F>
 __device__ __forceinline__ u64 descend(const SampleArgs &p, int64_t off, int64_t from, int64_t to,
                                        u64 rest, u64 *sums, u64 *found, F value) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  while (to - from > 512) {
+  while (to - from > Waves * 512) {
     const int64_t each = ((to - from + Waves - 1) / Waves + 511) / 512 * 512;
     const int64_t begin = from + wave * each;
     const u64 sum = wave_mass<B16>(p, off, begin, begin + each < to ? begin + each : to, value);
@@ -313,18 +313,31 @@ __device__ __forceinline__ u64 descend(const SampleArgs &p, int64_t off, int64_t
     from += w * each;
     to = from + each < to ? from + each : to;
   }
-  if (wave == 0) {
-    u64 sum = 0;
-    over<B16>(p, off, from, to, lane, 64, [&](float x, int64_t i) { sum += value(x, i); });
-    const u64 run = wave_run(sum);
-    u64 before = run - sum;
-    if (before <= rest && rest < run)
-      over<B16>(p, off, from, to, lane, 64, [&](float x, int64_t i) {
-        const u64 w = value(x, i);
-        if (before <= rest && rest < before + w) *found = place_of(x, i);
-        before += w;
-      });
+  const int64_t col = from + 512 * wave + 8 * lane;
+  u64 w[8] = {}, sum = 0;
+  float x[8] = {};
+  if (col < to) {
+    Vec8<B16> v;
+    load_row(v, p.logits, off, col, p.vocab);
+    settle_row(v, col, p.vocab, -__builtin_inff());  // of weight 0
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = v.get(e);
+      sum += w[e] = value(x[e], col + e);
+    }
   }
+  const u64 run = wave_run(sum);
+  __syncthreads();
+  if (lane == 63) sums[wave] = run;
+  __syncthreads();
+  u64 before = run - sum;
+  for (int i = 0; i < wave; ++i) before += sums[i];
+  if (before <= rest && rest < before + sum)  // one thread's
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (before <= rest && rest < before + w[e]) *found = place_of(x[e], col + e);
+      before += w[e];
+    }
   __syncthreads();
   return *found;
 }
@@ -803,7 +816,7 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
       if (only >= 0)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (weigh.steps(get(e)) != only) mine &= ~(1u << e);
+          if (weigh.bin(get(e)) != only) mine &= ~(1u << e);
       const uint32_t run = wave_run((uint32_t)__popc(mine));
       uint32_t room = 0;
       if (tid % 64 == 63 && run > 0) room = atomicAdd(&s.n, run);
@@ -841,7 +854,7 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
       const int64_t id = whole_runs + tid;
       const float x = B16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[off + id])
                           : static_cast<const float *>(p.logits)[off + id];
-      if (x >= lowest && x <= highest && (only < 0 || weigh.steps(x) == only)) {
+      if (x >= lowest && x <= highest && (only < 0 || weigh.bin(x) == only)) {
         const uint32_t to = atomicAdd(&s.n, 1u);
         if (to < kList) s.list[to] = place_of(x, id);
       }
@@ -877,18 +890,19 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
       const double d = weigh.below(x);
       const u64 wx = weigh.raw_at(d) - Weigh::kNone;
       w.sum += wx;
-      if (wx > tail) atomicAdd(&s.mass[-Weigh::low(weigh.whole(d))], wx);
+      if (wx > tail) atomicAdd(&s.mass[weigh.bin_at(d)], wx);
     });
     goal = share(r.top_p, block_range(s, w).sum);
     find_bin(s, goal, [&](int b) { return s.mass[b]; });
     const int bin = (int)s.bin;
     const u64 before = s.before;
     __syncthreads();
-    // how many logits that is, at most: none of a bin lies a whole step below it
+    // how many logits that is, at most: none of a bin weighs as little as the next one's first
     w = kNothing;
     for (int b = tid; b <= bin; b += kThreads) {
-      // 2^(shift - (b + 1) / kTable)
-      const double next = ldexp(s.power[-(b + 1) & (kTable - 1)], -(b + kTable) / kTable);
+      // 2^(shift - (b + 1) / kPerOctave)
+      const double next = ldexp(s.power[-2 * (b + 1) & (kTable - 1)],
+                                -(b + Weigh::kPerOctave) / Weigh::kPerOctave);
       w.sum += (u64)fmin((double)s.mass[b] / fmax(next - 1.0, 1.0) + 1.0, 0x1p40);
     }
     whole = block_range(s, w).sum <= kList;
@@ -898,7 +912,7 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
       const double x = (double)top - steps / weigh.rate;
       return (float)(x + slack * fabs(x));
     };
-    const float lowest = edge(bin + 0.75, -0x1p-20), highest = edge(bin - 0.75, 0x1p-20);
+    const float lowest = edge(2 * bin + 1.75, -0x1p-20), highest = edge(2 * bin - 0.75, 0x1p-20);
     gather(lowest, whole ? infinite : highest, whole ? -1 : bin);
     between(key_of(lowest), whole ? top_key : key_of(highest));
     if (n > kList) {
