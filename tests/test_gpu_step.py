@@ -419,6 +419,42 @@ def test_sample_parameters_of_each_row():
         same(one[1], logp[i:i + 1])
 
 
+@pytest.mark.parametrize("rows,vocab", [(1, 32768), (2, 50021), (9, 40007), (70, 33001), (128, 33000)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_sample_few_long_rows(rows, vocab, dtype):
+    """Rows that several workgroups share: every kind of row among them, with every filter."""
+    g = gen(rows * vocab)
+    x = rand(g, rows, vocab, scale=2.0)
+    inf = float("inf")
+    kinds = [lambda r: r.mul_(0.001), lambda r: r.fill_(3.0), lambda r: r[1:].fill_(-inf),
+             lambda r: r[:vocab - 2].fill_(-inf), lambda r: r.fill_(-inf), lambda r: r[5:6].fill_(inf),
+             lambda r: r[vocab - 1:].fill_(float("nan")), lambda r: r.mul_(1e4),
+             lambda r: r.fill_(torch.finfo(F32 if dtype == "f32" else BF16).min),
+             lambda r: r[::2].fill_(7.5)]
+    for i in range(rows):
+        if i % 12 < len(kinds) and rows > 1:
+            kinds[(i + rows) % 12 % len(kinds)](x[i])
+    x = x.to(DTYPES[dtype])
+    u = torch.rand(rows, generator=g)
+    some = FILTERS if rows < 10 else [dict(top_k=50, top_p=0.95), dict(top_p=0.9)]
+    for f in some + [dict(top_k=vocab // 2, top_p=0.5), dict(top_p=1 - 2.0 ** -24),
+                     dict(temperature=0.01, top_k=300), dict(temperature=1e-9, top_p=0.9)]:
+        check_draw(x, u, **f, label=f)
+
+
+def test_sample_parameters_of_few_long_rows():
+    g = gen(66)
+    n, vocab = 12, 34567
+    x = rand(g, n, vocab, scale=2.0, dtype=BF16)
+    u = torch.rand(n, generator=g)
+    t = torch.tensor([1.0, 0.5, 0.0, float("nan"), 1e30, -1.0, 1e-30, 2.0, 1.0, 1.0, 0.9, 0.8])
+    k = torch.tensor([0, 5, 5, 5, 5, 5, 5, -3, 20000, 2 ** 31 - 1, 0, 0], dtype=torch.int32)
+    p = torch.tensor([1.0, 0.9, 0.5, 0.5, 0.5, 0.5, 0.5, float("nan"), -1.0, 0.3, 0.999, 1.0])
+    least = torch.tensor([0.0, 0.1, 0.1, 0.1, 0.1, 0.1, 0.1, float("nan"), -2.0, 0.01, 0.0, 0.2])
+    check_draw(x, u, t, k, p, least)
+    check_draw(x, u, t, 0, p, least)
+
+
 def test_sample_rows_do_not_depend_on_the_batch():
     """Batches of other sizes, and so of other schedules."""
     g = gen(57)
@@ -866,7 +902,7 @@ def test_workspaces_may_hold_anything():
         logits, u = torch.zeros(2, 150000, device=DEV), torch.rand(2, generator=g).to(DEV)
         logits[:, ::3] = 1.0
         room = torch.full((max(size, 1),), fill, dtype=torch.uint8, device=DEV)
-        for f in (dict(), dict(top_p=0.5)):
+        for f in (dict(), dict(top_p=0.5), dict(top_k=9), dict(top_k=60000)):
             a = api.sample_tokens(logits, u, workspace=room if size else None, **f)
             for s, t in zip(a, api.sample_tokens(logits, u, **f)):
                 same(s, t)
