@@ -1026,7 +1026,8 @@ def linear_f8_fwd(xq, x_scale, wq, w_scale, *, out_dtype=None, y=None, stream=No
     """gdn_linear_f8_fwd: Y = X W^T of the values that 8-bit operands stand for, summed in
     binary32 in an order that the sizes do not change. xq [M, Kp] float8_e4m3fn or float8_e5m2,
     wq [N, Kp] float8_e4m3fn, with their scales, as quantize_f8 returns them. Returns y [M, N] in
-    out_dtype (float32 by default, or bfloat16)."""
+    out_dtype: float32 by default (products exact but for values below 2^-126), or bfloat16
+    (twice as fast, 1.5e-5 off before its own rounding)."""
     if stream is not None:
         return _elsewhere(stream, linear_f8_fwd, xq, x_scale, wq, w_scale, out_dtype=out_dtype,
                           y=y)
@@ -1118,7 +1119,7 @@ def adamw_step(params, grads, m, v, step, *, m_scale=None, v_scale=None, master=
     ceil(numel / ADAMW_BLOCK) values (all zeros at the start); master: float32 weights behind
     bfloat16 params. step (1 for the first) is a number or an int64 tensor [1], lr a number or
     a float32 tensor [1]; grad_scale a float32 tensor [1] that gradients are multiplied by, such
-    as grad_norm's factor: one that is not finite skips the step."""
+    as grad_norm's factor: one that is not finite skips the step. No two tensors may share memory."""
     if stream is not None:
         return _elsewhere(stream, adamw_step, params, grads, m, v, step, m_scale=m_scale,
                           v_scale=v_scale, master=master, lr=lr, betas=betas, eps=eps,

@@ -15,8 +15,8 @@
 // product of 2^3 is kept and one of 2^2 lost; eight places on all is kept), and the sums of eight
 // in binary32. Random operands come out 1.5e-5 off in the 2-norm, a hundredth of what rounding Y
 // to bf16 does (1.7e-3), so Y in bf16 takes them. Y in binary32 takes the bf16 instruction, half
-// as fast: an 8-bit value with its scale is exact in bf16, products are exact and their sums
-// binary32's (1e-7 off).
+// as fast: an 8-bit value with its scale is exact in bf16 (from 2^-126 up; below, bf16 has multiples
+// of 2^-133), products are exact and their sums binary32's (1e-7 off).
 
 #include <algorithm>
 
@@ -269,7 +269,7 @@ __device__ __forceinline__ void load_words_to_lds(const void *from, uint32_t to)
 // Few rows: W's bytes are what counts. A workgroup takes 16 columns of Y, up to MR rows, and all
 // of k in one chain by one wave for each 32 rows, as every kernel here; what it can spread is the
 // loading, so four waves keep LDS full of the chunks of 512 k that follow (112 KB of them for 16
-// rows: 16 x 4096 x 4096 NNN us against 14.2 by one wave that loads into registers).
+// rows: 16 x 4096 x 4096 8.0 us against 14.2 by one wave that loads into registers).
 //
 // A row's 32 chunks of 16 bytes lie at c ^ (row % 16): the 16 lanes of an operand read that are
 // served together have rows of 16 different remainders, so they meet no bank twice.

@@ -396,6 +396,12 @@ GDN_EXPORT gdn_status_t gdn_adamw_step(const gdn_adamw_shape_t *shape,
         gdn::any_misaligned({t.m, t.v}, eight ? 1 : 4) ||
         gdn::any_misaligned({t.m_scale, t.v_scale, t.master}, 4))
       return gdn::no(GDN_E_SHAPE, fn, "a buffer is not aligned to its element");
+    const void *const one[7] = {t.param, t.grad, t.m, t.v, t.master, eight ? t.m_scale : nullptr,
+                                eight ? t.v_scale : nullptr};
+    for (int j = 1; j < 7; ++j)
+      for (int l = 0; l < j; ++l)
+        if (one[j] && one[j] == one[l])
+          return gdn::no(GDN_E_SHAPE, fn, "two buffers of a tensor are the same");
   }
   if (!gdn::aligned(factor, 4) || !gdn::aligned(step_at, 8) || !gdn::aligned(lr_at, 4))
     return gdn::no(GDN_E_SHAPE, fn, "factor, step_at and lr_at must be aligned to their element");

@@ -5,6 +5,7 @@
 #include "gdn_step.h"
 #include "torch_binding.hpp"
 
+#include <algorithm>
 #include <vector>
 
 namespace {
@@ -288,6 +289,13 @@ PyObject *adamw_step(PyObject *const *a) {
     if (pt != kBf16) value_error("master needs bfloat16 params");
     more(a[7], "master", &gdn_adamw_tensor_t::master, 1);
   }
+  // a tensor in the list twice would be updated by two workgroups at once
+  std::vector<const void *> at;
+  for (const gdn_adamw_tensor_t &t : list)
+    if (t.numel > 0) at.push_back(t.param);
+  std::sort(at.begin(), at.end());
+  if (std::adjacent_find(at.begin(), at.end()) != at.end())
+    value_error("params has a tensor twice");
   gdn_adamw_shape_t shape = {pt == kBf16 ? GDN_DTYPE_BF16 : GDN_DTYPE_F32,
                              gt == kBf16 ? GDN_DTYPE_BF16 : GDN_DTYPE_F32,
                              eight ? GDN_STATE_8BIT : GDN_STATE_F32, 0, 0.0, number(a[9]),

@@ -56,7 +56,8 @@ const char *gdn_step_last_error(void);
  * its exponent + 127 in a byte (torch's float8_e8m0fnu). The scales lie as the product reads
  * them, four blocks of a row side by side:
  *   scale [ceil(c_pad / 512)][r rounded up to 4][4]: that of row i, block b at [b / 4][i][b % 4]
- * Bytes of rows past the last and blocks past the last hold 127 (a scale of 1).
+ * Bytes of rows past the last and blocks past the last hold 127 (a scale of 1). 255, which no
+ * block gets, stands for no scale: products with one are unspecified.
  *
  * With a = max |x| of a block, its scale is 2^e for the least whole e >= -127 with
  * a <= 1.75 * 2^emax * 2^e, the format's largest value (448 for E4M3, 57344 for E5M2); a block
@@ -75,8 +76,11 @@ gdn_status_t gdn_quantize_f8(const void *x, int64_t rows, int64_t k, int64_t x_s
                              uint8_t *qt, uint8_t *scale_t, void *stream);
 
 /* Y [m, n] = the sum over k of x[m, k] w[n, k], of the values that xq and wq stand for:
- * products of a block of 128 and their sum by one matrix instruction, the blocks' sums added
- * in binary32 in ascending order, the same for every m and n; rounded to y_dtype once.
+ * added up in binary32 by one chain of matrix instructions over ascending k, the same for every
+ * m and n, and rounded to y_dtype once. To F32 the values are taken in bf16, which holds them all but those
+ * below 2^-126 (rounded to multiples of 2^-133), products are exact and 16 k are added at a time.
+ * To BF16 64 k are, and of eight neighbouring k each product is cut off 13 bits below the power of
+ * two of the largest: 1.5e-5 in the 2-norm for random operands, where rounding Y is 1.7e-3.
  *   xq [m, k_pad] in x_format with x_scale; wq [n, k_pad] in E4M3 with w_scale
  *   y [m, n]  : F32 or BF16
  * Admitted: 0 <= m, n < 2^31; k_pad a multiple of GDN_F8_BLOCK in [0, 2^20]. m == 0 or n == 0
@@ -228,9 +232,12 @@ typedef struct gdn_adamw_shape {
  *                                   change between replays of a captured call; NULL for the
  *                                   shape's. A step below 1 counts as 1
  * A NaN or an infinity in a block's gradients without such a factor spreads to the values of its
- * block in 8-bit states. Admitted: 0 <= count <= 2^20, each numel < 2^40; no two buffers may
- * overlap, but grad may be NULL where numel is 0. master needs param_dtype BF16.
- * Errors: GDN_E_NULL, GDN_E_SHAPE (sizes, values, alignment), GDN_E_UNSUPPORTED (dtype, state),
+ * block in 8-bit states. Admitted: 0 <= count <= 2^20, each numel < 2^40; no two buffers of the
+ * list may overlap (a param that stands in it twice would be updated by two workgroups at once;
+ * equal pointers of one tensor are refused), but grad may be NULL where numel is 0. master needs
+ * param_dtype BF16.
+ * Errors: GDN_E_NULL, GDN_E_SHAPE (sizes, values, alignment, one buffer for two), GDN_E_UNSUPPORTED
+ * (dtype, state),
  * GDN_E_DEVICE. */
 gdn_status_t gdn_adamw_step(const gdn_adamw_shape_t *shape, const gdn_adamw_tensor_t *tensors,
                             int64_t count, const float *factor, const int64_t *step_at,

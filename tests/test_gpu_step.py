@@ -192,6 +192,29 @@ def cut(scale, rows):
     return out.view(torch.float8_e8m0fnu)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("m", [5, 70, 600])
+def test_product_of_values_next_to_nothing(m, fmt):
+    """Blocks whose largest value is near 2^-116. A product to binary32 takes its values in bf16,
+    whose least number is 2^-133: 2^-134 is a tie and becomes 0, powers of two above are held.
+    Sums of powers of two 21 bits apart at most are exact."""
+    g = gen(33)
+    k, n = 384, 520
+    x = torch.exp2(torch.randint(-131, -115, (m, k), generator=g).float())
+    x[torch.rand(m, k, generator=g) < 0.2] = 0.0
+    x[1, :] = 2.0 ** -134
+    w = torch.exp2(torch.randint(100, 103, (n, k), generator=g).float())
+    xq, xs = api.quantize_f8(x.to(DEV), fmt=fmt)
+    wq, ws = api.quantize_f8(w.to(DEV))
+    held_x, held_w = (R.values(*held(q, s)) for q, s in ((xq, xs), (wq, ws)))
+    in_bf16 = held_x.clone()
+    in_bf16[1] = 0.0
+    same(api.linear_f8_fwd(xq, xs, wq, ws), (in_bf16 @ held_w.t()).float())
+    y = api.linear_f8_fwd(xq, xs, wq, ws, out_dtype=BF16).cpu().double()
+    want, off = bounds(xq, xs, wq, ws, BF16)
+    assert bool(((y - want).abs() <= off).all())
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_product_of_far_scales(dtype):
     """Scales at both ends, products that stay in binary32's range: whole numbers, so exact."""
@@ -955,5 +978,10 @@ def test_binding_refuses():
         api.adamw_step(one, [f(300)], [f(300)], [f(300)], 1, master=[f(300)])
     with pytest.raises(api.GdnError, match="step"):
         api.adamw_step(one, [f(300)], [f(300)], [f(300)], 0)
+    with pytest.raises(ValueError, match="params has a tensor twice"):
+        api.adamw_step(one * 2, [f(300), f(300)], [f(300), f(300)], [f(300), f(300)], 1)
+    with pytest.raises(api.GdnError, match="two buffers of a tensor are the same"):
+        m = f(300)
+        api.adamw_step(one, [f(300)], [m], [m], 1)
     with pytest.raises(ValueError, match="scale must be"):
         api.adamw_state_values(torch.zeros(300, dtype=torch.uint8, device=DEV), f(1))

@@ -237,6 +237,16 @@ def test_refused_before_launch(L, name, call, status):
                     L.gdn_step_last_error().decode())
 
 
+def test_a_tensor_needs_buffers_of_its_own(L):
+    names = ("param", "grad", "m", "v", "m_scale", "v_scale", "master")
+    apart = {n: FAKE + 4096 * i for i, n in enumerate(names)}
+    for a in names:
+        for b in names:
+            if a < b:
+                assert aw(L, tensors(**dict(apart, **{a: apart[b]})), param_dtype=BF16) == SHAPE
+                assert L.gdn_step_last_error().endswith(b"two buffers of a tensor are the same")
+
+
 def test_empty_sizes_launch_nothing(L):
     assert qf(L, rows=0, x=None) == OK
     assert lf(L, m=0) == OK and lf(L, n=0, y=None) == OK
