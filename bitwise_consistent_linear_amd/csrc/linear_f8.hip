@@ -427,6 +427,11 @@ __device__ __forceinline__ void load_word_to_lds(const void *base, uint32_t offs
       :: "s"(to), "v"(offset), "s"(base) : "memory", "m0");
 }
 
+// Products of one launch, by tiles: blockIdx.y says which.
+struct Products {
+  LinearF8Args of[2];
+};
+
 // A BN x BM tile of Y by (BN / TN) x (BM / TM) waves, each TN columns by TM rows.
 //
 // K goes through LDS in stages of 64 bytes of every row of the tile, four buffers of one stage
@@ -448,7 +453,8 @@ __device__ __forceinline__ int chunk_key(int r) { return r >> chunk_key_shift & 
 
 template <int BM, int BN, int TM, int TN, bool E5M2, bool YB, bool Through>
 __global__ __launch_bounds__(BM / TM *(BN / TN) * 64) __attribute__((amdgpu_waves_per_eu(2)))
-void linear_f8_tile_kernel(const LinearF8Args p) {
+void linear_f8_tile_kernel(const Products list) {
+  const LinearF8Args &p = list.of[blockIdx.y];
   constexpr int kWaves = BM / TM * (BN / TN), MI = TM / 32, NJ = TN / 32;
   constexpr int kLoads = (BM + BN) / 16 / kWaves;  // 1 KiB (16 rows) each, per wave and stage
   constexpr int kStage = (BM + BN) * 64, kWords = (BM + BN) / 64;
@@ -681,26 +687,25 @@ Launch tile_launch(const LinearF8Args &a) {
           BM / TM * (BN / TN) * 64, (total + 7) / 8 * 8};
 }
 
-// The kernel of a size. Up to 256 workgroups of 16 columns (one for each compute unit) the rows
-// kernels: 16 x 4096 x 4096 takes 8 us in them and 11.5 in 64 of 64 x 64 tiles, 128 x 2048 x 4096
-// 9.7, 64 x 1024 x 16384 18.6 against 34.6. Past that, the tile whose rounds over the units take
-// the least: the microseconds of a round of 4096 k are below, to bf16 and to binary32 (measured
-// from 128 x 4096 x 4096 to 65536 x 4096 x 4096).
+int64_t count_of(const LinearF8Args &a, int rows, int cols) {
+  return (a.m + rows - 1) / rows * ((a.n + cols - 1) / cols);
+}
+
+// Tiles, with the microseconds that a round of them over the 256 compute units takes for 4096 k,
+// to bf16 and to binary32 (measured from 128 x 4096 x 4096 to 65536 x 4096 x 4096).
+struct Tile {
+  int rows, cols;
+  double bf16, f32;
+  double time(int64_t count, const LinearF8Args &a) const {
+    return (double)((count + 255) / 256) * (a.y_bf16 ? bf16 : f32) * a.k / 4096;
+  }
+};
+constexpr Tile kTiles[5] = {{256, 256, 60.0, 102.0}, {128, 256, 36.5, 55.0}, {128, 128, 20.5, 28.0},
+                            {64, 128, 15.0, 19.5}, {64, 64, 10.5, 13.0}};
+
 template <bool E>
-Launch pick(const LinearF8Args &a) {
-  auto count = [&](int rows, int cols) {
-    return (a.m + rows - 1) / rows * ((a.n + cols - 1) / cols);
-  };
-  if (a.m <= 16 && count(16, 16) <= 256) return rows_launch<16, E>(a);
-  if (count(32, 16) <= 256) return rows_launch<32, E>(a);
-  if (count(64, 16) <= 256) return rows_launch<64, E>(a);
-  auto time = [&](int rows, int cols, double bf16, double f32) {
-    return (double)((count(rows, cols) + 255) / 256) * (a.y_bf16 ? bf16 : f32);
-  };
-  const double t[5] = {time(256, 256, 60.0, 102.0), time(128, 256, 36.5, 55.0),
-                       time(128, 128, 20.5, 28.0), time(64, 128, 15.0, 19.5),
-                       time(64, 64, 10.5, 13.0)};
-  switch (std::min_element(t, t + 5) - t) {
+Launch tile_launch(int tile, const LinearF8Args &a) {
+  switch (tile) {
     case 0: return tile_launch<256, 256, 64, 128, E>(a);
     case 1: return tile_launch<128, 256, 64, 64, E>(a);
     case 2: return tile_launch<128, 128, 64, 64, E>(a);
@@ -708,8 +713,70 @@ Launch pick(const LinearF8Args &a) {
     default: return tile_launch<64, 64, 32, 32, E>(a);
   }
 }
+Launch tile_launch(int tile, const LinearF8Args &a) {
+  return a.e5m2 ? tile_launch<true>(tile, a) : tile_launch<false>(tile, a);
+}
 
-Launch pick(const LinearF8Args &a) { return a.e5m2 ? pick<true>(a) : pick<false>(a); }
+// The tile whose rounds take the least, and their time.
+int best_tile(const LinearF8Args &a, double &least) {
+  int best = 0;
+  for (int t = 0; t < 5; ++t) {
+    const double time = kTiles[t].time(count_of(a, kTiles[t].rows, kTiles[t].cols), a);
+    if (t == 0 || time < least) {
+      best = t;
+      least = time;
+    }
+  }
+  return best;
+}
+
+// Up to 256 workgroups of 16 columns (one for each compute unit) the rows kernels: 16 x 4096 x 4096
+// takes 8 us in them and 11.5 in 64 of 64 x 64 tiles, 128 x 2048 x 4096 9.7, 64 x 1024 x 16384 18.6
+// against 34.6.
+int few_rows(const LinearF8Args &a) {
+  if (a.m <= 16 && count_of(a, 16, 16) <= 256) return 16;
+  if (count_of(a, 32, 16) <= 256) return 32;
+  return count_of(a, 64, 16) <= 256 ? 64 : 0;
+}
+
+template <bool E>
+Launch rows_launch(int rows, const LinearF8Args &a) {
+  switch (rows) {
+    case 16: return rows_launch<16, E>(a);
+    case 32: return rows_launch<32, E>(a);
+    default: return rows_launch<64, E>(a);
+  }
+}
+
+// The kernel of a size.
+Launch pick(const LinearF8Args &a) {
+  const int rows = few_rows(a);
+  if (rows) return a.e5m2 ? rows_launch<true>(rows, a) : rows_launch<false>(rows, a);
+  double time;
+  return tile_launch(best_tile(a, time), a);
+}
+
+// The tile that takes two products in one launch in less time than they take one after the other,
+// or -1: small ones leave compute units idle. Both gradients of 1024 x 1024 x 1024 to binary32 take
+// 16.9 us so and 20.9 in two launches, of 2048 x 2048 x 2048 45.3 and 50.3, to bf16 31.5 and 36.0.
+int shared_tile(const LinearF8Args &a, const LinearF8Args &b) {
+  if (a.k == 0 || b.k == 0 || few_rows(a) || few_rows(b)) return -1;
+  double ta, tb;
+  best_tile(a, ta);
+  best_tile(b, tb);
+  double least = ta + tb;
+  int best = -1;
+  for (int t = 0; t < 5; ++t) {
+    const Tile &tile = kTiles[t];
+    const int64_t count = count_of(a, tile.rows, tile.cols) + count_of(b, tile.rows, tile.cols);
+    const double time = tile.time(count, a.k > b.k ? a : b);
+    if (time < least && tile_launch(t, a).fn == tile_launch(t, b).fn) {
+      best = t;
+      least = time;
+    }
+  }
+  return best;
+}
 
 }  // namespace
 
@@ -750,10 +817,23 @@ hipError_t launch_linear_f8(const LinearF8Args &a, hipStream_t stream) {
                            dim3((unsigned)std::min<int64_t>((halves + 255) / 256, 1 << 16)),
                            dim3(256), kargs, 0, stream);
   }
-  LinearF8Args args = a;
-  void *kargs[] = {&args};
+  Products list = {{a, a}};  // the rows kernels take the first alone
+  void *kargs[] = {&list};
   const Launch go = pick(a);
   return hipLaunchKernel(go.fn, dim3((unsigned)go.grid), dim3(go.threads), kargs, 0, stream);
+}
+
+hipError_t launch_linear_f8(const LinearF8Args &a, const LinearF8Args &b, hipStream_t stream) {
+  const int tile = shared_tile(a, b);
+  if (tile < 0) {
+    const hipError_t e = launch_linear_f8(a, stream);
+    return e == hipSuccess ? launch_linear_f8(b, stream) : e;
+  }
+  Products list = {{a, b}};
+  void *kargs[] = {&list};
+  const Launch one = tile_launch(tile, a), two = tile_launch(tile, b);  // grids in multiples of 8
+  return hipLaunchKernel(one.fn, dim3((unsigned)std::max(one.grid, two.grid), 2), dim3(one.threads),
+                         kargs, 0, stream);
 }
 
 }  // namespace gdn

@@ -277,9 +277,12 @@ GDN_EXPORT gdn_status_t gdn_linear_f8_bwd(const gdn_linear_f8_shape_t *shape, co
       q.scale_t = at + room.scale_t;
     }
     e = gdn::launch_quantize_f8(q, s);
-    if (e == hipSuccess && dx) e = gdn::launch_linear_f8(ax, s);
+    if (e == hipSuccess)
+      e = !dw ? gdn::launch_linear_f8(ax, s)
+              : !dx ? gdn::launch_linear_f8(aw, s) : gdn::launch_linear_f8(ax, aw, s);
+  } else if (dw) {
+    e = gdn::launch_linear_f8(aw, s);
   }
-  if (e == hipSuccess && dw) e = gdn::launch_linear_f8(aw, s);
   return gdn::launched(fn, e);
 }
 

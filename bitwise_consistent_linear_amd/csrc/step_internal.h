@@ -23,6 +23,8 @@ struct LinearF8Args {
 };
 int64_t linear_f8_threads(const LinearF8Args &args);  // of the launch; at most 2^32 - 1 fit one
 hipError_t launch_linear_f8(const LinearF8Args &args, hipStream_t stream);
+// Two products that have nothing to do with each other, in one launch where that pays.
+hipError_t launch_linear_f8(const LinearF8Args &a, const LinearF8Args &b, hipStream_t stream);
 
 // Rows of the scales' layout, and bytes of a matrix's scales.
 inline int64_t f8_pad(int64_t c) { return (c + GDN_F8_BLOCK - 1) / GDN_F8_BLOCK * GDN_F8_BLOCK; }
