@@ -1069,7 +1069,7 @@ def linear_f8_bwd(dy, wtq=None, wt_scale=None, xtq=None, xt_scale=None, *, fmt="
 
 
 def sample_tokens_workspace_bytes(shape: GdnSampleShape) -> int:
-    """gdn_sample_tokens_workspace: device bytes the draw needs (often 0)."""
+    """gdn_sample_tokens_workspace: device bytes the draw needs (0 for up to 4096 logits a row)."""
     n = ctypes.c_size_t(0)
     _step_check(step_lib().gdn_sample_tokens_workspace(ctypes.byref(shape), ctypes.byref(n)))
     return n.value
