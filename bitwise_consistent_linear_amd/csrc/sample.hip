@@ -372,7 +372,8 @@ __device__ __forceinline__ void answer(const SampleArgs &p, int64_t row, u64 pla
 // ------------------------------------------------------------------------- without cuts
 
 // No top-k or top-p: two readings of the row, its maximum and the sum of its weights, and a few
-// of ever smaller parts of it. A row a workgroup at a time.
+// of ever smaller parts of it. A row a workgroup at a time. 512 x 131072 bf16 take 71 us: the maximum
+// 25 (134 MB, memory), the sums the rest (22 instructions a logit, most of them in 64 bits).
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_plain_kernel(const SampleArgs p) {
   constexpr int kWaves = kThreads / 64;
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(kThreads) void sample_plain_kernel(const SampleArgs
 }
 
 // Few rows: a row in slices, a workgroup each, in three launches: the slices' maxima, their sums,
-// and the draw within one slice.
+// and the draw within one slice. 8 x 131072 f32: 3.0 + 4.4 + 5.1 us, mostly each launch's own 2 to 3.
 constexpr int kSliceThreads = 256, kSliceWaves = kSliceThreads / 64;
 
 struct Slices {
@@ -673,7 +674,8 @@ constexpr u64 kNothingLeft = ~0ull, kAllLeft = 0;
 
 // Rows whose cuts keep more than LDS holds, or whose candidates did not fit there: bins of the
 // logits and then of places narrow every cut down in the row itself. A kernel of its own, as its
-// registers would make the common path's spill.
+// registers would make the common path's spill (151 us for both in one against 51 + 23: 256 x 65536
+// bf16, top-p 0.95, draws behind a known cut).
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs p) {
   constexpr int kWaves = kThreads / 64;
@@ -772,6 +774,10 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs 
 //           end is known to a bin, and the logits down to there are gathered;
 // then each cut and the draw itself is a search among these, by the same steps. A run too long
 // for LDS is cut among its last bin's logits and drawn from by sample_left_kernel.
+// 256 x 65536 bf16, top-p 0.95: 51 us, of them the maximum 6, the bins 16 to 20, gathering 11, a
+// search 4 to 6; 100 x 50021 f32 with every filter 27. Both are bound by the instructions of one
+// workgroup. Slices of a row over several, in five launches, make few rows of top-p faster (1 x
+// 131072 62 us against 86) and a top-k slower (32 against 24): not taken.
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p) {
   __shared__ Shared s;

@@ -45,7 +45,7 @@ struct SampleArgs {
   float *logp;
   void *workspace;
 };
-int64_t sample_workspace_bytes(const SampleArgs &args);  // 0: a row is one workgroup's
+int64_t sample_workspace_bytes(const SampleArgs &args);
 hipError_t launch_sample(const SampleArgs &args, hipStream_t stream);
 
 struct AdamwArgs {
