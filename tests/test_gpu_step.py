@@ -290,6 +290,20 @@ def test_backward(m, n, k, dtype, fmt):
         same(a, b)
 
 
+@pytest.mark.parametrize("m,n,k", [(1024, 1024, 1024), (1021, 2049, 1111), (2048, 2048, 2048),
+                                   (300, 700, 5000), (2000, 130, 900), (17, 2100, 4100)])
+@pytest.mark.parametrize("dtypes", [(F32, F32), (BF16, BF16), (BF16, F32)], ids=str)
+def test_backward_together_and_alone(m, n, k, dtypes):
+    """Both gradients of one call, in one launch or two, are those of two calls."""
+    g = gen(m + n + k)
+    dy = rand(g, m, n).to(DEV)
+    w = api.quantize_f8(rand(g, n, k, scale=k ** -0.5).to(DEV), layout="columns")
+    x = api.quantize_f8(rand(g, m, k).to(DEV), layout="columns")
+    dx, dw = api.linear_f8_bwd(dy, *w, *x, fmt="e5m2", dx_dtype=dtypes[0], dw_dtype=dtypes[1])
+    same(dx, api.linear_f8_bwd(dy, *w, fmt="e5m2", dx_dtype=dtypes[0])[0])
+    same(dw, api.linear_f8_bwd(dy, None, None, *x, fmt="e5m2", dw_dtype=dtypes[1])[1])
+
+
 def test_backward_against_differences():
     """sum(dy Y) along steps of X and W that 8 bits hold, with dy that they hold: linear, so a
     difference is the gradient times the step, up to binary32's sums."""
