@@ -535,7 +535,7 @@ struct Shared {
   uint32_t count[kBins];
   u64 list[kList];
   u64 few[kFew], few_value[kFew], few_sum[kFew];
-  u64 wave[4][kThreads / 64], wave2[kThreads / 64];
+  u64 wave[4][kThreads / 64], wave2[kThreads / 64], part[kThreads / 64];
   u64 found, before;
   uint32_t n, bin;
 };
@@ -668,36 +668,43 @@ __device__ __forceinline__ u64 share(double top_p, u64 all) {  // where top_p cu
   return t > 0 ? t : 1;
 }
 
-// What sample_cut_kernel leaves of a row to sample_left_kernel, in two words of the workspace:
-// nothing, the draw behind a cut (its place, above 0, and the largest key), or all of it.
-constexpr u64 kNothingLeft = ~0ull, kAllLeft = 0;
+// The weight of a logit that a cut (a place, 0 for none) and min_p keep, else 0.
+struct Kept {
+  const Weigh &weigh;
+  float last;
+  int64_t last_id;
+  u64 floor;
+  __device__ __forceinline__ Kept(const Weigh &weigh, u64 cut, u64 floor, int64_t vocab)
+      : weigh(weigh), last(cut ? logit_of((uint32_t)(cut >> 32)) : -__builtin_inff()),
+        last_id(cut ? (int64_t)(uint32_t)~(uint32_t)cut : vocab), floor(floor) {}
+  __device__ __forceinline__ u64 operator()(float x, int64_t id) const {
+    const u64 w = x > last || (x == last && id <= last_id) ? weigh(x) : 0;
+    return w >= floor ? w : 0;
+  }
+};
 
 // Rows whose cuts keep more than LDS holds, or whose candidates did not fit there: bins of the
 // logits and then of places narrow every cut down in the row itself. A kernel of its own, as its
-// registers would make the common path's spill (151 us for both in one against 51 + 23: 256 x 65536
-// bf16, top-p 0.95, draws behind a known cut).
+// registers would make the common path's spill. The workspace holds a word for each row: whether
+// it is one.
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs p) {
   constexpr int kWaves = kThreads / 64;
   __shared__ Shared s;
   const int tid = threadIdx.x;
   const int64_t row = p.first + blockIdx.x, off = row * p.stride, V = p.vocab;
-  const u64 state = static_cast<const u64 *>(p.workspace)[2 * row];
-  if (state == kNothingLeft) return;
+  if (!static_cast<const uint32_t *>(p.workspace)[row]) return;
   Weigh::fill(s.power, p.shift, tid, kThreads);
-  uint32_t top_key = (uint32_t) static_cast<const u64 *>(p.workspace)[2 * row + 1];
-  if (state == kAllLeft) {
-    const uint32_t mine = thread_top<B16>(p, off, 0, V, tid, kThreads);
-    top_key = (uint32_t)block_range(s, {0, 0, mine, mine}).hi;
-  }
+  const uint32_t mine = thread_top<B16>(p, off, 0, V, tid, kThreads);
+  const uint32_t top_key = (uint32_t)block_range(s, {0, 0, mine, mine}).hi;
   const Request r(p, row);
   const float top = logit_of(top_key);
   const Weigh weigh(s.power, top, r.T);
   const float bins = (float)fmin((double)kBinsPerNat / r.T, 0x1p100);
   auto bin_of = [&](float x) { return (int)fminf((top - x) * bins, (float)(kBins - 1)); };
   const u64 floor = r.floor(p.shift);
-  u64 cut = state;  // the least place that is kept
-  for (int by_mass = 0; by_mass < 2 && state == kAllLeft; ++by_mass) {
+  u64 cut = 0;  // the least place that is kept
+  for (int by_mass = 0; by_mass < 2; ++by_mass) {
     if (by_mass ? !(r.top_p < 1.0) : !(r.k > 0 && r.k < V)) continue;
     auto value = [&](u64 c) { return by_mass ? weigh(c) : 1ull; };
     clear_bins(s);
@@ -742,12 +749,7 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs 
                   },
                   [](u64 c) { return c; }, value);
   }
-  const float last = cut ? logit_of((uint32_t)(cut >> 32)) : -__builtin_inff();
-  const int64_t last_id = cut ? (int64_t)(uint32_t)~(uint32_t)cut : V;
-  auto value = [&](float x, int64_t i) {
-    const u64 w = x > last || (x == last && i <= last_id) ? weigh(x) : 0;
-    return w >= floor ? w : 0;
-  };
+  const Kept value(weigh, cut, floor, V);
   const int wave = tid / 64;
   const int64_t each = ((V + kWaves - 1) / kWaves + 511) / 512 * 512, begin = wave * each;
   u64 sum = 0;
@@ -772,21 +774,24 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs 
 //   top-k : the k-th largest of the threads' maxima has k logits at or above it;
 //   top-p alone : the weights are added up in bins of a 32nd of an octave, so that the run's
 //           end is known to a bin, and the logits down to there are gathered;
-// then each cut and the draw itself is a search among these, by the same steps. A run too long
-// for LDS is cut among its last bin's logits and drawn from by sample_left_kernel.
-// 256 x 65536 bf16, top-p 0.95: 51 us, of them the maximum 6, the bins 16 to 20, gathering 11, a
-// search 4 to 6; 100 x 50021 f32 with every filter 27. Both are bound by the instructions of one
-// workgroup. Slices of a row over several, in five launches, make few rows of top-p faster (1 x
-// 131072 62 us against 86) and a top-k slower (32 against 24): not taken.
+// then each cut and the draw itself is a search among these, by the same steps. Of a run too long
+// for LDS the last bin's logits alone are gathered, and on the way the weights of the bins before
+// it added up for sixteen parts of the row: the cut is found in the bin, and the token in one part.
+// 256 x 65536 bf16, top-p 0.95: 58 us, of them the maximum 6, the bins 16 to 20, gathering the bin
+// and the sums 18, a search 4 to 6 (with the sums in a launch of their own behind the cut 51 + 23);
+// 100 x 50021 f32 with every filter 27. Both are bound by the instructions of one workgroup. Slices
+// of a row over several, in five launches, make a top-k slower (1 x 131072 32 us against 24) and a
+// top-p faster (62 against 76): not taken.
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p) {
   __shared__ Shared s;
   const int tid = threadIdx.x;
   const int64_t row = p.first + blockIdx.x, off = row * p.stride, V = p.vocab;
-  u64 *const left = static_cast<u64 *>(p.workspace);
+  constexpr int kWaves = kThreads / 64;
+  uint32_t *const left = static_cast<uint32_t *>(p.workspace);  // of a row: sample_left_kernel's
   const bool small = V <= kList;  // the list takes the row
   Weigh::fill(s.power, p.shift, tid, kThreads);
-  if (tid == 0 && !small) left[2 * row] = kNothingLeft;
+  if (tid == 0 && !small) left[row] = 0;
   const Request r(p, row);
   const uint32_t mine = thread_top<B16>(p, off, 0, V, tid, kThreads);
   const Range tops = block_range(s, {0, 0, mine, mine});
@@ -805,24 +810,20 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
   const u64 floor = r.floor(p.shift);
   const bool by_count = r.k > 0 && r.k < V, by_mass = r.top_p < 1.0;
   if (!small && (by_count ? r.k > kThreads : !by_mass)) {
-    if (tid == 0) left[2 * row] = kAllLeft;
+    if (tid == 0) left[row] = 1;
     return;
   }
   u64 cut = 0;     // the least place that is kept
   u64 goal = 0;    // where top_p cuts the sum off, if that is known
   uint32_t n = 0;  // places in the list
   bool whole = true;  // the list holds all that is kept
-  // Logits from `lowest` to `highest` into the list, of them those of bin `only` where that is one;
-  // a wave takes room for its eight times 64 at once.
-  auto gather = [&](float lowest, float highest, int only) {
+  const uint32_t each = ((uint32_t)V + kWaves * 512 - 1) / (kWaves * 512) * 512;  // of a wave
+  // Logits from `lowest` on into the list; a wave takes room for its eight times 64 at once.
+  auto gather = [&](float lowest) {
     if (tid == 0) s.n = 0;
     __syncthreads();
     auto append = [&](uint32_t mine, auto get, int64_t id) {  // bit e: get(e) may go in
       if (__ballot(mine != 0) == 0) return;
-      if (only >= 0)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (weigh.bin(get(e)) != only) mine &= ~(1u << e);
       const uint32_t run = wave_run((uint32_t)__popc(mine));
       uint32_t room = 0;
       if (tid % 64 == 63 && run > 0) room = atomicAdd(&s.n, run);
@@ -851,7 +852,7 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
         uint32_t mine = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          mine |= v[u].get(e) >= lowest && v[u].get(e) <= highest ? 1u << e : 0u;
+          mine |= v[u].get(e) >= lowest ? 1u << e : 0u;
         append(i < runs ? mine : 0, [&](int e) { return v[u].get(e); }, 8 * (int64_t)i);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -860,7 +861,7 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
       const int64_t id = whole_runs + tid;
       const float x = B16 ? bf16_lo(static_cast<const uint16_t *>(p.logits)[off + id])
                           : static_cast<const float *>(p.logits)[off + id];
-      if (x >= lowest && x <= highest && (only < 0 || weigh.bin(x) == only)) {
+      if (x >= lowest) {
         const uint32_t to = atomicAdd(&s.n, 1u);
         if (to < kList) s.list[to] = place_of(x, id);
       }
@@ -869,7 +870,31 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
     n = s.n;
     __syncthreads();
   };
-  const float infinite = __builtin_inff();
+  // Those of bin `only` into the list, and the weights of the bins before it added up for a part
+  // of the row each.
+  auto gather_bin = [&](int only) {
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    const int lane = tid % 64, wave = tid / 64;
+    const int64_t begin = (int64_t)wave * each;
+    u64 sum = 0;
+    over<B16, 2>(p, off, begin, begin + each < V ? begin + each : V, lane, 64,
+                 [&](float x, int64_t id) {
+                   const double d = weigh.below(x);
+                   const int bin = weigh.bin_at(d);
+                   const u64 w = weigh.raw_at(d) - Weigh::kNone;
+                   sum += bin < only && w >= floor ? w : 0;
+                   if (bin == only) {
+                     const uint32_t to = atomicAdd(&s.n, 1u);
+                     if (to < kList) s.list[to] = place_of(x, id);
+                   }
+                 });
+    sum = wave_sum(sum);
+    if (lane == 0) s.part[wave] = sum;
+    __syncthreads();
+    n = s.n;
+    __syncthreads();
+  };
   enum { kTops, kCount, kMass, kDraw };
   int stage = kCount;
   // what the next search goes over, where that is known without a look at the list
@@ -878,7 +903,7 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
     known = {0, n, (u64)lo << 32, (u64)hi << 32 | 0xFFFFFFFFu};
   };
   if (small) {
-    gather(-infinite, infinite, -1);
+    gather(-__builtin_inff());
   } else if (by_count) {
     stage = kTops;
     s.list[tid] = (u64)mine << 32 | (uint32_t)~tid;
@@ -919,22 +944,19 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
       return (float)(x + slack * fabs(x));
     };
     const float lowest = edge(2 * bin + 1.75, -0x1p-20), highest = edge(2 * bin - 0.75, 0x1p-20);
-    gather(lowest, whole ? infinite : highest, whole ? -1 : bin);
+    if (whole)
+      gather(lowest);
+    else
+      gather_bin(bin);
     between(key_of(lowest), whole ? top_key : key_of(highest));
     if (n > kList) {
-      if (tid == 0) left[2 * row] = kAllLeft;
+      if (tid == 0) left[row] = 1;
       return;
     }
   }
   for (; stage <= kDraw; ++stage) {
     if ((stage == kCount && !by_count) || (stage == kMass && !by_mass)) continue;
-    if (stage == kDraw && !whole) {
-      if (tid == 0) {
-        left[2 * row] = cut;
-        left[2 * row + 1] = top_key;
-      }
-      return;
-    }
+    if (stage == kDraw && !whole) break;
     const u64 least = stage == kDraw ? floor : 0;
     auto value = [&](u64 c) {
       if (stage < kMass) return 1ull;
@@ -961,16 +983,33 @@ __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p
     if (stage == kDraw) {
       if (tid == 0) answer(p, row, found, top, r.T, w.sum);
     } else if (stage == kTops) {
-      gather(logit_of((uint32_t)(found >> 32)), infinite, -1);
+      gather(logit_of((uint32_t)(found >> 32)));
       between((uint32_t)(found >> 32), top_key);
       if (n > kList) {
-        if (tid == 0) left[2 * row] = kAllLeft;
+        if (tid == 0) left[row] = 1;
         return;
       }
     } else {
       cut = found;
     }
   }
+  if (whole) return;
+  // the bin's part of the cut among the parts of the row, then the draw from one of them
+  for (uint32_t i = tid; i < n; i += kThreads) {
+    const u64 c = s.list[i], w = weigh(c);
+    if (c >= cut && w >= floor)
+      atomicAdd(&s.part[~(uint32_t)c / each], w);
+  }
+  __syncthreads();
+  u64 all = 0;
+  for (int i = 0; i < kWaves; ++i) all += s.part[i];
+  u64 rest = r.point(all);
+  int w = 0;
+  while (w < kWaves - 1 && rest >= s.part[w]) rest -= s.part[w++];
+  const int64_t from = (int64_t)w * each;
+  const u64 place = descend<B16, kWaves>(p, off, from, from + each < V ? from + each : V, rest,
+                                         s.wave2, &s.found, Kept(weigh, cut, floor, V));
+  if (tid == 0) answer(p, row, place, top, r.T, all);
 }
 
 bool cuts(const SampleArgs &a) { return a.top_ks || a.top_k > 0 || a.top_ps || a.top_p < 1.0; }
@@ -993,7 +1032,7 @@ int64_t sample_workspace_bytes(const SampleArgs &a) {
   const Slices s = slices_of(a);
   const int64_t slices = s.count > 1 ? a.rows * s.count * 12 : 0;
   // what is left of each row; a row's own parameters, which the sizes do not show, may cut too
-  const int64_t left = a.vocab > kList ? a.rows * 16 : 0;
+  const int64_t left = a.vocab > kList ? a.rows * 4 : 0;
   return (std::max(slices, left) + 255) / 256 * 256;
 }
 
