@@ -1,5 +1,5 @@
-// Device helpers of the products whose tiles go through LDS: loads straight from memory into
-// LDS, the wait that goes with them, and stores of a tile's rows.
+// Helpers of the products whose tiles go through LDS: which workgroup takes which tile, loads
+// straight from memory into LDS, the wait that goes with them, and stores of a tile's rows.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,6 +9,22 @@
 namespace gdn {
 
 using i32x4 = int __attribute__((ext_vector_type(4)));
+
+// The tile of Y, counted in tiles, that a workgroup takes; rows below 0: none. Each XCD (workgroup
+// % 8) has a run of neighbours, in bands of 8 tiles of rows. The grid may be larger than the
+// product's own, as where two products share one.
+struct TilePlace {
+  int64_t row, col;
+};
+__host__ __device__ __forceinline__ TilePlace tile_place(int64_t workgroup, int64_t tiles_m,
+                                                         int64_t tiles_n) {
+  const int64_t total = tiles_m * tiles_n, per = (total + 7) / 8, turn = workgroup / 8;
+  const int64_t tile = workgroup % 8 * per + turn;
+  if (turn >= per || tile >= total) return {-1, 0};  // past its XCD's run: another one's tiles
+  const int64_t band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
+  const int64_t height = tiles_m - 8 * band < 8 ? tiles_m - 8 * band : 8;
+  return {8 * band + in_band % height, in_band / height};
+}
 
 // 16 bytes per lane from base + offset to LDS, lane after lane from `to` (uniform) on.
 __device__ __forceinline__ void load_to_lds(const void *base, uint32_t offset, uint32_t to) {

@@ -470,14 +470,9 @@ void linear_f8_tile_kernel(const Products list) {
   __shared__ __align__(128) uint8_t lds[4 * kStage];
   __shared__ __align__(128) uint32_t scales[2][BM + BN];
   const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  // tiles: each XCD (workgroup % 8) a run of neighbours, in bands of 8 tiles of rows
-  const int64_t tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
-  const int64_t total = tiles_m * tiles_n, per = (total + 7) / 8;
-  const int64_t tile = blockIdx.x % 8 * per + blockIdx.x / 8;
-  if (tile >= total) return;
-  const int64_t band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
-  const int64_t height = tiles_m - 8 * band < 8 ? tiles_m - 8 * band : 8;
-  const int64_t m0 = (8 * band + in_band % height) * BM, n0 = in_band / height * BN;
+  const TilePlace tile = tile_place(blockIdx.x, (p.m + BM - 1) / BM, (p.n + BN - 1) / BN);
+  if (tile.row < 0) return;
+  const int64_t m0 = tile.row * BM, n0 = tile.col * BN;
 
   // the wave's loads of a stage: a base in scalar registers and an offset per lane (below
   // 256 rows of 2^20 bytes); rows past the end repeat the last one
