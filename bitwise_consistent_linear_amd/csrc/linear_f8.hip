@@ -779,10 +779,19 @@ int shared_tile(const LinearF8Args &a, const LinearF8Args &b) {
   return best;
 }
 
+// Workgroups: by rows the kernel goes on from a grid's end, by columns a tile each.
+int64_t quantize_grid(const QuantizeF8Args &a) {
+  if (a.qt) return (a.rows + 127) / 128 * ((a.k + 127) / 128);
+  return std::min<int64_t>((f8_scale_rows(a.rows) * ((a.k + 511) / 512) + 3) / 4, 1 << 20);
+}
+
 }  // namespace
+
+int64_t quantize_f8_threads(const QuantizeF8Args &a) { return quantize_grid(a) * 256; }
 
 hipError_t launch_quantize_f8(const QuantizeF8Args &a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
+  const dim3 grid((unsigned)quantize_grid(a));
   QuantizeF8Args args = a;
   void *kargs[] = {&args};
   if (!a.qt) {
@@ -790,16 +799,13 @@ hipError_t launch_quantize_f8(const QuantizeF8Args &a, hipStream_t stream) {
                                         : (const void *)quantize_f8_rows_kernel<true, false>)
                               : (a.e5m2 ? (const void *)quantize_f8_rows_kernel<false, true>
                                         : (const void *)quantize_f8_rows_kernel<false, false>);
-    const int64_t need = (f8_scale_rows(a.rows) * ((a.k + 511) / 512) + 3) / 4;
-    return hipLaunchKernel(fn, dim3((unsigned)std::min<int64_t>(need, 1 << 20)), dim3(256), kargs,
-                           0, stream);
+    return hipLaunchKernel(fn, grid, dim3(256), kargs, 0, stream);
   }
   const void *fn = a.x_bf16 ? (a.e5m2 ? (const void *)quantize_f8_columns_kernel<true, true>
                                       : (const void *)quantize_f8_columns_kernel<true, false>)
                             : (a.e5m2 ? (const void *)quantize_f8_columns_kernel<false, true>
                                       : (const void *)quantize_f8_columns_kernel<false, false>);
-  const int64_t tiles = (a.rows + 127) / 128 * ((a.k + 127) / 128);  // at most 2^26
-  return hipLaunchKernel(fn, dim3((unsigned)tiles), dim3(256), kargs, 0, stream);
+  return hipLaunchKernel(fn, grid, dim3(256), kargs, 0, stream);
 }
 
 int64_t linear_f8_threads(const LinearF8Args &a) {

@@ -18,6 +18,7 @@ constexpr int64_t kMaxStride = int64_t(1) << 31;
 constexpr int64_t kMaxF8Width = int64_t(1) << 20;
 constexpr int64_t kMaxTensors = int64_t(1) << 20;
 constexpr int64_t kMaxValues = int64_t(1) << 40;
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;  // of a launch
 
 bool aligned(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 bool known_dtype(int32_t d) { return d == GDN_DTYPE_F32 || d == GDN_DTYPE_BF16; }
@@ -162,6 +163,8 @@ GDN_EXPORT gdn_status_t gdn_quantize_f8(const void *x, int64_t rows, int64_t k, 
   a.scale = scale;
   a.qt = qt;
   a.scale_t = scale_t;
+  if (gdn::quantize_f8_threads(a) > gdn::kMaxThreads)
+    return gdn::no(GDN_E_SHAPE, fn, "2^24 tiles of 128 x 128 values are too many for one launch");
   return gdn::launched(fn, gdn::launch_quantize_f8(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -195,7 +198,7 @@ GDN_EXPORT gdn_status_t gdn_linear_f8_fwd(int64_t m, int64_t n, int64_t k_pad, i
   a.wq = wq;
   a.w_scale = w_scale;
   a.y = y;
-  if (gdn::linear_f8_threads(a) > int64_t(0xFFFFFFFF))
+  if (gdn::linear_f8_threads(a) > gdn::kMaxThreads)
     return gdn::no(GDN_E_SHAPE, fn, "the tiles of m * n values are too many for one launch");
   return gdn::launched(fn, gdn::launch_linear_f8(a, static_cast<hipStream_t>(stream)));
 }
@@ -256,26 +259,28 @@ GDN_EXPORT gdn_status_t gdn_linear_f8_bwd(const gdn_linear_f8_shape_t *shape, co
   aw.wq = xtq;
   aw.w_scale = xt_scale;
   aw.y = dw;
-  if ((dx && gdn::linear_f8_threads(ax) > int64_t(0xFFFFFFFF)) ||
-      (dw && gdn::linear_f8_threads(aw) > int64_t(0xFFFFFFFF)))
+  gdn::QuantizeF8Args q{};
+  q.rows = m;
+  q.k = n;
+  q.x_stride = shape->dy_stride;
+  q.x_bf16 = shape->dy_dtype == GDN_DTYPE_BF16;
+  q.e5m2 = a.e5m2;
+  q.x = dy;
+  if (dx) {
+    q.q = at + room.q;
+    q.scale = at + room.scale;
+  }
+  if (dw) {
+    q.qt = at + room.qt;
+    q.scale_t = at + room.scale_t;
+  }
+  if (gdn::quantize_f8_threads(q) > gdn::kMaxThreads)
+    return gdn::no(GDN_E_SHAPE, fn, "dy's 2^24 tiles of 128 x 128 values are too many for one launch");
+  if ((dx && gdn::linear_f8_threads(ax) > gdn::kMaxThreads) ||
+      (dw && gdn::linear_f8_threads(aw) > gdn::kMaxThreads))
     return gdn::no(GDN_E_SHAPE, fn, "the tiles of a gradient are too many for one launch");
   hipError_t e = hipSuccess;
   if (m > 0) {
-    gdn::QuantizeF8Args q{};
-    q.rows = m;
-    q.k = n;
-    q.x_stride = shape->dy_stride;
-    q.x_bf16 = shape->dy_dtype == GDN_DTYPE_BF16;
-    q.e5m2 = a.e5m2;
-    q.x = dy;
-    if (dx) {
-      q.q = at + room.q;
-      q.scale = at + room.scale;
-    }
-    if (dw) {
-      q.qt = at + room.qt;
-      q.scale_t = at + room.scale_t;
-    }
     e = gdn::launch_quantize_f8(q, s);
     if (e == hipSuccess)
       e = !dw ? gdn::launch_linear_f8(ax, s)

@@ -13,6 +13,7 @@ struct QuantizeF8Args {
   const void *x;
   uint8_t *q, *scale, *qt, *scale_t;
 };
+int64_t quantize_f8_threads(const QuantizeF8Args &args);  // of the launch; at most 2^32 - 1 fit one
 hipError_t launch_quantize_f8(const QuantizeF8Args &args, hipStream_t stream);
 
 struct LinearF8Args {

@@ -68,7 +68,8 @@ const char *gdn_step_last_error(void);
 /* Quantises x [rows, k] (row stride x_stride, x_dtype F32 or BF16) by rows, into q [rows,
  * k_pad] with its scale, and by columns, its transpose into qt [k, rows_pad] with its scale_t;
  * either pair may be NULL, and both are made from one reading of x.
- * Admitted: 0 <= rows <= 2^31 - 1 and 1 <= k <= 2^20; with qt also rows <= 2^20.
+ * Admitted: 0 <= rows <= 2^31 - 1 and 1 <= k <= 2^20; with qt also rows <= 2^20 and fewer than
+ * 2^24 tiles of 128 x 128 values, which is what one launch holds.
  * Errors: GDN_E_NULL, GDN_E_SHAPE (sizes, stride, alignment), GDN_E_UNSUPPORTED (k, format,
  * dtype), GDN_E_DEVICE. rows == 0 does nothing. */
 gdn_status_t gdn_quantize_f8(const void *x, int64_t rows, int64_t k, int64_t x_stride,
@@ -110,7 +111,8 @@ gdn_status_t gdn_linear_f8_bwd_workspace(const gdn_linear_f8_shape_t *shape, siz
  * and W. dx with wtq and wt_scale, or dw with xtq and xt_scale, may be NULL, not both.
  *   workspace : device, 256-byte aligned, gdn_linear_f8_bwd_workspace() bytes; its contents on
  *               entry do not matter
- * m == 0 gives dw = 0. Errors as for the forward. */
+ * m == 0 gives dw = 0. Errors as for the forward; GDN_E_SHAPE also where dw is wanted of a dy of
+ * 2^24 tiles of 128 x 128 values and more. */
 gdn_status_t gdn_linear_f8_bwd(const gdn_linear_f8_shape_t *shape, const void *dy,
                                const uint8_t *wtq, const uint8_t *wt_scale, const uint8_t *xtq,
                                const uint8_t *xt_scale, void *dx, void *dw, void *workspace,
