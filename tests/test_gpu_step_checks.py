@@ -1,6 +1,6 @@
 """The operators around the policy head where a first set of tests did not look: rows past 2^31
-elements in every kernel that draws or quantises, all that a skipped update leaves alone, and calls
-made again that give the same bits."""
+elements in every kernel that draws or quantises, all that a skipped update leaves alone, products
+that cancel, and calls made again that give the same bits."""
 
 import pytest
 import torch
@@ -67,6 +67,26 @@ def test_adamw_leaves_everything_without_a_factor(eight, bad):
     for name, ts in d.items():
         for a, b in zip(ts, before[name]):
             same(a, b, name)
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 100, 512), (40, 300, 1024), (300, 1000, 512), (700, 2500, 640)])
+def test_products_that_cancel(m, n, k):
+    """Of every eight k two products are 2^16 and -2^16, the others whole numbers to 3. To binary32
+    every partial sum is a whole number below 2^24 (k / 8 pairs of 2^16, of which at most 16 k are
+    added at a time: under 2^18 and 3 k): exact. To bf16 every product is cut off 13 bits below 2^16
+    at most, so each eight is off by 8 2^-13 2^16, k additions round by 2^-24 of at most (k / 4)
+    2^16 + 3 k each, and Y by 2^-8 of itself."""
+    g = gen(m + k)
+    x = torch.randint(-3, 4, (m, k), generator=g).float()
+    w = torch.randint(0, 2, (n, k), generator=g).float() * 2 - 1
+    x[:, ::8], x[:, 5::8] = 256.0, -256.0
+    w[:, ::8] = w[:, 5::8] = 256.0
+    ops = (*api.quantize_f8(x.to(DEV)), *api.quantize_f8(w.to(DEV)))
+    want = x.double() @ w.double().t()
+    same(api.linear_f8_fwd(*ops), want.float())
+    off = k / 8 * 8 * 2.0 ** 3 + k * 2.0 ** -24 * (k / 4 * 2.0 ** 16 + 3 * k)
+    got = api.linear_f8_fwd(*ops, out_dtype=BF16).cpu().double()
+    assert bool(((got - want).abs() <= off + 2.0 ** -8 * (want.abs() + off)).all())
 
 
 @pytest.mark.parametrize("m,n,k", [(16, 4096, 4096), (1021, 2049, 1111), (1024, 1024, 1024),
