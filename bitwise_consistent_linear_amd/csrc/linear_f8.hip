@@ -759,7 +759,9 @@ Launch pick(const LinearF8Args &a) {
 
 // The tile that takes two products in one launch in less time than they take one after the other,
 // or -1: small ones leave compute units idle. Both gradients of 1024 x 1024 x 1024 to binary32 take
-// 16.9 us so and 20.9 in two launches, of 2048 x 2048 x 2048 45.3 and 50.3, to bf16 31.5 and 36.0.
+// 16.9 us so and 20.9 in two launches, of 2048 x 2048 x 2048 44 to 45 and 50.3, to bf16 31.5 and
+// 36.0. One launch has one kernel, so both need the same output type and rows of Y that are whole
+// 16-byte chunks or are not in both; a dx in bf16 beside a dw in binary32 takes two.
 int shared_tile(const LinearF8Args &a, const LinearF8Args &b) {
   if (a.k == 0 || b.k == 0 || few_rows(a) || few_rows(b)) return -1;
   double ta, tb;

@@ -780,8 +780,9 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(const SampleArgs 
 // 256 x 65536 bf16, top-p 0.95: 58 us, of them the maximum 6, the bins 16 to 20, gathering the bin
 // and the sums 18, a search 4 to 6 (with the sums in a launch of their own behind the cut 51 + 23);
 // 100 x 50021 f32 with every filter 27. Both are bound by the instructions of one workgroup. Slices
-// of a row over several, in five launches, make a top-k slower (1 x 131072 32 us against 24) and a
-// top-p faster (62 against 76): not taken.
+// of a row over several, in five launches, made a top-k slower (1 x 131072 32 us against 24) and a
+// top-p of few rows faster (62 against 86), measured while both forms drew behind a long top-p in a
+// launch of their own: not taken. 1 x 131072 top-p takes 61 here now, 8 rows 79.
 template <bool B16>
 __global__ __launch_bounds__(kThreads) void sample_cut_kernel(const SampleArgs p) {
   __shared__ Shared s;

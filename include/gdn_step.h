@@ -19,8 +19,8 @@
  * graph; a workspace belongs to one call at a time, a captured one included. Values that the
  * host cannot see (parameters of a row, random numbers) never lead to an access out of bounds.
  * Outputs must not alias inputs unless a call says so. Pointers must be aligned to their
- * element, the product's operands and scales to 16 bytes. gdn_step_last_error() returns the text of the
- * calling thread's last error. All functions are thread-safe.
+ * element, the product's operands and scales to 16 bytes. gdn_step_last_error() returns the text
+ * of the calling thread's last error. All functions are thread-safe.
  *
  * Row strides are in elements; rows are contiguous inside. An input's stride may be any
  * value in [0, 2^31] (0 repeats one row); outputs are dense.
@@ -78,10 +78,12 @@ gdn_status_t gdn_quantize_f8(const void *x, int64_t rows, int64_t k, int64_t x_s
 
 /* Y [m, n] = the sum over k of x[m, k] w[n, k], of the values that xq and wq stand for:
  * added up in binary32 by one chain of matrix instructions over ascending k, the same for every
- * m and n, and rounded to y_dtype once. To F32 the values are taken in bf16, which holds them all but those
- * below 2^-126 (rounded to multiples of 2^-133), products are exact and 16 k are added at a time.
- * To BF16 64 k are, and of eight neighbouring k each product is cut off 13 bits below the power of
- * two of the largest: 1.5e-5 in the 2-norm for random operands, where rounding Y is 1.7e-3.
+ * m and n, and rounded to y_dtype once. To F32 the values are taken in bf16, which holds them all
+ * but those below 2^-126 (rounded to multiples of 2^-133), products are exact and 16 k are added at
+ * a time. To BF16 64 k are, and of eight neighbouring k each product is cut off 13 bits below the
+ * power of two of the largest: 1.5e-5 in the 2-norm for random operands, where rounding Y is 1.7e-3.
+ * At most that is 2^-10 of the largest product of each eight k, added up over them: where the
+ * products of a row cancel it may exceed the rounding of Y, and Y to F32 is the remedy.
  *   xq [m, k_pad] in x_format with x_scale; wq [n, k_pad] in E4M3 with w_scale
  *   y [m, n]  : F32 or BF16
  * Admitted: 0 <= m, n < 2^31; k_pad a multiple of GDN_F8_BLOCK in [0, 2^20]. m == 0 or n == 0
@@ -109,8 +111,8 @@ gdn_status_t gdn_linear_f8_bwd_workspace(const gdn_linear_f8_shape_t *shape, siz
  *   dw [n, k] = dy^T x    over m, from xtq [k, m_pad]: X [m, k] quantised by columns
  * (both in E4M3, with their scales). The gradient passes straight through the rounding of X
  * and W. dx with wtq and wt_scale, or dw with xtq and xt_scale, may be NULL, not both.
- *   workspace : device, 256-byte aligned, gdn_linear_f8_bwd_workspace() bytes; its contents on
- *               entry do not matter
+ *   workspace : device, 256-byte aligned, gdn_linear_f8_bwd_workspace() bytes (dy quantised both
+ *               ways, also where one gradient is wanted); its contents on entry do not matter
  * m == 0 gives dw = 0. Errors as for the forward; GDN_E_SHAPE also where dw is wanted of a dy of
  * 2^24 tiles of 128 x 128 values and more. */
 gdn_status_t gdn_linear_f8_bwd(const gdn_linear_f8_shape_t *shape, const void *dy,
@@ -186,7 +188,8 @@ gdn_status_t gdn_grad_norm_workspace(const gdn_grad_tensor_t *tensors, int64_t c
  *   grad_dtype F32 or BF16; max_norm >= 0, infinity for a factor of 1
  *   workspace : device, 256-byte aligned, gdn_grad_norm_workspace() bytes; its contents on
  *               entry do not matter
- * Admitted: 0 <= count <= 2^20, each numel < 2^40. An empty list has norm 0. */
+ * Admitted: 0 <= count <= 2^20, each numel < 2^40. An empty list has norm 0. One call takes
+ * gradients of one type; a norm over both types has to have them in one first. */
 gdn_status_t gdn_grad_norm(const gdn_grad_tensor_t *tensors, int64_t count, int32_t grad_dtype,
                            double max_norm, float *norm, float *factor, void *workspace,
                            size_t workspace_bytes, void *stream);
